@@ -305,6 +305,141 @@ TQ_API tq_status tq_lloyd_max_fit_status(const void* workspace, void* stream);
  * [2, 256]. */
 TQ_API int64_t tq_lloyd_max_fit_workspace_size(int levels);
 
+/* ---- ragged packed caches ---------------------------------------------------
+ * The four calls below serve a batch whose sequences have unequal lengths that
+ * only the device knows (no counterpart on the pages: an addition of this
+ * library for speculative decoding and cache eviction). Batch row b of a cache
+ * holds its tokens at [left_pad[b], lens[b]); lens and left_pad are int32
+ * device arrays [B] read while the call runs, so one captured graph serves
+ * every step. Values outside [0, T] count as the nearer end of that range;
+ * lens == NULL stands for T everywhere, left_pad == NULL for 0. T, known to the
+ * host, bounds lens.
+ *
+ * One decode step with drafted tokens: encode the draft's keys and values into
+ * a small cache of their own (tq_encode_kv, tokens [0, N)); attend with
+ * tq_tree_attention; after the draft is verified, append the accepted path's
+ * tokens to each sequence with tq_cache_gather. To cut a cache: add up the
+ * weights that queries give to its tokens with tq_attention_weights, choose
+ * the tokens that stay with tq_evict_select, move them into a smaller cache
+ * with tq_cache_gather. */
+
+/* A packed cache by its five buffers [B, H, t_cap, X] (see above). A call that
+ * only reads the cache does not write through the pointers. */
+typedef struct {
+    void* k_codes;
+    void* k_scales;
+    void* k_zeros;
+    void* v_codes;
+    void* v_scales;
+    int64_t t_cap; /* token capacity */
+} tq_packed_cache;
+
+/* Attention of a tree of drafted tokens over a packed cache: the arithmetic of
+ * tq_decode_attention (bf16 K, rotated bf16 V, fp32 scores and weights, the
+ * inverse rotation of the output) with the keys of two caches.
+ *   q        [B, Hq, N, D] bf16, contiguous: one query row per head and node.
+ *   cache    the sequences: node rows attend to tokens [left_pad[b], lens[b]).
+ *   tree     the N nodes' own keys and values, tokens [0, N), in the bit
+ *            widths of `cache` (tree->t_cap >= N).
+ *   parents  int32 device array [B, N]: the node's parent, an earlier node
+ *            (parents[b][i] < i), or -1 for a node that follows the sequence
+ *            itself. Node i attends to itself and to its ancestors. A node
+ *            whose chain of parents does not end at -1 (any other negative
+ *            value, or a value >= i) is absent: its output rows are zero, its
+ *            lse is -inf and no present node attends to it. NULL: a chain, node i - 1
+ *            before node i.
+ *   scale    the softmax scale.
+ *   out      [B, Hq, N, D] of out_dtype, contiguous.
+ *   lse      NULL, or [B, Hq, N] fp32: the natural logarithm of the sum over
+ *            the row's keys of exp(scale * q . K[t]); -inf where the row has
+ *            no key (its output is zero).
+ *   Masked tokens (outside [left_pad, lens), other branches of the tree) never
+ *   reach a row, whatever their bytes decode to. A key that decodes to NaN or
+ *   a value group with an infinite or NaN scale makes NaN every row (all of
+ *   it, and its lse) that attends to it.
+ *   workspace  device scratch of at least tq_tree_attention_workspace_size
+ *            bytes (16-byte aligned), not in use by another call still
+ *            running; it needs no initialisation.
+ * Limits: D in {64, 128, 256, 512}; Hq a multiple of Hkv; 1 <= N <= 64; T at
+ * most cache->t_cap. B == 0 is a no-op. No buffer needs t_cap to be a multiple
+ * of 16. */
+#define TQ_TREE_MAX_NODES 64
+TQ_API tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int64_t N,
+                                   const tq_packed_cache* cache, int64_t Hkv, int64_t T, int64_t D,
+                                   const tq_packed_cache* tree, const int32_t* parents,
+                                   int k_bits, int k_signed, int v_bits,
+                                   const int32_t* lens, const int32_t* left_pad, float scale,
+                                   void* out, tq_dtype out_dtype, float* lse,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of scratch tq_tree_attention needs for these sizes on the current
+ * device. Negative: -TQ_ERR_HEAD_DIM or -TQ_ERR_INVALID_ARG. */
+TQ_API int64_t tq_tree_attention_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D);
+
+/* Sums of attention weights per cached token, by which a cache is cut. The
+ * observers of batch row b are its last n = n_path[b] tokens, in order: number
+ * i (0 <= i < n) is query row node = path[b][i] of every head, sits at token
+ * lens[b] - n + i, and attends to the tokens left_pad[b] <= t <= lens[b] - n + i:
+ *   weights_out[b][h][t] = weights_in[b][h][t] + sum over the heads hq of group
+ *     h and the observers that attend to t of
+ *     exp(scale * q[b][hq][node] . K[b][h][t] - lse[b][hq][node]).
+ * With lse from tq_tree_attention and after the accepted path was appended to
+ * the cache these are the softmax weights that its rows used.
+ *   q        [B, Hq, N, D] bf16; lse [B, Hq, N] fp32 (an observer whose lse
+ *            is -inf adds nothing).
+ *   k_codes, k_scales, k_zeros  the cache's key buffers [B, Hkv, t_cap, X].
+ *   path     int32 device array [B, P] of query rows; an entry outside [0, N)
+ *            adds nothing. NULL: the identity (then P <= N). n_path: int32
+ *            device array [B], values outside [0, P] count as the nearer end;
+ *            NULL: P everywhere.
+ *   weights_in, weights_out  fp32 [B, Hkv, w_cap], w_cap >= T; weights_in may
+ *            be NULL (zeros) or weights_out itself. Every element of
+ *            weights_out is written unless the two are the same array: then
+ *            only those that an observer attends to.
+ * The sum over a token's observers has a fixed order: equal calls give equal
+ * bits. Limits as for tq_tree_attention, but N and P are bounded only by
+ * (Hq / Hkv) * P <= 65536. */
+TQ_API tq_status tq_attention_weights(const void* q, const float* lse, int64_t B, int64_t Hq, int64_t N,
+                                      const void* k_codes, const void* k_scales, const void* k_zeros,
+                                      int64_t Hkv, int64_t T, int64_t D, int64_t t_cap, int k_bits, int k_signed,
+                                      const int32_t* lens, const int32_t* left_pad,
+                                      const int32_t* path, const int32_t* n_path, int64_t P, float scale,
+                                      const float* weights_in, float* weights_out, int64_t w_cap, void* stream);
+
+/* The tokens that stay when a cache is cut to `keep` tokens a head: per (batch
+ * row, head) with more than `keep` tokens, its last `recent` ones and those of
+ * the largest weights among the others (equal weights: the lowest token
+ * first; NaN ranks as -inf), else all of them.
+ *   weights  fp32 [B, H, w_cap], w_cap >= T.
+ *   index    int32 [B, H, keep]: the kept tokens in ascending order, then -1.
+ *   count    int32 [B]: min(keep, lens[b] - left_pad[b]), the kept tokens of
+ *            every head of row b.
+ * Limits: 0 <= recent <= keep, B * H < 2^31. keep == 0 writes count alone. */
+TQ_API tq_status tq_evict_select(const float* weights, int64_t B, int64_t H, int64_t T, int64_t w_cap,
+                                 const int32_t* lens, const int32_t* left_pad, int64_t keep, int64_t recent,
+                                 int32_t* index, int32_t* count, void* stream);
+
+/* Copies chosen tokens between two packed caches of the same B, H, D and bit
+ * widths, whole rows of each buffer: destination token dst_off[b] + j of every
+ * head receives source token index[b][j] (index_heads == 0, index [B, n]) or
+ * index[b][h][j] (index_heads == 1, index [B, H, n]), 0 <= j < count[b].
+ *   count    int32 device array [B], values outside [0, n] count as the nearer
+ *            end; NULL: n everywhere. dst_off: int32 device array [B], negative
+ *            values count as 0; NULL: 0.
+ *   dst_len  NULL, or int32 [B]: receives min(dst_off[b] + count[b],
+ *            dst->t_cap); it must not overlap dst_off or count.
+ *   src_weights, dst_weights  fp32 [B, H, the cache's t_cap] moved beside the
+ *            tokens; src_weights NULL with dst_weights given: zeros are
+ *            written. Both NULL: no weights.
+ * An index outside [0, src->t_cap) leaves its destination token as it was, as
+ * are all tokens from dst->t_cap on (dropped) and every token that is not a
+ * destination. Source and destination memory must not overlap. */
+TQ_API tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed_cache* dst,
+                                 int64_t B, int64_t H, int64_t D, int k_bits, int v_bits,
+                                 const int32_t* index, int64_t n, int index_heads,
+                                 const int32_t* count, const int32_t* dst_off, int32_t* dst_len,
+                                 const float* src_weights, float* dst_weights, void* stream);
+
 /* Device-side failures of the library's kernels on the current device (no
  * counterpart on the pages: failure detection of this library). Kernels that
  * wait on an asynchronous copy (the decode's bulk-copy path) bound the wait;

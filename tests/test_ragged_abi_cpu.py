@@ -1,0 +1,171 @@
+"""Host-side refusals of the calls on ragged packed caches: every call below is
+invalid by construction (or a no-op), so none reaches a kernel launch, and they
+run without a GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests import ragged_common as rc
+
+OK, INVALID, HEAD_DIM, BITS, ALIGN, DTYPE = range(6)
+P = 1 << 20  # an aligned address that is never read
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from turboquant_kv_cache_tq_gb300 import build
+
+    build.build()
+    import turboquant_kv_cache_tq_gb300 as tq
+
+    tq.lib()
+    return tq
+
+
+def _cache(tq, cap=64, **bad):
+    c = dict(k_codes=P, k_scales=P, k_zeros=P, v_codes=P, v_scales=P)
+    c.update(bad)
+    return tq.TQPackedCache(c["k_codes"], c["k_scales"], c["k_zeros"], c["v_codes"], c["v_scales"], cap)
+
+
+def _tree(tq, q=P, B=1, Hq=4, N=8, cache=None, Hkv=2, T=64, D=128, tree=None, parents=None, kb=8, ks=1, vb=3, lens=None,
+          pad=None, out=P, dtype=1, lse=None, ws=P, ws_bytes=1 << 40):
+    c = _cache(tq) if cache is None else cache
+    t = _cache(tq, 8) if tree is None else tree
+    return tq.lib().tq_tree_attention(q, B, Hq, N, ctypes.byref(c), Hkv, T, D, ctypes.byref(t), parents, kb, ks, vb, lens,
+                                      pad, ctypes.c_float(1.0), out, dtype, lse, ws, ws_bytes, None)
+
+
+def test_tree_refusals(tq):
+    assert _tree(tq, B=0) == OK
+    for kw in (dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(N=0), dict(N=65, tree=_cache(tq, 65)), dict(T=-1), dict(T=65),
+               dict(Hq=5), dict(q=0), dict(out=0), dict(ws=0), dict(ws_bytes=0), dict(tree=_cache(tq, 7)),
+               dict(cache=_cache(tq, v_codes=0)), dict(tree=_cache(tq, 8, k_zeros=0)), dict(B=1 << 32),
+               dict(B=1 << 20, Hq=1 << 12), dict(cache=_cache(tq, 1 << 40)), dict(ws_bytes=-1)):
+        assert _tree(tq, **kw) == INVALID, kw
+    for D in (0, 32, 96, 1024, -64):
+        assert _tree(tq, D=D) == HEAD_DIM
+    for kw in (dict(kb=3, ks=0), dict(kb=4, ks=1), dict(vb=6), dict(vb=1), dict(kb=0, ks=0)):
+        assert _tree(tq, **kw) == BITS, kw
+    assert _tree(tq, dtype=2) == DTYPE
+    for kw in (dict(q=P + 8), dict(out=P + 2), dict(ws=P + 4), dict(cache=_cache(tq, k_scales=P + 2)),
+               dict(tree=_cache(tq, 8, v_scales=P + 8)), dict(parents=P + 1), dict(lens=P + 2), dict(pad=P + 3),
+               dict(lse=P + 1)):
+        assert _tree(tq, **kw) == ALIGN, kw
+    assert tq.lib().tq_tree_attention(P, 1, 4, 8, None, 2, 64, 128, None, None, 8, 1, 3, None, None,
+                                      ctypes.c_float(1.0), P, 1, None, P, 1 << 40, None) == INVALID
+
+
+def test_tree_workspace_refusals(tq):
+    f = tq.lib().tq_tree_attention_workspace_size
+    for a in ((-1, 4, 2, 8, 128), (1, 0, 1, 8, 128), (1, 4, 0, 8, 128), (1, 4, 3, 8, 128), (1, 4, 2, 0, 128),
+              (1, 4, 2, 65, 128), (1 << 40, 4, 2, 8, 128)):
+        assert f(*a) == -INVALID, a
+    assert f(1, 4, 2, 8, 100) == -HEAD_DIM
+    with pytest.raises(tq.TQError):
+        tq.tq_tree_attention_workspace_size(1, 4, 3, 8, 128)
+
+
+def _weights(tq, q=P, lse=P, B=1, Hq=4, N=8, kc=P, ks_=P, kz=P, Hkv=2, T=64, D=128, cap=64, kb=8, ks=1, lens=None,
+             pad=None, path=None, n_path=None, Pn=8, w_in=None, w_out=P, w_cap=64):
+    return tq.lib().tq_attention_weights(q, lse, B, Hq, N, kc, ks_, kz, Hkv, T, D, cap, kb, ks, lens, pad, path, n_path,
+                                         Pn, ctypes.c_float(1.0), w_in, w_out, w_cap, None)
+
+
+def test_weights_refusals(tq):
+    assert _weights(tq, B=0) == OK
+    assert _weights(tq, T=0, w_cap=0) == OK
+    for kw in (dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(N=0), dict(T=-1), dict(T=65), dict(w_cap=63), dict(Hq=5),
+               dict(Pn=-1), dict(Pn=9), dict(path=P, Pn=32769), dict(q=0), dict(lse=0), dict(kc=0), dict(ks_=0),
+               dict(kz=0), dict(w_out=0), dict(B=1 << 33), dict(cap=1 << 40)):
+        assert _weights(tq, **kw) == INVALID, kw
+    for D in (0, 100, 1024):
+        assert _weights(tq, D=D) == HEAD_DIM
+    assert _weights(tq, kb=3, ks=0) == BITS and _weights(tq, kb=2, ks=1) == BITS
+    for kw in (dict(q=P + 8), dict(kc=P + 4), dict(ks_=P + 2), dict(kz=P + 8), dict(lse=P + 2), dict(lens=P + 1),
+               dict(pad=P + 2), dict(path=P + 3), dict(n_path=P + 1), dict(w_in=P + 2), dict(w_out=P + 1)):
+        assert _weights(tq, **kw) == ALIGN, kw
+
+
+def _select(tq, w=P, B=1, H=2, T=64, w_cap=64, lens=None, pad=None, keep=8, recent=2, index=P, count=P):
+    return tq.lib().tq_evict_select(w, B, H, T, w_cap, lens, pad, keep, recent, index, count, None)
+
+
+def test_select_refusals(tq):
+    assert _select(tq, B=0) == OK and _select(tq, H=0) == OK
+    for kw in (dict(B=-1), dict(H=-1), dict(T=-1), dict(w_cap=63), dict(keep=-1, recent=-1), dict(recent=-1),
+               dict(recent=9), dict(w=0), dict(index=0), dict(count=0), dict(keep=1 << 31), dict(B=1 << 31),
+               dict(B=1 << 16, H=1 << 16)):
+        assert _select(tq, **kw) == INVALID, kw
+    for kw in (dict(w=P + 2), dict(index=P + 1), dict(count=P + 2), dict(lens=P + 1), dict(pad=P + 2)):
+        assert _select(tq, **kw) == ALIGN, kw
+
+
+def _gather(tq, src=None, dst=None, B=1, H=2, D=128, kb=8, vb=3, index=P, n=4, heads=0, count=None, off=None, length=P,
+            sw=None, dw=None):
+    s = _cache(tq) if src is None else src
+    d = _cache(tq) if dst is None else dst
+    return tq.lib().tq_cache_gather(ctypes.byref(s), ctypes.byref(d), B, H, D, kb, vb, index, n, heads, count, off,
+                                    length, sw, dw, None)
+
+
+def test_gather_refusals(tq):
+    assert _gather(tq, B=0) == OK and _gather(tq, H=0) == OK and _gather(tq, n=0, length=None) == OK
+    for kw in (dict(B=-1), dict(H=-1), dict(n=-1), dict(index=0), dict(src=_cache(tq, k_codes=0)),
+               dict(dst=_cache(tq, v_scales=0)), dict(src=_cache(tq, -1)), dict(dst=_cache(tq, -1)), dict(sw=P),
+               dict(B=1 << 30, H=4), dict(n=1 << 31), dict(src=_cache(tq, 1 << 40)), dict(B=1 << 20, n=1 << 20)):
+        assert _gather(tq, **kw) == INVALID, kw
+    assert _gather(tq, D=96) == HEAD_DIM
+    assert _gather(tq, kb=3) == BITS and _gather(tq, vb=7) == BITS
+    for kw in (dict(index=P + 2), dict(count=P + 1), dict(off=P + 2), dict(length=P + 1), dict(sw=P + 2, dw=P),
+               dict(sw=P, dw=P + 1), dict(src=_cache(tq, k_codes=P + 8)), dict(dst=_cache(tq, v_codes=P + 4))):
+        assert _gather(tq, **kw) == ALIGN, kw
+    assert tq.lib().tq_cache_gather(None, None, 1, 2, 128, 8, 3, P, 4, 0, None, None, None, None, None, None) == INVALID
+
+
+def test_binding_refuses_wrong_tensors(tq):
+    """Shapes, types and devices are checked before the library is called."""
+    G = 4
+    cache = {"k_codes": torch.zeros((1, 2, 16, 128), dtype=torch.uint8),
+             "k_scales": torch.zeros((1, 2, 16, G), dtype=torch.float16),
+             "k_zeros": torch.zeros((1, 2, 16, G), dtype=torch.float16),
+             "v_codes": torch.zeros((1, 2, 16, 48), dtype=torch.uint8),
+             "v_scales": torch.zeros((1, 2, 16, G), dtype=torch.float16)}
+    q = torch.zeros((1, 4, 3, 128), dtype=torch.bfloat16)
+    lse = torch.zeros((1, 4, 3))
+    for bad in (dict(q=q.float()), dict(q=q[..., ::2]), dict(q=q[0]), dict(cache=dict(cache, k_scales=cache["k_scales"].float())),
+                dict(cache=dict(cache, v_codes=cache["v_codes"][:, :, :8])), dict(vb=4), dict(out_dtype=torch.float16),
+                dict(parents=torch.zeros((1, 3), dtype=torch.int64)), dict(parents=torch.zeros((1, 2), dtype=torch.int32)),
+                dict(lens=torch.zeros((2,), dtype=torch.int32)), dict(q=q.expand(2, -1, -1, -1)), dict()):
+        a = dict(q=q, cache=cache, vb=3, out_dtype=torch.bfloat16, parents=None, lens=None)
+        a.update(bad)
+        with pytest.raises(ValueError):  # the last: tensors on the host
+            tq.tq_tree_attention(a["q"], a["cache"], 16, cache, 8, True, a["vb"], parents=a["parents"], lens=a["lens"],
+                                 out_dtype=a["out_dtype"])
+    with pytest.raises(ValueError):
+        tq.tq_attention_weights(q, lse, cache, 16, 8, True)
+    with pytest.raises(ValueError):
+        tq.tq_attention_weights(q.float(), lse, cache, 16, 8, True)
+    with pytest.raises(ValueError):
+        tq.tq_evict_select(torch.zeros((1, 2, 16)), 16, 4, 1)
+    with pytest.raises(ValueError):
+        tq.tq_evict_select(torch.zeros((2, 16)), 16, 4, 1)
+    with pytest.raises(ValueError):
+        tq.tq_cache_gather(cache, cache, torch.zeros((1, 4), dtype=torch.int32))
+
+
+def test_reference_of_one_token_by_hand():
+    """The reference itself: one key alone gives its own value row back, and
+    lse is the score."""
+    c = rc.random_cache(1, 1, 1, 64, 8, True, 8, 3)
+    t = rc.random_cache(1, 1, 1, 64, 8, True, 8, 4)
+    q = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16)
+    out, lse, _, _ = rc.tree_reference(q, c, 1, t, 8, True, 8, lens=[0])
+    _, v = rc.decoded(t, 1, 8, True, 8)
+    assert np.allclose(out[0, 0, 0], v[0, 0, 0] @ rc.rotation(64)) and lse[0, 0, 0] == 0
+    out, lse, _, _ = rc.tree_reference(q, c, 1, t, 8, True, 8)
+    assert abs(lse[0, 0, 0] - np.log(2)) < 1e-12
+    index, count = rc.select_reference(torch.tensor([[[1.0, 5.0, 5.0, 0.0, 2.0]]]), 5, 3, 1)
+    assert index.tolist() == [[[1, 2, 4]]] and count.tolist() == [3]

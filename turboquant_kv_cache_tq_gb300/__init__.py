@@ -11,6 +11,7 @@ five packed-cache buffers with torch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -21,7 +22,8 @@ __all__ = [
     "TQError", "lib", "tq_packed_dim", "tq_encode_kv", "tq_decode_kv", "tq_decode_kv_rotated",
     "tq_unrotate", "tq_lloyd_max_index", "tq_decode_attention", "tq_decode_attention_workspace_size",
     "tq_cache_assemble", "merge_rows", "extend_rows", "extract_row", "filter_rows", "tq_lloyd_max_fit",
-    "tq_lloyd_max_fit_status",
+    "tq_lloyd_max_fit_status", "tq_tree_attention", "tq_tree_attention_workspace_size", "tq_attention_weights",
+    "tq_evict_select", "tq_cache_gather", "commit_path", "evict_rows",
     "tq_status_string", "alloc_cache", "HEAD_DIMS", "VALUE_BITS", "KEY_MODES",
 ]
 
@@ -88,6 +90,18 @@ def load_library(path: str) -> ctypes.CDLL:
     L.tq_decode_attention_workspace_size.argtypes = [I64, I64, I64, I64]
     L.tq_cache_assemble.restype = I
     L.tq_cache_assemble.argtypes = [P, I64, I64, I64, I, I, P, P, P, P, P, I64, I64, P]
+    L.tq_tree_attention.restype = I
+    L.tq_tree_attention.argtypes = [P, I64, I64, I64, P, I64, I64, I64, P, P, I, I, I, P, P, ctypes.c_float, P, I,
+                                    P, P, I64, P]
+    L.tq_tree_attention_workspace_size.restype = I64
+    L.tq_tree_attention_workspace_size.argtypes = [I64, I64, I64, I64, I64]
+    L.tq_attention_weights.restype = I
+    L.tq_attention_weights.argtypes = [P, P, I64, I64, I64, P, P, P, I64, I64, I64, I64, I, I, P, P, P, P, I64,
+                                       ctypes.c_float, P, P, I64, P]
+    L.tq_evict_select.restype = I
+    L.tq_evict_select.argtypes = [P, I64, I64, I64, I64, P, P, I64, I64, P, P, P]
+    L.tq_cache_gather.restype = I
+    L.tq_cache_gather.argtypes = [P, P, I64, I64, I64, I, I, P, I64, I, P, P, P, P, P, P]
     L.tq_lloyd_max_fit.restype = I
     L.tq_lloyd_max_fit.argtypes = [P, I64, I, I, P, P, P, P, I64, P]
     L.tq_lloyd_max_fit_bounded.restype = I
@@ -358,6 +372,229 @@ def filter_rows(batch, S: int, keep, stream=None) -> dict:
     dst = _alloc_like(batch, len(keep), batch["k_codes"].shape[2])
     tq_cache_assemble([(batch, int(b), 0, S) for b in keep], dst, S, stream)
     return dst
+
+
+# ---- ragged packed caches: draft trees and eviction --------------------------------
+class TQPackedCache(ctypes.Structure):
+    """tq_packed_cache of include/tq.h."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("k_zeros", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("t_cap", ctypes.c_int64)]
+
+
+_BUFFERS = ("k_codes", "k_scales", "k_zeros", "v_codes", "v_scales")
+
+
+def _cache_shape(cache: dict, B, H, D, k_bits, v_bits, device, names=_BUFFERS) -> int:
+    """Checks the buffers of a packed cache [B,H,t_cap,X]; returns t_cap."""
+    t_cap = cache["k_codes"].shape[2] if cache["k_codes"].dim() == 4 else -1
+    G = D // GROUP
+    for name in names:
+        t = cache[name]
+        x = G if name[2:] in ("scales", "zeros") else D * (k_bits if name == "k_codes" else v_bits) // 8
+        dtype = torch.uint8 if name[2:] == "codes" else torch.float16
+        if t.dtype != dtype or tuple(t.shape) != (B, H, t_cap, x) or not t.is_contiguous() or t.device != device:
+            raise ValueError("cache buffer %s must be a contiguous [%d,%d,t_cap,%d] %s tensor on %s"
+                             % (name, B, H, x, dtype, device))
+    return t_cap
+
+
+def _int_ptr(t, shape, what, device):
+    """Device pointer of an optional int32 tensor of a given shape."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous int32 tensor %s on %s" % (what, list(shape), device))
+    return t.data_ptr()
+
+
+def _float_ptr(t, shape, what, device):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous float32 tensor %s on %s" % (what, list(shape), device))
+    return t.data_ptr()
+
+
+def _view(cache: dict, t_cap: int) -> TQPackedCache:
+    return TQPackedCache(*(cache[n].data_ptr() for n in _BUFFERS), t_cap)
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _launching(device, stream):
+    """A context for allocations and one or more calls: the tensors' device is
+    current (the library asks the current device for its size and error word)
+    and so is the stream the work goes to (the allocator gives memory back in
+    that stream's order)."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device, got %s" % device)
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _switched(device, stream)
+
+
+def tq_tree_attention_workspace_size(B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
+    """Bytes of scratch tq_tree_attention needs (on the current device)."""
+    r = int(lib().tq_tree_attention_workspace_size(int(B), int(Hq), int(Hkv), int(N), int(D)))
+    if r < 0:
+        raise TQError(-r, "tq_tree_attention_workspace_size")
+    return r
+
+
+def tq_tree_attention(q: torch.Tensor, cache: dict, T: int, tree: dict, k_bits: int, k_signed: bool, v_bits: int,
+                      parents=None, lens=None, left_pad=None, scale=None, out_dtype=torch.bfloat16, out=None,
+                      lse=None, workspace=None, stream=None):
+    """Attention of a tree of N drafted tokens, q [B,Hq,N,D] bf16, over tokens
+    [left_pad[b], lens[b]) of a packed cache and over the nodes' own keys and
+    values in the packed cache `tree` (tokens [0,N)): node i attends to itself
+    and its ancestors by parents [B,N] (int32; -1: follows the sequence; other
+    values outside [0,i): the node is absent; None: a chain). lens and left_pad:
+    int32 device tensors [B] or None; lens <= T. Returns (out [B,Hq,N,D] of
+    out_dtype, lse [B,Hq,N] fp32). workspace: a uint8 device tensor of at least
+    tq_tree_attention_workspace_size bytes (allocated when None)."""
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
+    if out_dtype not in _DTYPE:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    B, Hq, N, D = q.shape
+    dev = q.device
+    Hkv = cache["k_codes"].shape[1]
+    views = []
+    for c in (cache, tree):
+        views.append(_view(c, _cache_shape(c, B, Hkv, D, k_bits, v_bits, dev)))
+    parents_p = _int_ptr(parents, (B, N), "parents", dev)
+    lens_p, pad_p = _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev)
+    if out is not None and (out.dtype != out_dtype or out.shape != q.shape or not out.is_contiguous()
+                            or out.device != dev):
+        raise ValueError("out must be a contiguous [B,Hq,N,D] tensor of out_dtype on q's device")
+    with _launching(dev, stream):
+        if out is None:
+            out = torch.empty((B, Hq, N, D), dtype=out_dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = tq_tree_attention_workspace_size(B, Hq, Hkv, N, D)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        st = lib().tq_tree_attention(
+            q.data_ptr(), B, Hq, N, ctypes.byref(views[0]), Hkv, int(T), D, ctypes.byref(views[1]), parents_p,
+            int(k_bits), int(bool(k_signed)), int(v_bits), lens_p, pad_p, D ** -0.5 if scale is None else float(scale),
+            out.data_ptr(), _DTYPE[out_dtype], _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    _check(st, "tq_tree_attention")
+    return out, lse
+
+
+def tq_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: dict, T: int, k_bits: int, k_signed: bool,
+                         path=None, n_path=None, lens=None, left_pad=None, scale=None, weights=None, out=None,
+                         stream=None) -> torch.Tensor:
+    """weights + the attention weights that the last n_path[b] tokens of each
+    sequence give to its tokens, [B,Hkv,w_cap] fp32 (w_cap >= T): observer i is
+    query row path[b,i] of q [B,Hq,N,D] with log-sum-exp lse [B,Hq,N]
+    (tq_tree_attention). path: int32 [B,P] or None (rows 0..N-1, P = N);
+    n_path: int32 [B] or None (P). weights: None (zeros), or the sums so far;
+    out: None (a new tensor), or where to write, `weights` itself for an update
+    in place."""
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
+    B, Hq, N, D = q.shape
+    dev = q.device
+    Hkv = cache["k_codes"].shape[1]
+    t_cap = _cache_shape(cache, B, Hkv, D, k_bits, 0, dev, _BUFFERS[:3])
+    P = N if path is None else path.shape[-1]
+    with _launching(dev, stream):
+        if out is None:
+            w_cap = int(T) if weights is None else weights.shape[-1]
+            out = torch.empty((B, Hkv, w_cap), dtype=torch.float32, device=dev)
+        w_cap = out.shape[-1]
+        st = lib().tq_attention_weights(
+            q.data_ptr(), _float_ptr(lse, (B, Hq, N), "lse", dev), B, Hq, N, cache["k_codes"].data_ptr(),
+            cache["k_scales"].data_ptr(), cache["k_zeros"].data_ptr(), Hkv, int(T), D, t_cap, int(k_bits),
+            int(bool(k_signed)), _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
+            _int_ptr(path, (B, P), "path", dev), _int_ptr(n_path, (B,), "n_path", dev), P,
+            D ** -0.5 if scale is None else float(scale), _float_ptr(weights, (B, Hkv, w_cap), "weights", dev),
+            _float_ptr(out, (B, Hkv, w_cap), "out", dev), w_cap, _stream_handle(stream, dev))
+    _check(st, "tq_attention_weights")
+    return out
+
+
+def tq_evict_select(weights: torch.Tensor, T: int, keep: int, recent: int, lens=None, left_pad=None, index=None,
+                    count=None, stream=None):
+    """The tokens that stay when each (batch row, head) is cut to `keep` tokens:
+    the last `recent` ones and the largest weights [B,H,w_cap] among the others
+    (equal weights: the lowest token). Returns (index int32 [B,H,keep],
+    ascending, then -1; count int32 [B])."""
+    if weights.dim() != 3:
+        raise ValueError("weights must be a [B,H,w_cap] tensor")
+    B, H, w_cap = weights.shape
+    dev = weights.device
+    if keep < 0:
+        raise ValueError("keep must not be negative")
+    with _launching(dev, stream):
+        if index is None:
+            index = torch.empty((B, H, int(keep)), dtype=torch.int32, device=dev)
+        if count is None:
+            count = torch.empty((B,), dtype=torch.int32, device=dev)
+        st = lib().tq_evict_select(
+            _float_ptr(weights, (B, H, w_cap), "weights", dev), B, H, int(T), w_cap, _int_ptr(lens, (B,), "lens", dev),
+            _int_ptr(left_pad, (B,), "left_pad", dev), int(keep), int(recent),
+            _int_ptr(index, (B, H, int(keep)), "index", dev), _int_ptr(count, (B,), "count", dev),
+            _stream_handle(stream, dev))
+    _check(st, "tq_evict_select")
+    return index, count
+
+
+def tq_cache_gather(src: dict, dst: dict, index: torch.Tensor, count=None, dst_off=None, src_weights=None,
+                    dst_weights=None, dst_len=None, stream=None):
+    """Copies tokens index [B,n] or [B,H,n] (int32) of the packed cache src to
+    tokens dst_off[b] + j, j < count[b], of dst (with their weights, or zero
+    weights, when dst_weights is given). Returns (dst, dst_len), dst_len int32
+    [B] = min(dst_off + count, capacity)."""
+    B, H, _, D, kb, vb = _cache_geometry(src)
+    dev = src["k_codes"].device
+    s_cap = _cache_shape(src, B, H, D, kb, vb, dev)
+    d_cap = _cache_shape(dst, B, H, D, kb, vb, dev)
+    heads = index.dim() == 3
+    n = index.shape[-1]
+    sv, dv = _view(src, s_cap), _view(dst, d_cap)
+    with _launching(dev, stream):
+        if dst_len is None:
+            dst_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        st = lib().tq_cache_gather(
+            ctypes.byref(sv), ctypes.byref(dv), B, H, D, kb, vb,
+            _int_ptr(index, (B, H, n) if heads else (B, n), "index", dev), n, int(heads),
+            _int_ptr(count, (B,), "count", dev), _int_ptr(dst_off, (B,), "dst_off", dev),
+            _int_ptr(dst_len, (B,), "dst_len", dev), _float_ptr(src_weights, (B, H, s_cap), "src_weights", dev),
+            _float_ptr(dst_weights, (B, H, d_cap), "dst_weights", dev), _stream_handle(stream, dev))
+    _check(st, "tq_cache_gather")
+    return dst, dst_len
+
+
+def commit_path(cache: dict, lens: torch.Tensor, tree: dict, path: torch.Tensor, n_path: torch.Tensor, weights=None,
+                stream=None) -> torch.Tensor:
+    """Appends the accepted nodes path[b, :n_path[b]] of a draft tree's cache to
+    each sequence of `cache` (weights, when given, start at zero). Returns the
+    new lengths."""
+    return tq_cache_gather(tree, cache, path, count=n_path, dst_off=lens, dst_weights=weights, stream=stream)[1]
+
+
+def evict_rows(cache: dict, weights: torch.Tensor, T: int, keep: int, recent: int, lens=None, left_pad=None,
+               t_cap=None, stream=None):
+    """Cuts every (batch row, head) to at most `keep` tokens by their attention
+    weights -> (a fresh cache whose rows start at token 0, its weights, its
+    lengths)."""
+    B, H, cap = cache["k_codes"].shape[:3]
+    if weights.shape[-1] != cap:
+        raise ValueError("weights must be [B,H,%d], the cache's capacity" % cap)
+    with _launching(weights.device, stream):
+        dst = _alloc_like(cache, B, keep if t_cap is None else t_cap)
+        new = torch.zeros((B, H, dst["k_codes"].shape[2]), dtype=torch.float32, device=weights.device)
+        index, count = tq_evict_select(weights, T, keep, recent, lens=lens, left_pad=left_pad)
+        _, length = tq_cache_gather(cache, dst, index, count=count, src_weights=weights, dst_weights=new)
+    return dst, new, length
 
 
 # ---- Lloyd-Max table fit (turboquant-tables.ts) -----------------------------------

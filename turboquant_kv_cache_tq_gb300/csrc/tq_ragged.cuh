@@ -1,0 +1,62 @@
+// Shared by the calls on ragged packed caches (tq_tree_attention,
+// tq_attention_weights, tq_evict_select, tq_cache_gather): per-row lengths
+// that only the device knows, draft trees, and the host's checks.
+#pragma once
+
+#include <cstdint>
+
+#include "../../include/tq.h"
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+// A packed cache as the kernels read it.
+struct PackedView {
+  const uint8_t* k_codes;
+  const uint16_t* k_scales;
+  const uint16_t* k_zeros;
+  const uint8_t* v_codes;
+  const uint16_t* v_scales;
+  long long t_cap;
+};
+
+// Tokens [lo, hi) of batch row b: lens and left_pad clamped as tq.h says.
+__device__ __forceinline__ void row_range(const int* lens, const int* left_pad, int b, int T, int& lo, int& hi) {
+  hi = lens != nullptr ? min(max(lens[b], 0), T) : T;
+  lo = left_pad != nullptr ? min(max(left_pad[b], 0), hi) : 0;
+}
+
+// The nodes that node i of a tree attends to, one bit each: i and its
+// ancestors, or none when i's chain of parents does not end at -1. A parent is
+// a lower number, so the walk ends.
+__device__ __forceinline__ unsigned long long node_ancestors(const int* parents, int i) {
+  if (parents == nullptr) return i == 63 ? ~0ull : (2ull << i) - 1ull;
+  unsigned long long m = 0;
+  for (;;) {
+    m |= 1ull << i;
+    const int up = parents[i];
+    if (up == -1) return m;
+    if (up < 0 || up >= i) return 0ull;
+    i = up;
+  }
+}
+
+// ---- host side
+inline bool ragged_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool ragged_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool ragged_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }
+inline bool ragged_value_bits_ok(int b) { return b == 2 || b == 3 || b == 4 || b == 5 || b == 8; }
+inline int ragged_key_mode(int bits, int is_signed) {
+  if (is_signed) return bits == 8 ? kK8Signed : -1;
+  return bits == 2 ? kK2 : bits == 4 ? kK4 : bits == 5 ? kK5 : bits == 8 ? kK8 : -1;
+}
+// Whether B * H rows of t_cap tokens can be addressed: byte offsets of any
+// buffer (at most 512 bytes a token) stay far inside 63 bits.
+inline bool ragged_sizes_ok(int64_t B, int64_t H, int64_t t_cap) {
+  const int64_t lim = 0x7fffffffLL;
+  return B <= lim && H <= lim && t_cap <= lim && (B == 0 || H <= lim / B) &&
+         (B == 0 || H == 0 || t_cap <= (1LL << 62) / (B * H * 512));
+}
+
+}  // namespace tq
