@@ -4,6 +4,8 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
+#include <vector>
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -43,6 +45,27 @@ __device__ __forceinline__ unsigned long long node_ancestors(const int* parents,
 }
 
 // ---- host side
+// Lets a kernel take `bytes` of dynamic shared memory on the current device
+// (asked for once per kernel and device).
+template <typename Params>
+inline cudaError_t allow_smem(void (*kernel)(Params), int bytes) {
+  struct Entry {
+    const void* kernel;
+    int dev;
+  };
+  static std::mutex mutex;
+  static std::vector<Entry> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  for (const Entry& x : done)
+    if (x.kernel == reinterpret_cast<const void*>(kernel) && x.dev == dev) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.push_back(Entry{reinterpret_cast<const void*>(kernel), dev});
+  return e;
+}
+
 inline bool ragged_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ragged_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool ragged_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }
