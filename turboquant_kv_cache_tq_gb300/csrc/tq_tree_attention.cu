@@ -14,13 +14,13 @@ struct TreePlan {
 
 bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, TreePlan* t) {
   const long long lim = 0x7fffffffLL;
-  t->TT = D == 512 ? TreeShape<512>::TT : TreeShape<128>::TT;
+  t->TT = D == 512 ? TreeShape<512>::TT : D == 256 ? TreeShape<256>::TT : D == 128 ? TreeShape<128>::TT : TreeShape<64>::TT;
   t->DV = static_cast<int>(D == 512 ? TreeShape<512>::DV : D);
   t->R = Hq / Hkv * N;
   t->RB = (t->R + kTreeRows - 1) / kTreeRows;
   t->rows = (t->R + t->RB - 1) / t->RB;
-  // (head_dim 512 has tiles of 32 tokens, a share too small to cut)
-  t->copies = D == 512 || t->rows > 64 ? 1 : t->rows > 32 ? 2 : 4;
+  // (a lane's share is 16 tokens at least)
+  t->copies = t->rows > 64 ? 1 : t->rows > 32 || t->TT == 32 ? 2 : 4;
   t->slots = (t->copies * t->rows + 3) / 4 * 4;
   if (t->RB * (D / t->DV) > lim / Hkv) return false;
   t->HH = Hkv * t->RB * (D / t->DV);
@@ -68,7 +68,7 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   TreePlan t;
   tree_plan(B, Hq, Hkv, N, D, &t);
   // tiles in all, of which a block counts its own in 32 bits
-  const long long tiles = (T + t.TT - 1) / t.TT + (N + t.TT - 1) / t.TT;
+  const long long tiles = (T + t.TT - 1) / t.TT + 1 + (N + t.TT - 1) / t.TT;
   if (tiles > (1LL << 36) / (B * t.HH)) return TQ_ERR_INVALID_ARG;
   const void* ptrs[] = {q, out, workspace, tree->k_codes, tree->k_scales, tree->k_zeros, tree->v_codes, tree->v_scales,
                         cache->k_codes, cache->k_scales, cache->k_zeros, cache->v_codes, cache->v_scales};
@@ -111,6 +111,12 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   p.HH = static_cast<int>(t.HH);
   p.kmode = kmode;
   p.vb = v_bits;
+  p.x_keys = static_cast<int>(D * k_bits / 8);
+  p.x_values = static_cast<int>(D * v_bits / 8);
+  p.vtab_stride = 128;
+  p.bulk = 1;
+  for (const int64_t cap : {cache->t_cap, tree->t_cap})
+    if (cap * (D / 16) % 16 != 0 || cap * p.x_keys % 16 != 0 || cap * p.x_values % 16 != 0) p.bulk = 0;
   p.out_f32 = out_dtype == TQ_F32;
   p.err = device_error_word();
   // one range of tiles per SM (a block holds all of an SM's tensor memory)

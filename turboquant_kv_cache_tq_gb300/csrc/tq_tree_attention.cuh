@@ -27,6 +27,8 @@
 // lengths.
 #pragma once
 
+#include <type_traits>
+
 #include "tq_attention.cuh"
 #include "tq_ragged.cuh"
 #include "tq_tcgen05.cuh"
@@ -51,6 +53,9 @@ struct TreeParams {
   int slots;          // rows a record holds (copies * rows, a multiple of 4)
   int HH;             // segments of a batch row: Hkv * RB * value halves
   int kmode, vb, out_f32, grid;
+  int x_keys, x_values;  // bytes of a token's packed codes
+  unsigned vtab_stride;  // 128: bytes between entries of the value table
+  int bulk;              // every tile of both caches starts on 16 bytes in every buffer
   float scale_log2;   // |scale| * log2(e)
   int negate;         // scale < 0
   float rot_scale;
@@ -58,42 +63,68 @@ struct TreeParams {
 
 template <int D>
 struct TreeShape {
-  static constexpr int TT = D == 512 ? 32 : 64;      // tokens of a tile
+  static constexpr int TT = D >= 256 ? 32 : 64;      // tokens of a tile
   static constexpr int DV = D == 512 ? 256 : D;      // value elements a block accumulates
   static constexpr int VH = D / DV;
   static constexpr int NGK = D / kGroup, NGV = DV / kGroup;
-  static constexpr int KP = TT * NGK / 128, VP = TT * NGV / 128;  // groups a decoding thread takes of a tile
   static constexpr int K_BYTES = TT * D * 2, V_BYTES = TT * DV * 2;
   static constexpr int KS = D == 512 ? 1 : 2, VS = 2;  // decoded stages
-  static constexpr bool Q_TMEM = D != 512;
-  static constexpr int Q_BYTES = Q_TMEM ? 0 : 128 * D * 2;
+  // A group of four decoding warps owns a stage and takes every other tile;
+  // with one stage both groups share each tile (a barrier's parity tells
+  // neighbouring phases apart only, so a warp has to see every phase).
+  static constexpr int KWARPS = KS == 1 ? 8 : 4, VWARPS = 4;
+  static constexpr int KP = TT * NGK / (32 * KWARPS), VP = TT * NGV / (32 * VWARPS);  // groups a thread takes of a tile
+  // Queries: the first QT elements of a row in tensor memory, the rest (head_dim
+  // 512: no room beside 256 output columns) in shared memory.
+  static constexpr int QT = D == 512 ? 256 : D;
+  static constexpr int Q_BYTES = 128 * (D - QT) * 2;
   static constexpr int TAB = 32768;
-  // shared memory: K stages | V stages | queries | value table | control
+  // packed stages: codes, then scales (keys: and zero points; values: and the
+  // tile's first and last token of the sequence)
+  static constexpr int NR = D == 512 ? 2 : 4;
+  static constexpr int KR_SC = TT * D, KR_ZP = KR_SC + TT * NGK * 2, KR_BYTES = KR_ZP + TT * NGK * 2;
+  static constexpr int VR_SC = TT * DV, VR_SPAN = VR_SC + TT * NGV * 2, VR_BYTES = VR_SPAN + 16;
+  // shared memory: K stages | V stages | queries | packed K | packed V | value table | control
   static constexpr int V_OFF = KS * K_BYTES;
   static constexpr int Q_OFF = V_OFF + VS * V_BYTES;
-  static constexpr int T_OFF = Q_OFF + Q_BYTES;
+  static constexpr int KR_OFF = Q_OFF + Q_BYTES;
+  static constexpr int VR_OFF = KR_OFF + NR * KR_BYTES;
+  static constexpr int T_OFF = VR_OFF + NR * VR_BYTES;
   static constexpr int C_OFF = T_OFF + TAB;
   static constexpr int SMEM = C_OFF + 512;
-  // tensor memory columns: O | S | P high | P low | Q
-  static constexpr int O_COL = 0, S_COL = DV, PH_COL = DV + TT, PL_COL = PH_COL + TT / 2, Q_COL = PL_COL + TT / 2;
-  static_assert(Q_COL + (Q_TMEM ? D / 2 : 0) <= 512, "tensor memory");
+  // tensor memory columns: O | S, NS times | P (high half, low half), NS times | Q
+  static constexpr int NS = 2;
+  static constexpr int O_COL = 0, S_COL = DV, P_COL = S_COL + NS * TT, Q_COL = P_COL + NS * TT;
+  static_assert(Q_COL + QT / 2 <= 512, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
-  static constexpr int TAILS = 64 / TT;              // tail tiles of the largest tree
 };
 
-constexpr int kTreeThreads = 416;  // warps 0-3 softmax, 4-7 keys, 8-11 values, 12 matrix instructions
+// Warps 0-3 softmax (tensor memory ties each to a quadrant of lanes and so to
+// one of the SM's four schedulers), 4-19 decoding, 20 scores, 21 weighted
+// values, 22 and 23 load packed keys and values. Instruction fetch bounds a kernel of many roles: a
+// scheduler's instruction cache holds some hundred instructions and a warp
+// that misses it waits (7 of 20 cycles an instruction with every role on every
+// scheduler and unrolled loops). So warps 4-19 decode keys on schedulers 0 and
+// 1 and values on 2 and 3, four warps to a loop, and the loops are rolled.
+constexpr int kTreeThreads = 768;
 constexpr int kTreeRows = 128;
 
 // Control words in shared memory (byte offsets).
-enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcSFree = 72, kcPFull = 80,
-             kcPFree = 88, kcQFull = 96, kcDrain = 104, kcTmem = 112, kcQuit = 116, kcTile = 120, kcB = 124, kcHH = 128,
-             kcCount = 136, kcBad = 256 };
+enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcSFree = 80, kcPFull = 96,
+             kcPFree = 112, kcQFull = 128, kcDrain = 136, kcTmem = 152, kcQuit = 156, kcTile = 160, kcB = 164,
+             kcHH = 168, kcCount = 172, kcKLoaded = 176, kcKTaken = 208, kcVLoaded = 240, kcVTaken = 272, kcAnyBad = 304, kcBad = 320 };
 
-// Tiles of one segment of batch row b, and its token range.
+// Tiles of the sequence of a batch row with tokens [lo, hi); they start at a
+// multiple of 16 tokens, which keeps every buffer's rows 16-byte aligned.
 template <int TT>
-__device__ __forceinline__ int tree_row_tiles(const TreeParams& p, int b, int& lo, int& hi) {
+__device__ __forceinline__ int tree_main_tiles(int lo, int hi) {
+  return hi > lo ? (hi - (lo & ~15) + TT - 1) / TT : 0;
+}
+template <int TT>
+__device__ __forceinline__ int tree_row_tiles(const TreeParams& p, int b) {
+  int lo, hi;
   row_range(p.lens, p.left_pad, b, p.T, lo, hi);
-  return (hi - lo + TT - 1) / TT + (p.N + TT - 1) / TT;
+  return tree_main_tiles<TT>(lo, hi) + (p.N + TT - 1) / TT;
 }
 
 // A walk over the block's tiles, the same in every warp.
@@ -104,8 +135,9 @@ struct TreeWalk {
   int left;  // tiles still to come, this one included
 
   __device__ __forceinline__ void row(const TreeParams& p) {
-    n = tree_row_tiles<TT>(p, b, lo, hi);
-    n_main = (hi - lo + TT - 1) / TT;
+    row_range(p.lens, p.left_pad, b, p.T, lo, hi);
+    n_main = tree_main_tiles<TT>(lo, hi);
+    n = n_main + (p.N + TT - 1) / TT;
   }
   __device__ __forceinline__ void init(const TreeParams& p, const uint8_t* ctl) {
     tile = *reinterpret_cast<const int*>(ctl + kcTile);
@@ -122,284 +154,407 @@ struct TreeWalk {
       if (left > 0) row(p);
     }
   }
-  __device__ __forceinline__ void next(const TreeParams& p) {
-    --left;
-    if (++tile == n) next_segment(p);
-  }
   __device__ __forceinline__ bool tail() const { return tile >= n_main; }
-  // the tile's first token and its number of tokens
-  __device__ __forceinline__ void span(const TreeParams& p, int& t0, int& valid) const {
-    t0 = tail() ? (tile - n_main) * TT : lo + tile * TT;
-    valid = min(TT, (tail() ? p.N : hi) - t0);
+  // the tile's first token, and which of its tokens [first, end) are in the
+  // sequence or the tree
+  __device__ __forceinline__ void span(const TreeParams& p, int& t0, int& first, int& end) const {
+    const bool t = tail();
+    t0 = t ? (tile - n_main) * TT : (lo & ~15) + tile * TT;
+    first = t ? 0 : max(lo - t0, 0);
+    end = min(TT, (t ? p.N : hi) - t0);
   }
 };
 
-// Where the group of a decoding thread sits: unit u = (octet of tokens, group)
-// by quarter-warps of eight tokens of one group, so that their 16-byte stores
-// into the swizzled tile meet eight distinct banks groups and a warp reads
-// whole rows.
+// Where the group of a decoding thread sits. Eight lanes take four groups of
+// two tokens (head_dim 64: two groups of four), and a thread decodes its
+// group's two halves of 16 elements in the order (flip, 1 - flip). So the eight
+// lanes' 16-byte reads of 8-bit codes and their 16-byte stores into the
+// swizzled tile each meet eight distinct places of a 128-byte line (64: the
+// stores only).
+template <int NG, int WARPS>
+__device__ __forceinline__ void tree_unit(int piece, int warp, int lane, int& token, int& group) {
+  const int c = (piece * WARPS + warp) * 4 + (lane >> 3);
+  if constexpr (NG == 2) {
+    token = c * 4 + ((lane >> 1) & 3);
+    group = lane & 1;
+  } else {
+    token = c / (NG / 4) * 2 + ((lane >> 2) & 1);
+    group = c % (NG / 4) * 4 + (lane & 3);
+  }
+}
 template <int NG>
-__device__ __forceinline__ void tree_unit(int piece, int warp4, int lane, int& token, int& group) {
-  const int u = (piece * 4 + warp4) * 4 + (lane >> 3);
-  group = u % NG;
-  token = (u / NG) * 8 + (lane & 7);
+__device__ __forceinline__ int tree_flip(int lane) {
+  return NG == 2 ? 0 : ((lane >> 2) ^ (lane >> 1)) & 1;
 }
 
-// Stores the 32 bf16 of a group (16 words) into a decoded tile.
+// Stores the 16 bf16 of half h of a group (8 words) into a decoded tile.
 template <int TT>
-__device__ __forceinline__ void tree_store_group(uint32_t tile, int token, int group, const uint32_t (&w)[16]) {
+__device__ __forceinline__ void tree_store_half(uint32_t tile, int token, int group, int h, const uint32_t (&w)[8]) {
   const uint32_t line = tile + (group >> 1) * (TT * 128) + token * 128;
-  const int c0 = (group & 1) * 4, x = token & 7;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    sts128(line + (((c0 + j) ^ x) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  const int c0 = (group & 1) * 4 + 2 * h, x = token & 7;
+  sts128(line + ((c0 ^ x) << 4), w[0], w[1], w[2], w[3]);
+  sts128(line + (((c0 + 1) ^ x) << 4), w[4], w[5], w[6], w[7]);
 }
 
+// The packed words of half h (16 codes of B bits, from bit 0 of w on) of the
+// group at `a`.
 template <int B>
-struct TreeGroup {
-  uint32_t w[B];
-  uint32_t scale, zero;  // fp16 bits
-};
+__device__ __forceinline__ void tree_words(uint32_t a, int h, uint32_t (&w)[(B + 1) / 2]) {
+  if constexpr (B == 8) {
+    const uint4 u = lds128(a + 16 * h);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else if constexpr (B == 4) {
+    const uint2 u = lds64(a + 8 * h);
+    w[0] = u.x; w[1] = u.y;
+  } else if constexpr (B == 2) {
+    w[0] = lds32(a + 4 * h);
+  } else if constexpr (B == 3) {
+    const uint32_t x = lds32(a + 4 * h), y = lds32(a + 4 * h + 4);
+    w[0] = __funnelshift_r(x, y, 16 * h);
+    w[1] = y >> (16 * h);
+  } else {
+    const uint32_t x = lds32(a + 8 * h), y = lds32(a + 8 * h + 4), z = lds32(a + 8 * h + 8);
+    w[0] = __funnelshift_r(x, y, 16 * h);
+    w[1] = __funnelshift_r(y, z, 16 * h);
+    w[2] = z >> (16 * h);
+  }
+}
 
-// The keys' warps: decode tile after tile into the key stages, with the packed
-// words of the next tiles on their way in registers.
-template <int D, int KMODE>
-__device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp4, int lane) {
+// One warp copies n rows of X bytes, src_pitch bytes apart, side by side, in
+// the widest pieces that the rows' alignment allows.
+__device__ __forceinline__ void tree_copy_rows(uint32_t dst, const uint8_t* src, int src_pitch, int X, int n, int lane) {
+  const int odd = X | src_pitch;
+  const int shift = (odd & 15) == 0 ? 4 : (odd & 7) == 0 ? 3 : 2;
+  const int per = X >> shift;
+#pragma unroll 1
+  for (int i = lane; i < n * per; i += 32) {
+    const int t = i / per, c = (i - t * per) << shift;
+    const uint8_t* from = src + static_cast<long long>(t) * src_pitch + c;
+    const uint32_t to = dst + t * X + c;
+    if (shift == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else if (shift == 3) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+  }
+}
+
+// The loading warps (keys and values): the packed rows of tile after tile into
+// the stages, by bulk copies where every tile of both caches starts on 16 bytes
+// in every buffer (p.bulk: t_cap times a row's bytes a multiple of 16), else by
+// 4- to 16-byte copies. Rows are copied as far as the cache goes; which of them
+// belong to the sequence goes to the values' warps with the tile. A warp's
+// steps are in one chain, so pointers move on instead of being computed anew.
+template <int D, bool KEYS>
+__device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int lane) {
   using S = TreeShape<D>;
-  using M = KeySpec<KMODE>;
-  constexpr int KB = M::B, PD = D * KB / 8;
+  constexpr int NG = KEYS ? S::NGK : S::NGV;
+  constexpr bool ROWWISE = !KEYS && S::VH > 1;  // half of each row
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
-  TreeWalk<D> ahead;
-  ahead.init(p, ctl);
-  const int count = ahead.left;
-  auto load = [&](TreeGroup<KB> (&g)[S::KP]) {
-    if (ahead.left <= 0) return;
-    int t0, valid;
-    ahead.span(p, t0, valid);
-    const PackedView& c = ahead.tail() ? p.tree : p.cache;
-    const int h = ahead.hh / (p.RB * S::VH);
-    const long long base = (static_cast<long long>(ahead.b) * p.Hkv + h) * c.t_cap + t0;
-#pragma unroll
-    for (int i = 0; i < S::KP; ++i) {
-      int token, group;
-      tree_unit<S::NGK>(i, warp4, lane, token, group);
-      const long long r = base + token;
-      if (token < valid && TQ_CHECK(t0 >= 0 && t0 + token < c.t_cap, p.err)) {
-        load_words<KB>(c.k_codes + r * PD + group * (4 * KB), g[i].w);
-        g[i].scale = __ldg(c.k_scales + r * S::NGK + group);
-        g[i].zero = __ldg(c.k_zeros + r * S::NGK + group);
-      } else {
-#pragma unroll
-        for (int k = 0; k < KB; ++k) g[i].w[k] = 0;
-        g[i].scale = g[i].zero = 0;
+  const int loaded = KEYS ? kcKLoaded : kcVLoaded, taken = KEYS ? kcKTaken : kcVTaken;
+  const int row_bytes = KEYS ? p.x_keys : p.x_values, X = KEYS ? row_bytes : row_bytes / S::VH;
+  const uint32_t ring = sm + (KEYS ? S::KR_OFF : S::VR_OFF);
+  constexpr int STAGE = KEYS ? S::KR_BYTES : S::VR_BYTES, SC = KEYS ? S::KR_SC : S::VR_SC;
+  int it = 0;
+  bool going = true;
+  // `tiles` tiles of head h from token t0 on; tokens [lo, hi) are real
+  auto part = [&](const PackedView& c, int b, int h, int half, int t0, int tiles, int lo, int hi) {
+    const long long row = (static_cast<long long>(b) * p.Hkv + h) * c.t_cap + t0;
+    const uint8_t* codes = (KEYS ? c.k_codes : c.v_codes) + row * row_bytes + half * X;
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>((KEYS ? c.k_scales : c.v_scales) + row * S::NGK + half * NG);
+    const uint8_t* zeros = reinterpret_cast<const uint8_t*>(c.k_zeros + row * S::NGK);
+    int room = static_cast<int>(min(c.t_cap - t0, static_cast<long long>(0x7fffffff)));
+#pragma unroll 1
+    for (int j = 0; j < tiles && going; ++j, ++it) {
+      const int st = it % S::NR;
+      const uint32_t bar = bars + loaded + 8 * st, dst = ring + st * STAGE;
+      if (it >= S::NR) {
+        const unsigned parity = (it / S::NR - 1) & 1;
+        going = p.bulk && !ROWWISE ? wait_or_quit(bars + taken + 8 * st, parity, quit, p.err)
+                                   : warp_wait(bars + taken + 8 * st, parity, quit, p.err);
+        if (!going) break;
       }
+      int n = min(S::TT, room);
+      if (!TQ_CHECK(t0 >= 0 && min(hi - t0, S::TT) <= room, p.err)) n = 0;
+      if (!KEYS && lane == 0)
+        *reinterpret_cast<int2*>(smem + S::VR_OFF + st * STAGE + S::VR_SPAN) =
+            make_int2(max(lo - t0, 0), min(hi - t0, S::TT));
+      if (p.bulk) {
+        if (lane == 0) {
+          mbar_expect_tx(bar, n * (X + (KEYS ? 4 : 2) * NG));
+          if (!ROWWISE && n > 0) {
+            bulk_load(dst, codes, n * X, bar);
+            bulk_load(dst + SC, scales, n * NG * 2, bar);
+            if constexpr (KEYS) bulk_load(dst + S::KR_ZP, zeros, n * NG * 2, bar);
+          }
+        }
+        if constexpr (ROWWISE) {
+          __syncwarp();
+          if (lane < n) {
+            bulk_load(dst + lane * X, codes + static_cast<long long>(lane) * row_bytes, X, bar);
+            bulk_load(dst + SC + lane * NG * 2, scales + lane * S::NGK * 2, NG * 2, bar);
+          }
+        }
+      } else {
+        tree_copy_rows(dst, codes, row_bytes, X, n, lane);
+        tree_copy_rows(dst + SC, scales, 2 * S::NGK, 2 * NG, n, lane);
+        if constexpr (KEYS) tree_copy_rows(dst + S::KR_ZP, zeros, 2 * NG, 2 * NG, n, lane);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      }
+      t0 += S::TT;
+      room -= S::TT;
+      codes += static_cast<long long>(S::TT) * row_bytes;
+      scales += S::TT * S::NGK * 2;
+      if constexpr (KEYS) zeros += S::TT * S::NGK * 2;
     }
-    ahead.next(p);
   };
-  auto decode = [&](int it, TreeGroup<KB> (&g)[S::KP]) -> bool {
-    const int st = it % S::KS;
-    if (it >= S::KS && !warp_wait(bars + kcKEmpty + 8 * st, (it / S::KS - 1) & 1, quit, p.err)) return false;
-#pragma unroll
-    for (int i = 0; i < S::KP; ++i) {
+  if (!p.bulk || ROWWISE || lane == 0) {
+    TreeWalk<D> w;
+    w.init(p, ctl);
+    while (w.left > 0 && going) {
+      const int n = min(w.left, w.n - w.tile), main = max(min(n, w.n_main - w.tile), 0);
+      const int h = p.HH == p.Hkv ? w.hh : w.hh / (p.RB * S::VH), half = KEYS || S::VH == 1 ? 0 : w.hh % S::VH;
+      if (main > 0) part(p.cache, w.b, h, half, (w.lo & ~15) + w.tile * S::TT, main, w.lo, w.hi);
+      if (n > main) part(p.tree, w.b, h, half, max(w.tile - w.n_main, 0) * S::TT, n - main, 0, p.N);
+      w.left -= n;
+      w.next_segment(p);
+    }
+    // the last copies land before the block ends, whatever became of its other warps
+    if (p.bulk)
+      for (int k = max(it - S::NR, 0); k < it; ++k) mbar_wait(bars + loaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
+  }
+  __syncwarp();
+}
+
+// The keys' decoding warps: tile after tile from the packed stages into the
+// key stages.
+template <int D, int KMODE>
+__device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp8, int lane) {
+  using S = TreeShape<D>;
+  using M = KeySpec<KMODE>;
+  constexpr int KB = M::B, X = D * KB / 8;
+  volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
+  const uint32_t bars = sm + S::C_OFF;
+  const int count = *reinterpret_cast<const int*>(ctl + kcCount);
+  constexpr int STEP = 8 / S::KWARPS;  // tiles from one of the warp's tiles to the next
+  const int wk = warp8 % S::KWARPS, flip = tree_flip<S::NGK>(lane);
+#pragma unroll 1
+  for (int it = warp8 / S::KWARPS; it < count; it += STEP) {
+    const int st = it % S::KS, rs = it % S::NR;
+    if (!warp_wait(bars + kcKLoaded + 8 * rs, (it / S::NR) & 1, quit, p.err)) return;
+    if (it >= S::KS && !warp_wait(bars + kcKEmpty + 8 * st, (it / S::KS - 1) & 1, quit, p.err)) return;
+    const uint32_t src = sm + S::KR_OFF + rs * S::KR_BYTES;
+#pragma unroll 1
+    for (int i = 0; i < 2 * S::KP; ++i) {
       int token, group;
-      tree_unit<S::NGK>(i, warp4, lane, token, group);
-      const float sc = __half2float(__ushort_as_half(static_cast<unsigned short>(g[i].scale)));
-      const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(g[i].zero)));
-      uint32_t o[16];
+      tree_unit<S::NGK, S::KWARPS>(i >> 1, wk, lane, token, group);
+      const int h = (i & 1) ^ flip;
+      uint32_t w[(KB + 1) / 2];
+      tree_words<KB>(src + token * X + group * (4 * KB), h, w);
+      const uint32_t at = src + (token * S::NGK + group) * 2;
+      const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at + S::KR_SC)))));
+      const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at + S::KR_ZP))));
+      uint32_t o[8];
       // RN(code + zero), RN(. * scale), bf16: the two forms of the decode
       // attention (code plus zero is exact in both: the zero point is an
       // integer)
       if constexpr (KB == 8) {
         const float z = __fsub_rn(zp, 1024.0f + (M::SIGNED ? 128.0f : 0.0f));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t w = M::SIGNED ? g[i].w[j] ^ 0x80808080u : g[i].w[j];
-          const uint32_t h01 = __byte_perm(w, 0x64646464u, 0x4140), h23 = __byte_perm(w, 0x64646464u, 0x4342);
-          const float2 a = mul2(make_float2(add_f16_f32<false>(h01, z), add_f16_f32<true>(h01, z)), f2(sc));
-          const float2 b = mul2(make_float2(add_f16_f32<false>(h23, z), add_f16_f32<true>(h23, z)), f2(sc));
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = M::SIGNED ? w[j] ^ 0x80808080u : w[j];
+          const uint32_t h01 = __byte_perm(x, 0x64646464u, 0x4140), h23 = __byte_perm(x, 0x64646464u, 0x4342);
+          const float2 a = mul2(make_float2(add_f16_f32<false>(h01, z), add_f16_f32<true>(h01, z)), sc);
+          const float2 b = mul2(make_float2(add_f16_f32<false>(h23, z), add_f16_f32<true>(h23, z)), sc);
           o[2 * j] = pack_bf16x2(a.x, a.y);
           o[2 * j + 1] = pack_bf16x2(b.x, b.y);
         }
       } else {
         const float2 z = f2(__fsub_rn(zp, kMagic));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 a = mul2(add2(make_float2(__uint_as_float(kMagicBits | unpack_code<KB>(g[i].w, 2 * j)),
-                                                 __uint_as_float(kMagicBits | unpack_code<KB>(g[i].w, 2 * j + 1))),
+        for (int j = 0; j < 8; ++j) {
+          const float2 a = mul2(add2(make_float2(__uint_as_float(kMagicBits | code_at<KB>(w, 2 * j)),
+                                                 __uint_as_float(kMagicBits | code_at<KB>(w, 2 * j + 1))),
                                      z),
-                                f2(sc));
+                                sc);
           o[j] = pack_bf16x2(a.x, a.y);
         }
       }
-      tree_store_group<S::TT>(sm + st * S::K_BYTES, token, group, o);
+      tree_store_half<S::TT>(sm + st * S::K_BYTES, token, group, h, o);
     }
     fence_proxy_async();
-    warp_arrive(bars + kcKFull + 8 * st, lane);
-    return true;
-  };
-  TreeGroup<KB> a[S::KP], b[S::KP];
-  load(a);
-  load(b);
-  for (int it = 0; it < count; it += 2) {
-    if (!decode(it, a)) return;
-    load(a);
-    if (it + 1 >= count || !decode(it + 1, b)) return;
-    load(b);
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bars + kcKFull + 8 * st);
+      mbar_arrive(bars + kcKTaken + 8 * rs);
+    }
   }
 }
 
-// The values' warps. A group whose scale is infinite or NaN is decoded as
-// zeros and its token marked: the softmax warps make NaN every row that
-// attends to it, and the matrix product never meets a non-finite value that a
-// row with weight zero would turn into NaN.
+// The values' decoding warps. Tokens outside the sequence are decoded as zeros,
+// and so is a group whose scale is infinite or NaN, whose token is marked: the
+// softmax warps make NaN every row that attends to it, and the matrix product
+// never meets a non-finite value that a row with weight zero would turn into
+// NaN.
 template <int D, int VB>
-__device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int warp4, int lane) {
+__device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int warp8, int lane) {
   using S = TreeShape<D>;
   using VT = ValueTable<VB>;
-  constexpr int PD = D * VB / 8;
+  constexpr int X = S::DV * VB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const uint8_t* tab = smem + S::T_OFF;
   const uint32_t vlane = VT::PAIRS ? 8u * (lane & 15) : 4u * lane;  // the lane's copy of the table
-  TreeWalk<D> ahead;
-  ahead.init(p, ctl);
-  const int count = ahead.left;
-  auto load = [&](TreeGroup<VB> (&g)[S::VP]) {
-    if (ahead.left <= 0) return;
-    int t0, valid;
-    ahead.span(p, t0, valid);
-    const PackedView& c = ahead.tail() ? p.tree : p.cache;
-    const int h = ahead.hh / (p.RB * S::VH), half = ahead.hh % S::VH;
-    const long long base = (static_cast<long long>(ahead.b) * p.Hkv + h) * c.t_cap + t0;
-#pragma unroll
-    for (int i = 0; i < S::VP; ++i) {
-      int token, group;
-      tree_unit<S::NGV>(i, warp4, lane, token, group);
-      const long long r = base + token;
-      if (token < valid && TQ_CHECK(t0 >= 0 && t0 + token < c.t_cap, p.err)) {
-        load_words<VB>(c.v_codes + r * PD + (half * S::NGV + group) * (4 * VB), g[i].w);
-        g[i].scale = __ldg(c.v_scales + r * S::NGK + half * S::NGV + group);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VB; ++k) g[i].w[k] = 0;
-        g[i].scale = 0;
-      }
-    }
-    ahead.next(p);
-  };
-  auto decode = [&](int it, TreeGroup<VB> (&g)[S::VP]) -> bool {
-    const int st = it % S::VS;
-    if (it >= S::VS && !warp_wait(bars + kcVEmpty + 8 * st, (it / S::VS - 1) & 1, quit, p.err)) return false;
+  const uint32_t vstride = p.vtab_stride;
+  const int count = *reinterpret_cast<const int*>(ctl + kcCount);
+  const int wv = warp8 % S::VWARPS, flip = tree_flip<S::NGV>(lane);
+#pragma unroll 1
+  for (int it = warp8 / S::VWARPS; it < count; it += 8 / S::VWARPS) {
+    const int st = it % S::VS, rs = it % S::NR;
+    if (!warp_wait(bars + kcVLoaded + 8 * rs, (it / S::NR) & 1, quit, p.err)) return;
+    if (it >= S::VS && !warp_wait(bars + kcVEmpty + 8 * st, (it / S::VS - 1) & 1, quit, p.err)) return;
+    const uint32_t src = sm + S::VR_OFF + rs * S::VR_BYTES;
+    const uint2 span = lds64(src + S::VR_SPAN);
     unsigned long long bad = 0;
-#pragma unroll
-    for (int i = 0; i < S::VP; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < 2 * S::VP; ++i) {
       int token, group;
-      tree_unit<S::NGV>(i, warp4, lane, token, group);
-      if ((g[i].scale & 0x7c00u) == 0x7c00u) {
+      tree_unit<S::NGV, S::VWARPS>(i >> 1, wv, lane, token, group);
+      const int h = (i & 1) ^ flip;
+      uint32_t w[(VB + 1) / 2];
+      tree_words<VB>(src + token * X + group * (4 * VB), h, w);
+      uint32_t bits = lds16(src + S::VR_SC + (token * S::NGV + group) * 2);
+      if (token < static_cast<int>(span.x) || token >= static_cast<int>(span.y)) bits = 0;
+      if ((bits & 0x7c00u) == 0x7c00u) {
         bad |= 1ull << token;
-        g[i].scale = 0;
+        bits = 0;
       }
-      const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(g[i].scale))));
-      uint32_t o[16];
+      const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(bits))));
+      uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; ++j) {
         float2 cc;
-        if constexpr (VT::PAIRS) {
-          cc = *reinterpret_cast<const float2*>(tab + field_addr<2 * VB, 7>(g[i].w, 2 * j * VB, vlane));
+        if constexpr (VB == 4) {
+          cc = *reinterpret_cast<const float2*>(tab + byte_field_addr(w, j, vstride, vlane));
+        } else if constexpr (VT::PAIRS) {
+          cc = *reinterpret_cast<const float2*>(tab + field_addr<2 * VB, 7>(w, 2 * j * VB, vlane));
+        } else if constexpr (VB == 8) {
+          cc = make_float2(*reinterpret_cast<const float*>(tab + byte_field_addr(w, 2 * j, vstride, vlane)),
+                           *reinterpret_cast<const float*>(tab + byte_field_addr(w, 2 * j + 1, vstride, vlane)));
         } else {
-          cc = make_float2(*reinterpret_cast<const float*>(tab + field_addr<VB, 7>(g[i].w, 2 * j * VB, vlane)),
-                           *reinterpret_cast<const float*>(tab + field_addr<VB, 7>(g[i].w, (2 * j + 1) * VB, vlane)));
+          cc = make_float2(*reinterpret_cast<const float*>(tab + field_addr<VB, 7>(w, 2 * j * VB, vlane)),
+                           *reinterpret_cast<const float*>(tab + field_addr<VB, 7>(w, (2 * j + 1) * VB, vlane)));
         }
         const float2 x = mul2(cc, sc);
         o[j] = pack_bf16x2(x.x, x.y);
       }
-      tree_store_group<S::TT>(sm + S::V_OFF + st * S::V_BYTES, token, group, o);
+      tree_store_half<S::TT>(sm + S::V_OFF + st * S::V_BYTES, token, group, h, o);
     }
     uint2 marks = make_uint2(0u, 0u);
     if (__any_sync(kFull, bad != 0)) {
+      *reinterpret_cast<volatile int*>(ctl + kcAnyBad) = 1;
       marks.x = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
       marks.y = __reduce_or_sync(kFull, static_cast<unsigned>(bad >> 32));
     }
-    if (lane == 0) *reinterpret_cast<uint2*>(ctl + kcBad + (it & 3) * 32 + warp4 * 8) = marks;
+    if (lane == 0) *reinterpret_cast<uint2*>(ctl + kcBad + (it & 3) * 32 + wv * 8) = marks;
     fence_proxy_async();
-    warp_arrive(bars + kcVFull + 8 * st, lane);
-    return true;
-  };
-  TreeGroup<VB> a[S::VP], b[S::VP];
-  load(a);
-  load(b);
-  for (int it = 0; it < count; it += 2) {
-    if (!decode(it, a)) return;
-    load(a);
-    if (it + 1 >= count || !decode(it + 1, b)) return;
-    load(b);
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bars + kcVFull + 8 * st);
+      mbar_arrive(bars + kcVTaken + 8 * rs);
+    }
   }
 }
 
-// The matrix warp's one thread: S = Q K^T of the next tile, then O += P V of
-// the one before.
+// The scores' thread: S = Q K^T, tile after tile.
 template <int D>
-__device__ void tree_matrix(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
+__device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
   using S = TreeShape<D>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem);
-  const uint32_t kind_qk = mma_kind(S::TT, false, p.negate != 0);
-  constexpr uint32_t kind_pv = mma_kind(S::DV, true, false);
+  const uint32_t kind = mma_kind(S::TT, false, p.negate != 0);
   TreeWalk<D> w;
   w.init(p, ctl);
-  auto wait = [&](int bar, unsigned parity) { return wait_or_quit(bars + bar, parity, quit, p.err); };
-  auto weigh = [&](int it, bool first) -> bool {  // O += P V of tile it
-    const int st = it % S::VS;
-    if (!wait(kcPFull, it & 1) || !wait(kcVFull + 8 * st, (it / S::VS) & 1)) return false;
-    tmem_fence_after();
-    const uint32_t v = sm + S::V_OFF + st * S::V_BYTES;
-#pragma unroll
-    for (int ks = 0; ks < S::TT / 16; ++ks) {
-      const uint64_t b = smem_operand(v + ks * 2048, S::TT * 128, 1024);
-      mma_ts(tm + S::O_COL, tm + S::PH_COL + 8 * ks, b, kind_pv, !first || ks > 0);
-      mma_ts(tm + S::O_COL, tm + S::PL_COL + 8 * ks, b, kind_pv, true);
-    }
-    mma_commit(bars + kcVEmpty + 8 * st);
-    mma_commit(bars + kcPFree);
-    return true;
-  };
   int it = 0;
   for (unsigned seg = 0; w.left > 0; ++seg) {
-    const int n = min(w.left, w.n - w.tile);
-    if (!wait(kcQFull, seg & 1)) return;
-    for (int j = 0; j < n; ++j, ++it) {
-      const int st = it % S::KS;
-      if (!wait(kcKFull + 8 * st, (it / S::KS) & 1) || (it > 0 && !wait(kcSFree, (it - 1) & 1))) return;
+    const int end = it + min(w.left, w.n - w.tile);
+    w.left -= end - it;
+    w.next_segment(p);
+    if (!wait_or_quit(bars + kcQFull, seg & 1, quit, p.err)) return;
+#pragma unroll 1
+    for (; it < end; ++it) {
+      const int st = it % S::KS, sb = it % S::NS;
+      const uint64_t k0 = smem_operand(sm + st * S::K_BYTES, 16, 1024);
+      if (it >= S::NS && !wait_or_quit(bars + kcSFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
+      if (!wait_or_quit(bars + kcKFull + 8 * st, (it / S::KS) & 1, quit, p.err)) return;
       tmem_fence_after();
-      const uint32_t k = sm + st * S::K_BYTES;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        const uint64_t b = smem_operand(k + (ks >> 2) * (S::TT * 128) + (ks & 3) * 32, 16, 1024);
-        if constexpr (S::Q_TMEM) mma_ts(tm + S::S_COL, tm + S::Q_COL + 8 * ks, b, kind_qk, ks > 0);
+        // (operand addresses count 16 bytes)
+        const uint64_t b = k0 + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16;
+        if (ks < S::QT / 16) mma_ts(tm + S::S_COL + sb * S::TT, tm + S::Q_COL + 8 * ks, b, kind, ks > 0);
         else
-          mma_ss(tm + S::S_COL, smem_operand(sm + S::Q_OFF + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024), b,
-                 kind_qk, ks > 0);
+          mma_ss(tm + S::S_COL + sb * S::TT,
+                 smem_operand(sm + S::Q_OFF, 16, 1024) +
+                     (((ks - S::QT / 16) >> 2) * (128 * 128) + (ks & 3) * 32) / 16,
+                 b, kind, true);
       }
+      mma_commit(bars + kcSFull + 8 * sb);
       mma_commit(bars + kcKEmpty + 8 * st);
-      mma_commit(bars + kcSFull);
-      if (j > 0 && !weigh(it - 1, j == 1)) return;
     }
-    if (!weigh(it - 1, n == 1)) return;
-    w.left -= n;
-    w.next_segment(p);
   }
+}
+
+// The weighted values' thread: O += P V, the weights as a high and a low part.
+template <int D>
+__device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
+  using S = TreeShape<D>;
+  volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
+  const uint32_t bars = sm + S::C_OFF;
+  const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem);
+  constexpr uint32_t kind = mma_kind(S::DV, true, false);
+  TreeWalk<D> w;
+  w.init(p, ctl);
+  int it = 0;
+  while (w.left > 0) {
+    const int begin = it, end = it + min(w.left, w.n - w.tile);
+    w.left -= end - it;
+    w.next_segment(p);
+#pragma unroll 1
+    for (; it < end; ++it) {
+      const int st = it % S::VS, sb = it % S::NS;
+      const uint64_t v0 = smem_operand(sm + S::V_OFF + st * S::V_BYTES, S::TT * 128, 1024);
+      const uint32_t pc = tm + S::P_COL + sb * S::TT;
+      if (!wait_or_quit(bars + kcVFull + 8 * st, (it / S::VS) & 1, quit, p.err)) return;
+      if (!wait_or_quit(bars + kcPFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
+      tmem_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < S::TT / 16; ++ks) {
+        mma_ts(tm + S::O_COL, pc + 8 * ks, v0 + ks * 128, kind, it > begin || ks > 0);
+        mma_ts(tm + S::O_COL, pc + S::TT / 2 + 8 * ks, v0 + ks * 128, kind, true);
+      }
+      mma_commit(bars + kcPFree + 8 * sb);
+      mma_commit(bars + kcVEmpty + 8 * st);
+    }
+  }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // The softmax warps: a thread holds one lane of tensor memory, i.e. one query
 // row over its copy's share of each tile's tokens.
-template <int D, int COPIES>
-__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int warp, int lane) {
+template <int D>
+__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp, int lane) {
   using S = TreeShape<D>;
   constexpr int TT = S::TT;
-  constexpr int W = TT / COPIES;       // tokens of a tile that this lane takes
-  constexpr int QUADS = 4 / COPIES;    // warps per copy
+  const int W = TT / p.copies;         // tokens of a tile that this lane takes: 16, 32 or 64
+  const int QUADS = 4 / p.copies;      // warps per copy
   const float kNegInf = -__int_as_float(0x7f800000);
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
@@ -411,7 +566,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = 0;
 #pragma unroll
-    for (int c = 0; c < TT; c += 16) tmem_st16(tm + S::PH_COL + c, z);
+    for (int c = 0; c < S::NS * TT; c += 16) tmem_st16(tm + S::P_COL + c, z);
     tmem_wait_st();
   }
   TreeWalk<D> w;
@@ -434,134 +589,150 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     {
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + ((static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N + (row ? r : 0)) * D);
-      if constexpr (S::Q_TMEM) {
+#pragma unroll 1
+      for (int c = 0; c < S::QT / 2; c += 16) {
+        uint32_t x[16];
 #pragma unroll
-        for (int c = 0; c < D / 2; c += 16) {
-          uint32_t x[16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 u = row ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
-            x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
-          }
-          tmem_st16(tm + S::Q_COL + c, x);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = row ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+          x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
         }
-        tmem_wait_st();
-        tmem_fence_before();
-      } else {
+        tmem_st16(tm + S::Q_COL + c, x);
+      }
+      if constexpr (S::QT < D) {
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 u = row ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          sts128(sm + S::Q_OFF + (c >> 3) * (128 * 128) + rl * 128 + (((c & 7) ^ (rl & 7)) << 4), u.x, u.y, u.z, u.w);
+        for (int c = 0; c < (D - S::QT) / 8; ++c) {
+          const uint4 u = row ? __ldg(src + S::QT / 8 + c) : make_uint4(0u, 0u, 0u, 0u);
+          sts128(sm + S::Q_OFF + (c >> 3) * (128 * 128) + (warp * 32 + lane) * 128 + (((c ^ lane) & 7) << 4), u.x, u.y,
+                 u.z, u.w);
         }
         fence_proxy_async();
       }
+      tmem_wait_st();
+      tmem_fence_before();
       warp_arrive(bars + kcQFull, lane);
     }
     float m = kNegInf, l = 0.0f;
-    unsigned long long seen = 0, last_seen = 0;  // tokens of this and of the last tile that the row attends to
-    // a marked token (a value group with a non-finite scale) among them makes the row NaN
-    auto spoil = [&](int tile_it, unsigned long long attended) {
+    // which of a tile's tokens the row attends to
+    auto attended = [&](int tile) -> unsigned long long {
+      TreeWalk<D> x = w;
+      x.tile = tile;
+      int t0, first, end;
+      x.span(p, t0, first, end);
+      unsigned long long a = anc == 0 ? 0ull : x.tail() ? anc >> t0 : ~0ull << first;
+      if (end < 64) a &= (1ull << end) - 1ull;
+      return a;
+    };
+    // a marked token (a value group with a non-finite scale) that it attends to makes the row NaN
+    auto spoil = [&](int tile_it) {
       unsigned long long bad = 0;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         const uint2 u = lds64(bars + kcBad + (tile_it & 3) * 32 + 8 * i);
         bad |= static_cast<unsigned long long>(u.y) << 32 | u.x;
       }
-      if (bad & attended) l = __int_as_float(0x7fc00000);
+      if (bad & attended(w.tile + (tile_it - it))) l = __int_as_float(0x7fc00000);
     };
-    for (int j = 0; j < n; ++j, ++it) {
-      int t0, valid;
-      w.span(p, t0, valid);
-      last_seen = seen;
-      seen = !row || anc == 0 ? 0ull : w.tail() ? anc >> t0 : ~0ull;
-      if (valid < 64) seen &= (1ull << valid) - 1ull;
-      --w.left;
-      ++w.tile;
-      if (!warp_wait(bars + kcSFull, it & 1, quit, p.err)) return;
-      uint32_t s[W];
-      if (work) {
-        tmem_fence_after();
-        if constexpr (W >= 32) {
-#pragma unroll
-          for (int c = 0; c < W; c += 32) tmem_ld32(tm + S::S_COL + col0 + c, s + c);
-        } else {
-          tmem_ld16(tm + S::S_COL + col0, s);
-        }
-        tmem_wait_ld();
-        tmem_fence_before();
-      }
-      warp_arrive(bars + kcSFree, lane);
-      float mt = kNegInf;
-      if (work) {
-        // rows without a token here are ignored, so only a row that some
-        // tokens of the tile are hidden from needs the mask
-        const unsigned long long mine = (W == 64 ? ~0ull : (1ull << (W & 63)) - 1ull) << col0;
-        if (__any_sync(kFull, row && anc != 0 && (seen & mine) != mine)) {
-          const unsigned long long own = seen >> col0;
-#pragma unroll
-          for (int c = 0; c < W; ++c)
-            s[c] = (own >> c & 1) ? s[c] : 0xff800000u;
-        }
-        float m4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(s[c]);
-#pragma unroll
-        for (int c = 4; c < W; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(s[c]));
-        mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        mt = mt == kNegInf ? mt : __fmul_rn(mt, p.scale_log2);
-      }
-      // the reference maximum moves only when a weight would pass 2^8
-      const bool raise = mt > m + 8.0f || (m == kNegInf && mt > m);
-      const bool raised = __any_sync(kFull, raise);
-      if (it > 0 && !warp_wait(bars + kcPFree, (it - 1) & 1, quit, p.err)) return;
-      if (work) {
-        tmem_fence_after();
-        if (j > 0) spoil(it - 1, last_seen);
-        if (raised) {
-          const float f = raise ? fast_exp2(__fsub_rn(m, mt)) : 1.0f;
-          if (raise) m = mt;
-          l = __fmul_rn(l, f);
-          if (j > 0) {
 #pragma unroll 1
-            for (int c = 0; c < S::DV; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tm + S::O_COL + c, o);
-              tmem_wait_ld();
+    for (int j = 0; j < n; ++j, ++it, ++w.tile) {
+      const int sb = it % S::NS;
+      const uint32_t sc = tm + S::S_COL + sb * TT + col0, pc = tm + S::P_COL + sb * TT + col0 / 2;
+      if (!warp_wait(bars + kcSFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
+      bool raised = false;
+      float f = 1.0f;
+      if (work) {
+        tmem_fence_after();
+        // hidden tokens (a tile at an end of the sequence, the tree): their
+        // scores become -inf in place
+        if (w.tile >= w.n_main - 1 || (w.tile == 0 && (w.lo & 15) != 0)) {
+          unsigned long long own = attended(w.tile) >> col0;
+#pragma unroll 1
+          for (int c = 0; c < W; c += 16, own >>= 16) {
+            uint32_t s[16];
+            tmem_ld16(sc + c, s);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
-              tmem_st32(tm + S::O_COL + c, o);
-            }
+            for (int i = 0; i < 16; ++i) s[i] = (static_cast<uint32_t>(own) >> i & 1) ? s[i] : 0xff800000u;
+            tmem_st16(sc + c, s);
           }
+          tmem_wait_st();
         }
-        const float ref = m == kNegInf ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
+        float m2[2] = {kNegInf, kNegInf};
+#pragma unroll 1
         for (int c = 0; c < W; c += 16) {
-          // the weights as bf16 high part plus bf16 remainder: 2^-18 exact
-          uint32_t hi[8], lo[8];
+          uint32_t s[16];
+          tmem_ld16(sc + c, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 2)
+            m2[(i >> 1) & 1] = max3(m2[(i >> 1) & 1], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+        }
+        float mt = fmaxf(m2[0], m2[1]);
+        mt = mt == kNegInf ? mt : __fmul_rn(mt, p.scale_log2);
+        // the reference maximum moves only when a weight would pass 2^8
+        const bool raise = mt > m + 8.0f || (m == kNegInf && mt > m);
+        raised = __any_sync(kFull, raise);
+        if (raise) {
+          f = fast_exp2(__fsub_rn(m, mt));
+          m = mt;
+        }
+      }
+      // the weights' buffer is free: the tile NS before is weighed
+      if (it >= S::NS && !warp_wait(bars + kcPFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
+      if (*reinterpret_cast<volatile int*>(ctl + kcAnyBad) != 0 && j >= S::NS) spoil(it - S::NS);
+      if (raised && j > 0) {
+        if (S::NS > 1 && !warp_wait(bars + kcPFree + 8 * ((it - 1) % S::NS), ((it - 1) / S::NS) & 1, quit, p.err)) return;
+        tmem_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < S::DV; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(tm + S::O_COL + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
+          tmem_st16(tm + S::O_COL + c, o);
+        }
+      }
+      if (work) {
+        tmem_fence_after();
+        const float ref = m == kNegInf ? 0.0f : m;
+        const float2 minus = f2(-ref), by = f2(p.scale_log2);
+        float2 sum[2] = {f2(0.0f), f2(0.0f)};
+        // the weights as a bf16 high part plus a bf16 remainder: exact to 2^-18
+#pragma unroll 1
+        for (int c = 0; c < W; c += 16) {
+          uint32_t s[16], hi[8], lo[8];
+          tmem_ld16(sc + c, s);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float a = fast_exp2(__fmaf_rn(__uint_as_float(s[c + 2 * i]), p.scale_log2, -ref));
-            const float b = fast_exp2(__fmaf_rn(__uint_as_float(s[c + 2 * i + 1]), p.scale_log2, -ref));
-            sum[(2 * i) & 3] = __fadd_rn(sum[(2 * i) & 3], a);
-            sum[(2 * i + 1) & 3] = __fadd_rn(sum[(2 * i + 1) & 3], b);
-            hi[i] = pack_bf16x2(a, b);
-            lo[i] = pack_bf16x2(__fsub_rn(a, bf16_lo(hi[i])), __fsub_rn(b, bf16_hi(hi[i])));
+            const float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), by, minus);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum[i & 1] = add2(sum[i & 1], e);
+            hi[i] = pack_bf16x2(e.x, e.y);
+            const float2 rest = sub2(e, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
+            lo[i] = pack_bf16x2(rest.x, rest.y);
           }
-          tmem_st8(tm + S::PH_COL + (col0 + c) / 2, hi);
-          tmem_st8(tm + S::PL_COL + (col0 + c) / 2, lo);
+          tmem_st8(pc + c / 2, hi);
+          tmem_st8(pc + TT / 2 + c / 2, lo);
         }
-        l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])));
+        l = __fmaf_rn(l, f, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
         tmem_wait_st();
         tmem_fence_before();
       }
-      warp_arrive(bars + kcPFull, lane);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + kcSFree + 8 * sb);
+        mbar_arrive(bars + kcPFull + 8 * sb);
+      }
     }
+    w.left -= n;
     // ---- the segment's record
-    if (!warp_wait(bars + kcPFree, (it - 1) & 1, quit, p.err)) return;
+    if (!warp_wait(bars + kcPFree + 8 * ((it - 1) % S::NS), ((it - 1) / S::NS) & 1, quit, p.err)) return;
     if (work) {
       tmem_fence_after();
-      spoil(it - 1, seen);
+      if (*reinterpret_cast<volatile int*>(ctl + kcAnyBad) != 0)
+        for (int k = 1; k <= min(n, S::NS); ++k) spoil(it - k);
       const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(w.b) * p.HH + w.hh;
       float* rec = p.recs + slot * p.slots * (S::DV + 2);
       const bool store = row && TQ_CHECK(slot < p.n_recs, p.err);
@@ -573,13 +744,13 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
       }
       float4* dst = reinterpret_cast<float4*>(rec + 2 * p.slots + static_cast<long long>(at) * S::DV);
 #pragma unroll 1
-      for (int c = 0; c < S::DV; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tm + S::O_COL + c, o);
+      for (int c = 0; c < S::DV; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tm + S::O_COL + c, o);
         tmem_wait_ld();
         if (store) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 4; ++i)
             dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
@@ -606,21 +777,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
     case 5: fill_value_table<5>(smem + S::T_OFF); break;
     default: fill_value_table<8>(smem + S::T_OFF); break;
   }
-  if (warp == 12) tmem_alloc(bars + kcTmem, 512);
+  if (warp == 20) tmem_alloc(bars + kcTmem, 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + kcKFull + 8 * i, 4);
+      mbar_init(bars + kcKFull + 8 * i, S::KWARPS);
       mbar_init(bars + kcKEmpty + 8 * i, 1);
-      mbar_init(bars + kcVFull + 8 * i, 4);
+      mbar_init(bars + kcVFull + 8 * i, S::VWARPS);
       mbar_init(bars + kcVEmpty + 8 * i, 1);
+      mbar_init(bars + kcSFull + 8 * i, 1);
+      mbar_init(bars + kcSFree + 8 * i, 4);
+      mbar_init(bars + kcPFull + 8 * i, 4);
+      mbar_init(bars + kcPFree + 8 * i, 1);
+      mbar_init(bars + kcDrain + 8 * i, 1);
     }
-    mbar_init(bars + kcSFull, 1);
-    mbar_init(bars + kcSFree, 4);
-    mbar_init(bars + kcPFull, 4);
-    mbar_init(bars + kcPFree, 1);
     mbar_init(bars + kcQFull, 4);
-    mbar_init(bars + kcDrain, 1);
+    for (int i = 0; i < S::NR; ++i) {
+      mbar_init(bars + kcKLoaded + 8 * i, 1);
+      mbar_init(bars + kcKTaken + 8 * i, S::KWARPS);
+      mbar_init(bars + kcVLoaded + 8 * i, 1);
+      mbar_init(bars + kcVTaken + 8 * i, S::VWARPS);
+    }
     *reinterpret_cast<int*>(ctl + kcQuit) = 0;
+    *reinterpret_cast<int*>(ctl + kcAnyBad) = 0;
     mbar_fence_init();
   }
   pdl_launch_dependents();
@@ -628,9 +806,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
   if (warp == 0) {
     // the block's range of the line of all tiles: 32 batch rows at a time
     long long total = 0;
-    int lo, hi;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      long long c = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane, lo, hi) : 0;
+      long long c = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
         const long long y = __shfl_up_sync(kFull, c, x);
@@ -649,7 +826,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
     long long before = 0;
     bool found = false;
     for (int b0 = 0; b0 < p.B && !found && first < end; b0 += 32) {
-      const int n = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane, lo, hi) : 0;
+      const int n = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
       long long c = n;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
@@ -670,39 +847,49 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  // registers: 128 (40 + 4 * 72 + 152) = the launch's 768 * 80
   if (warp < 4) {
-    switch (p.copies) {
-      case 1: tree_softmax<D, 1>(p, sm, smem, ctl, warp, lane); break;
-      case 2: if constexpr (D != 512) tree_softmax<D, 2>(p, sm, smem, ctl, warp, lane); break;
-      default: if constexpr (D != 512) tree_softmax<D, 4>(p, sm, smem, ctl, warp, lane); break;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    tree_softmax<D>(p, sm, ctl, warp, lane);
+  } else if (warp < 20) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const int warp8 = (warp - 4) / 4 * 2 + (warp & 1);
+    if ((warp & 2) == 0) {
+      switch (p.kmode) {
+        case kK2: tree_decode_keys<D, kK2>(p, sm, ctl, warp8, lane); break;
+        case kK4: tree_decode_keys<D, kK4>(p, sm, ctl, warp8, lane); break;
+        case kK5: tree_decode_keys<D, kK5>(p, sm, ctl, warp8, lane); break;
+        case kK8: tree_decode_keys<D, kK8>(p, sm, ctl, warp8, lane); break;
+        default: tree_decode_keys<D, kK8Signed>(p, sm, ctl, warp8, lane); break;
+      }
+    } else {
+      switch (p.vb) {
+        case 2: tree_decode_values<D, 2>(p, sm, smem, ctl, warp8, lane); break;
+        case 3: tree_decode_values<D, 3>(p, sm, smem, ctl, warp8, lane); break;
+        case 4: tree_decode_values<D, 4>(p, sm, smem, ctl, warp8, lane); break;
+        case 5: tree_decode_values<D, 5>(p, sm, smem, ctl, warp8, lane); break;
+        default: tree_decode_values<D, 8>(p, sm, smem, ctl, warp8, lane); break;
+      }
     }
-  } else if (warp < 8) {
-    switch (p.kmode) {
-      case kK2: tree_decode_keys<D, kK2>(p, sm, ctl, warp - 4, lane); break;
-      case kK4: tree_decode_keys<D, kK4>(p, sm, ctl, warp - 4, lane); break;
-      case kK5: tree_decode_keys<D, kK5>(p, sm, ctl, warp - 4, lane); break;
-      case kK8: tree_decode_keys<D, kK8>(p, sm, ctl, warp - 4, lane); break;
-      default: tree_decode_keys<D, kK8Signed>(p, sm, ctl, warp - 4, lane); break;
-    }
-  } else if (warp < 12) {
-    switch (p.vb) {
-      case 2: tree_decode_values<D, 2>(p, sm, smem, ctl, warp - 8, lane); break;
-      case 3: tree_decode_values<D, 3>(p, sm, smem, ctl, warp - 8, lane); break;
-      case 4: tree_decode_values<D, 4>(p, sm, smem, ctl, warp - 8, lane); break;
-      case 5: tree_decode_values<D, 5>(p, sm, smem, ctl, warp - 8, lane); break;
-      default: tree_decode_values<D, 8>(p, sm, smem, ctl, warp - 8, lane); break;
-    }
-  } else if (lane == 0) {
-    tree_matrix<D>(p, sm, ctl);
-    if (*reinterpret_cast<volatile int*>(ctl + kcQuit) != 0) {  // gave up: let the matrix work in flight end
-      mma_commit(bars + kcDrain);
-      mbar_wait(bars + kcDrain, 0, kBulkWaitLimit);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 22) {
+      tree_load<D, true>(p, sm, smem, ctl, lane);
+    } else if (warp == 23) {
+      tree_load<D, false>(p, sm, smem, ctl, lane);
+    } else if (lane == 0) {
+      if (warp == 20) tree_scores<D>(p, sm, ctl);
+      else tree_weigh<D>(p, sm, ctl);
+      if (*reinterpret_cast<volatile int*>(ctl + kcQuit) != 0) {  // gave up: let the matrix work in flight end
+        mma_commit(bars + kcDrain + 8 * (warp - 20));
+        mbar_wait(bars + kcDrain + 8 * (warp - 20), 0, kBulkWaitLimit);
+      }
     }
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_fence_after();
     tmem_free(*reinterpret_cast<const uint32_t*>(ctl + kcTmem), 512);
   }
