@@ -8,11 +8,25 @@
 namespace tq {
 
 // ---- waits ----------------------------------------------------------------------
-// A wait that gives up sets the library's device error word and *quit, which
-// ends every other wait of the block too.
+// Completion of phase `parity` of a barrier. Each try may sleep up to 20 us in
+// hardware (a poll that returns at once takes issue slots from the working
+// warps); 2^14 of them end a wait that nothing answers after a third of a
+// second, with the library's device error word set and *quit, which ends every
+// other wait of the block too.
+constexpr unsigned kTryNs = 20000, kTries = 1u << 14;
+__device__ __forceinline__ bool try_wait(uint32_t bar, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool wait_or_quit(uint32_t bar, unsigned parity, volatile int* quit, unsigned* err) {
-  for (unsigned i = 0; i < kBulkWaitLimit; i += 64) {
-    if (mbar_wait(bar, parity, 64)) return true;
+#pragma unroll 1
+  for (unsigned i = 0; i < kTries; ++i) {
+    if (try_wait(bar, parity)) return true;
     if (*quit != 0) return false;
   }
   *quit = 1;

@@ -92,27 +92,32 @@ struct TreeShape {
   static constexpr int T_OFF = VR_OFF + NR * VR_BYTES;
   static constexpr int C_OFF = T_OFF + TAB;
   static constexpr int SMEM = C_OFF + 512;
-  // tensor memory columns: O | S, NS times | P (high half, low half), NS times | Q
-  static constexpr int NS = 2;
-  static constexpr int O_COL = 0, S_COL = DV, P_COL = S_COL + NS * TT, Q_COL = P_COL + NS * TT;
+  // Tensor memory columns: SW outputs | NS score tiles | queries. The weights
+  // of 16 tokens take the place of their scores: eight columns of high parts,
+  // eight of remainders. With SW = 2 two groups of softmax warps take the tiles
+  // in turn, each with an output of its own.
+  static constexpr int SW = D <= 128 ? 2 : 1;
+  static constexpr int NS = D == 128 ? 3 : 4;
+  static constexpr int O_COL = 0, S_COL = SW * DV, Q_COL = S_COL + NS * TT;
+  static constexpr int THREADS = 640 + 128 * SW;
   static_assert(Q_COL + QT / 2 <= 512, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// Warps 0-3 softmax (tensor memory ties each to a quadrant of lanes and so to
-// one of the SM's four schedulers), 4-19 decoding, 20 scores, 21 weighted
+// Warps 0-3 (and 24-27 where SW is 2) softmax (tensor memory ties each to a
+// quadrant of lanes and so to one of the SM's four schedulers), 4-19 decoding, 20 scores, 21 weighted
 // values, 22 and 23 load packed keys and values. Instruction fetch bounds a kernel of many roles: a
 // scheduler's instruction cache holds some hundred instructions and a warp
 // that misses it waits (7 of 20 cycles an instruction with every role on every
 // scheduler and unrolled loops). So warps 4-19 decode keys on schedulers 0 and
 // 1 and values on 2 and 3, four warps to a loop, and the loops are rolled.
-constexpr int kTreeThreads = 768;
 constexpr int kTreeRows = 128;
 
 // Control words in shared memory (byte offsets).
-enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcSFree = 80, kcPFull = 96,
-             kcPFree = 112, kcQFull = 128, kcDrain = 136, kcTmem = 152, kcQuit = 156, kcTile = 160, kcB = 164,
-             kcHH = 168, kcCount = 172, kcKLoaded = 176, kcKTaken = 208, kcVLoaded = 240, kcVTaken = 272, kcAnyBad = 304, kcBad = 320 };
+enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcPFull = 96, kcPFree = 128,
+             kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcTile = 192, kcB = 196, kcHH = 200,
+             kcCount = 204, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
+             kcBad = 352 };
 
 // Tiles of the sequence of a batch row with tokens [lo, hi); they start at a
 // multiple of 16 tokens, which keeps every buffer's rows 16-byte aligned.
@@ -487,7 +492,8 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
     for (; it < end; ++it) {
       const int st = it % S::KS, sb = it % S::NS;
       const uint64_t k0 = smem_operand(sm + st * S::K_BYTES, 16, 1024);
-      if (it >= S::NS && !wait_or_quit(bars + kcSFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
+      // the weights that took the scores' place are used
+      if (it >= S::NS && !wait_or_quit(bars + kcPFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
       if (!wait_or_quit(bars + kcKFull + 8 * st, (it / S::KS) & 1, quit, p.err)) return;
       tmem_fence_after();
 #pragma unroll
@@ -526,14 +532,14 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
     for (; it < end; ++it) {
       const int st = it % S::VS, sb = it % S::NS;
       const uint64_t v0 = smem_operand(sm + S::V_OFF + st * S::V_BYTES, S::TT * 128, 1024);
-      const uint32_t pc = tm + S::P_COL + sb * S::TT;
+      const uint32_t pc = tm + S::S_COL + sb * S::TT, o = tm + S::O_COL + (it % S::SW) * S::DV;
       if (!wait_or_quit(bars + kcVFull + 8 * st, (it / S::VS) & 1, quit, p.err)) return;
       if (!wait_or_quit(bars + kcPFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
       tmem_fence_after();
 #pragma unroll
       for (int ks = 0; ks < S::TT / 16; ++ks) {
-        mma_ts(tm + S::O_COL, pc + 8 * ks, v0 + ks * 128, kind, it > begin || ks > 0);
-        mma_ts(tm + S::O_COL, pc + S::TT / 2 + 8 * ks, v0 + ks * 128, kind, true);
+        mma_ts(o, pc + 16 * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0);
+        mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind, true);
       }
       mma_commit(bars + kcPFree + 8 * sb);
       mma_commit(bars + kcVEmpty + 8 * st);
@@ -547,10 +553,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The softmax warps: a thread holds one lane of tensor memory, i.e. one query
-// row over its copy's share of each tile's tokens.
+// The softmax warps (group `which` of SW, every SW-th tile): a thread holds one
+// lane of tensor memory, i.e. one query row over its copy's share of the tokens.
 template <int D>
-__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp, int lane) {
+__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int which, int warp, int lane) {
   using S = TreeShape<D>;
   constexpr int TT = S::TT;
   const int W = TT / p.copies;         // tokens of a tile that this lane takes: 16, 32 or 64
@@ -559,19 +565,13 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem) + (static_cast<uint32_t>(warp) << 21);
+  const uint32_t oc = tm + S::O_COL + which * S::DV;
   const int copy = warp / QUADS, rl = (warp % QUADS) * 32 + lane, col0 = copy * W;
-  // weights of the other copies' tokens, and of lanes without a row: zero
-  {
-    uint32_t z[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = 0;
-#pragma unroll
-    for (int c = 0; c < S::NS * TT; c += 16) tmem_st16(tm + S::P_COL + c, z);
-    tmem_wait_st();
-  }
+  auto s_full = [&](int it) { return warp_wait(bars + kcSFull + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
+  auto weighed = [&](int it) { return warp_wait(bars + kcPFree + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
   TreeWalk<D> w;
   w.init(p, ctl);
-  int it = 0, anc_b = -1, anc_rb = -1;
+  int it0 = 0, anc_b = -1, anc_rb = -1;
   unsigned long long anc = 0;
   while (w.left > 0) {
     const int n = min(w.left, w.n - w.tile);
@@ -585,8 +585,10 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
       anc_b = w.b;
       anc_rb = rb;
     }
-    // ---- the queries of the segment
-    {
+    // ---- the queries of the segment (every score of the last one is done)
+    if (which == 0) {
+      if (it0 > 0 && !s_full(it0 - 1)) return;
+      tmem_fence_after();
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + ((static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N + (row ? r : 0)) * D);
 #pragma unroll 1
@@ -624,44 +626,47 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
       return a;
     };
     // a marked token (a value group with a non-finite scale) that it attends to makes the row NaN
-    auto spoil = [&](int tile_it) {
+    auto spoil = [&](int it, int tile) {
       unsigned long long bad = 0;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
-        const uint2 u = lds64(bars + kcBad + (tile_it & 3) * 32 + 8 * i);
+        const uint2 u = lds64(bars + kcBad + (it & 3) * 32 + 8 * i);
         bad |= static_cast<unsigned long long>(u.y) << 32 | u.x;
       }
-      if (bad & attended(w.tile + (tile_it - it))) l = __int_as_float(0x7fc00000);
+      if (bad & attended(tile)) l = __int_as_float(0x7fc00000);
     };
+    const volatile int* any_bad = reinterpret_cast<const volatile int*>(ctl + kcAnyBad);
+    const int j0 = S::SW == 1 ? 0 : (which ^ it0) & 1;  // the group's first tile of the segment
+    int j = j0;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j, ++it, ++w.tile) {
-      const int sb = it % S::NS;
-      const uint32_t sc = tm + S::S_COL + sb * TT + col0, pc = tm + S::P_COL + sb * TT + col0 / 2;
-      if (!warp_wait(bars + kcSFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
+    for (; j < n; j += S::SW) {
+      const int it = it0 + j, tile = w.tile + j;
+      const uint32_t buf = tm + S::S_COL + (it % S::NS) * TT;
+      if (!s_full(it)) return;
       bool raised = false;
       float f = 1.0f;
       if (work) {
         tmem_fence_after();
         // hidden tokens (a tile at an end of the sequence, the tree): their
         // scores become -inf in place
-        if (w.tile >= w.n_main - 1 || (w.tile == 0 && (w.lo & 15) != 0)) {
-          unsigned long long own = attended(w.tile) >> col0;
+        if (tile >= w.n_main - 1 || (tile == 0 && (w.lo & 15) != 0)) {
+          unsigned long long own = attended(tile) >> col0;
 #pragma unroll 1
-          for (int c = 0; c < W; c += 16, own >>= 16) {
+          for (int c = col0; c < col0 + W; c += 16, own >>= 16) {
             uint32_t s[16];
-            tmem_ld16(sc + c, s);
+            tmem_ld16(buf + c, s);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = (static_cast<uint32_t>(own) >> i & 1) ? s[i] : 0xff800000u;
-            tmem_st16(sc + c, s);
+            tmem_st16(buf + c, s);
           }
           tmem_wait_st();
         }
         float m2[2] = {kNegInf, kNegInf};
 #pragma unroll 1
-        for (int c = 0; c < W; c += 16) {
+        for (int c = col0; c < col0 + W; c += 16) {
           uint32_t s[16];
-          tmem_ld16(sc + c, s);
+          tmem_ld16(buf + c, s);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; i += 2)
@@ -676,93 +681,96 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
           f = fast_exp2(__fsub_rn(m, mt));
           m = mt;
         }
-      }
-      // the weights' buffer is free: the tile NS before is weighed
-      if (it >= S::NS && !warp_wait(bars + kcPFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
-      if (*reinterpret_cast<volatile int*>(ctl + kcAnyBad) != 0 && j >= S::NS) spoil(it - S::NS);
-      if (raised && j > 0) {
-        if (S::NS > 1 && !warp_wait(bars + kcPFree + 8 * ((it - 1) % S::NS), ((it - 1) / S::NS) & 1, quit, p.err)) return;
-        tmem_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < S::DV; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(tm + S::O_COL + c, o);
-          tmem_wait_ld();
+        // the weights of the other copies' tokens are zero
+        uint32_t z[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
-          tmem_st16(tm + S::O_COL + c, o);
-        }
-      }
-      if (work) {
-        tmem_fence_after();
+        for (int i = 0; i < 16; ++i) z[i] = 0;
+#pragma unroll 1
+        for (int c = 0; c < TT; c += 16)
+          if (c < col0 || c >= col0 + W) tmem_st16(buf + c, z);
         const float ref = m == kNegInf ? 0.0f : m;
         const float2 minus = f2(-ref), by = f2(p.scale_log2);
         float2 sum[2] = {f2(0.0f), f2(0.0f)};
         // the weights as a bf16 high part plus a bf16 remainder: exact to 2^-18
 #pragma unroll 1
-        for (int c = 0; c < W; c += 16) {
-          uint32_t s[16], hi[8], lo[8];
-          tmem_ld16(sc + c, s);
+        for (int c = col0; c < col0 + W; c += 16) {
+          uint32_t s[16], x[16];
+          tmem_ld16(buf + c, s);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), by, minus);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            const float2 y = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), by, minus);
+            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             sum[i & 1] = add2(sum[i & 1], e);
-            hi[i] = pack_bf16x2(e.x, e.y);
-            const float2 rest = sub2(e, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
-            lo[i] = pack_bf16x2(rest.x, rest.y);
+            x[i] = pack_bf16x2(e.x, e.y);
+            const float2 rest = sub2(e, make_float2(bf16_lo(x[i]), bf16_hi(x[i])));
+            x[8 + i] = pack_bf16x2(rest.x, rest.y);
           }
-          tmem_st8(pc + c / 2, hi);
-          tmem_st8(pc + TT / 2 + c / 2, lo);
+          tmem_st16(buf + c, x);
         }
         l = __fmaf_rn(l, f, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
-        tmem_wait_st();
-        tmem_fence_before();
       }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + kcSFree + 8 * sb);
-        mbar_arrive(bars + kcPFull + 8 * sb);
+      if (j > j0) {  // the group's last tile is weighed
+        if (!weighed(it - S::SW)) return;
+        if (*any_bad != 0) spoil(it - S::SW, tile - S::SW);
+        if (raised) {
+          tmem_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < S::DV; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(oc + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
+            tmem_st16(oc + c, o);
+          }
+        }
       }
+      tmem_wait_st();
+      tmem_fence_before();
+      warp_arrive(bars + kcPFull + 8 * (it % S::NS), lane);
     }
-    w.left -= n;
     // ---- the segment's record
-    if (!warp_wait(bars + kcPFree + 8 * ((it - 1) % S::NS), ((it - 1) / S::NS) & 1, quit, p.err)) return;
+    if (j > j0) {
+      if (!weighed(it0 + j - S::SW)) return;
+      if (*any_bad != 0) spoil(it0 + j - S::SW, w.tile + j - S::SW);
+    }
     if (work) {
       tmem_fence_after();
-      if (*reinterpret_cast<volatile int*>(ctl + kcAnyBad) != 0)
-        for (int k = 1; k <= min(n, S::NS); ++k) spoil(it - k);
       const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(w.b) * p.HH + w.hh;
       float* rec = p.recs + slot * p.slots * (S::DV + 2);
       const bool store = row && TQ_CHECK(slot < p.n_recs, p.err);
-      const int at = copy * p.rows + rl;
+      const int at = (which * p.copies + copy) * p.rows + rl;
       if (store) {
         // a NaN row keeps a finite maximum, so that the combine takes it
         rec[at] = anc == 0 ? kNegInf : l != l ? 0.0f : m;
         rec[p.slots + at] = anc == 0 ? 0.0f : l;
       }
-      float4* dst = reinterpret_cast<float4*>(rec + 2 * p.slots + static_cast<long long>(at) * S::DV);
+      if (j > j0) {
+        float4* dst = reinterpret_cast<float4*>(rec + 2 * p.slots + static_cast<long long>(at) * S::DV);
 #pragma unroll 1
-      for (int c = 0; c < S::DV; c += 16) {
-        uint32_t o[16];
-        tmem_ld16(tm + S::O_COL + c, o);
-        tmem_wait_ld();
-        if (store) {
+        for (int c = 0; c < S::DV; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(oc + c, o);
+          tmem_wait_ld();
+          if (store) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            for (int i = 0; i < 4; ++i)
+              dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          }
         }
       }
       tmem_fence_before();
     }
+    it0 += n;
+    w.left -= n;
     w.next_segment(p);
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(const __grid_constant__ TreeParams p) {
   using S = TreeShape<D>;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* smem = tree_smem;
@@ -784,13 +792,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
       mbar_init(bars + kcKEmpty + 8 * i, 1);
       mbar_init(bars + kcVFull + 8 * i, S::VWARPS);
       mbar_init(bars + kcVEmpty + 8 * i, 1);
-      mbar_init(bars + kcSFull + 8 * i, 1);
-      mbar_init(bars + kcSFree + 8 * i, 4);
-      mbar_init(bars + kcPFull + 8 * i, 4);
-      mbar_init(bars + kcPFree + 8 * i, 1);
       mbar_init(bars + kcDrain + 8 * i, 1);
     }
     mbar_init(bars + kcQFull, 4);
+    for (int i = 0; i < S::NS; ++i) {
+      mbar_init(bars + kcSFull + 8 * i, 1);
+      mbar_init(bars + kcPFull + 8 * i, 4);
+      mbar_init(bars + kcPFree + 8 * i, 1);
+    }
     for (int i = 0; i < S::NR; ++i) {
       mbar_init(bars + kcKLoaded + 8 * i, 1);
       mbar_init(bars + kcKTaken + 8 * i, S::KWARPS);
@@ -847,12 +856,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  // registers: 128 (40 + 4 * 72 + 152) = the launch's 768 * 80
-  if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    tree_softmax<D>(p, sm, ctl, warp, lane);
+  // Registers per thread, in all those of the launch: one softmax group
+  // 88 + 4 * 88 + 40 = 6 * 80, two 2 * 88 + 4 * 72 + 40 = 7 * 72.
+  if (warp < 4 || warp >= 24) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    tree_softmax<D>(p, sm, ctl, warp >= 24 ? 1 : 0, warp & 3, lane);
   } else if (warp < 20) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (S::SW == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int warp8 = (warp - 4) / 4 * 2 + (warp & 1);
     if ((warp & 2) == 0) {
       switch (p.kmode) {
@@ -922,7 +932,8 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   const long long ranges = min(total, static_cast<long long>(p.grid));
   const int c0 = static_cast<int>(((x0 + 1) * ranges - 1) / total), c1 = static_cast<int>(((x1 + 1) * ranges - 1) / total);
   const long long slot = static_cast<long long>(c0) + static_cast<long long>(b) * p.HH + hh;
-  int parts = (c1 - c0 + 1) * p.copies;
+  const int parts_rec = p.copies * S::SW;
+  int parts = (c1 - c0 + 1) * parts_rec;
   if (!TQ_CHECK(slot + (c1 - c0) < p.n_recs, p.err)) parts = 0;
   const long long rec_floats = static_cast<long long>(p.slots) * (S::DV + 2);
   const float* recs = p.recs + slot * rec_floats;
@@ -940,8 +951,8 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   };
 #pragma unroll 2
   for (int s = warp % W; s < parts; s += W) {
-    const float* rec = recs + (s / p.copies) * rec_floats;
-    const int at = (s % p.copies) * p.rows + rl;
+    const float* rec = recs + (s / parts_rec) * rec_floats;
+    const int at = (s % parts_rec) * p.rows + rl;
     const float* src = rec + 2 * p.slots + static_cast<long long>(at) * S::DV + lane * E - half * S::DV;
     float x[E];
 #pragma unroll
@@ -1024,11 +1035,11 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
   using S = TreeShape<D>;
   cudaError_t e = allow_smem(tree_split_kernel<D>, S::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl_block(tree_split_kernel<D>, p.grid, kTreeThreads, p, s, S::SMEM);
+  e = launch_pdl_block(tree_split_kernel<D>, p.grid, S::THREADS, p, s, S::SMEM);
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.N;
   // many partial results a row (few segments, many blocks): four warps a row
-  const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies;
+  const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies * S::SW;
   if (parts >= 8) return launch_pdl_block(tree_combine_kernel<D, 4>, static_cast<int>(rows), 128, p, s, 0);
   return launch_pdl_block(tree_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, p, s, 0);
 }
