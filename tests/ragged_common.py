@@ -138,7 +138,7 @@ def tree_reference(q, cache, T, tree, kb, ks, vb, parents=None, lens=None, left_
                     p = np.exp(s - m)
                     out[b, hq, i] = (p @ v) / p.sum() @ R
                     lse[b, hq, i] = m + np.log(p.sum())
-                    mag = scale * (np.abs(k) @ np.abs(q[b, hq, i])).max()
+                    mag = abs(scale) * (np.abs(k) @ np.abs(q[b, hq, i])).max()
                 e = (D / 16 + 4) * 2 * HALF * mag + np.abs(s).max() * 2.0 ** -22 + 2.0 ** -21
                 steps = (len(s) / 16 + 32 + math.log2(D)) * 2 * HALF
                 tol[b, hq, i] = (2 * (e + 2.0 ** -18) + 2 * steps) * np.sqrt((v * v).sum(-1)).max()
@@ -200,7 +200,7 @@ def weights_reference(q, lse, cache, T, kb, ks, path=None, n_path=None, lens=Non
                 with np.errstate(all="ignore"):
                     x = scale * (k @ q[b, hq, node])
                     w = np.exp(x - lse[b, hq, node])
-                    mag = scale * (np.abs(k) @ np.abs(q[b, hq, node]))
+                    mag = abs(scale) * (np.abs(k) @ np.abs(q[b, hq, node]))
                     e = (D / 16 + 4) * 2 * HALF * mag + (np.abs(x) + abs(lse[b, hq, node])) * 2.0 ** -22 + 2.0 ** -21
                     out[b, hq // G, lo:last + 1] += w
                     tol[b, hq // G, lo:last + 1] += w * (e + (G * n + 2) * 2 * HALF)

@@ -99,6 +99,16 @@ def test_tree_sharp_rows_and_rising_maximum(D):
     rc.check_tree(got, lse, ref)
 
 
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1e-30, 3.0])
+def test_tree_scales(scale):
+    """Negative, zero, tiny and large softmax scales (hidden tokens stay hidden)."""
+    main, tree = (rc.random_cache(1, 2, n, 128, 8, True, 3, n) for n in (150, 6))
+    q, par = _q((1, 4, 6, 128), 2), _parents(1, 6, 3)
+    got, lse = tq.tq_tree_attention(q.cuda(), rc.to_gpu(main), 150, rc.to_gpu(tree), 8, True, 3, parents=_int(par),
+                                    left_pad=_int([5]), scale=scale, out_dtype=torch.float32)
+    rc.check_tree(got, lse, rc.tree_reference(q, main, 150, tree, 8, True, 3, par, None, [5], scale))
+
+
 def test_tree_lengths_outside_the_range_are_clamped():
     got, lse, ref = run_tree(4, 1, 2, 3, 70, 128, 8, True, 3, lens=[71, -5, 2**31 - 1, 10],
                              left_pad=[-7, 3, 2**31 - 1, 10])

@@ -170,36 +170,40 @@ struct TreeWalk {
   }
 };
 
-// Where the group of a decoding thread sits. Eight lanes take four groups of
+// Where the groups of a decoding thread sit. Eight lanes take four groups of
 // two tokens (head_dim 64: two groups of four), and a thread decodes its
 // group's two halves of 16 elements in the order (flip, 1 - flip). So the eight
 // lanes' 16-byte reads of 8-bit codes and their 16-byte stores into the
 // swizzled tile each meet eight distinct places of a 128-byte line (64: the
-// stores only).
-template <int NG, int WARPS>
-__device__ __forceinline__ void tree_unit(int piece, int warp, int lane, int& token, int& group) {
-  const int c = (piece * WARPS + warp) * 4 + (lane >> 3);
-  if constexpr (NG == 2) {
-    token = c * 4 + ((lane >> 1) & 3);
-    group = lane & 1;
-  } else {
-    token = c / (NG / 4) * 2 + ((lane >> 2) & 1);
-    group = c % (NG / 4) * 4 + (lane & 3);
+// stores only). The next group of a thread is the same one STEP tokens on
+// (a multiple of 8, so the swizzle stays).
+template <int D, int NG, int WARPS>
+struct TreeUnit {
+  static constexpr int TT = TreeShape<D>::TT;
+  static constexpr int STEP = NG == 2 ? 16 * WARPS : 32 * WARPS / NG;
+  int token, group, flip;
+  uint32_t chunk;  // byte offset of the first half's first 16 bytes in a decoded tile
+  __device__ __forceinline__ TreeUnit(int warp, int lane) {
+    const int c = warp * 4 + (lane >> 3);
+    if constexpr (NG == 2) {
+      token = c * 4 + ((lane >> 1) & 3);
+      group = lane & 1;
+      flip = 0;
+    } else {
+      token = c / (NG / 4) * 2 + ((lane >> 2) & 1);
+      group = c % (NG / 4) * 4 + (lane & 3);
+      flip = ((lane >> 2) ^ (lane >> 1)) & 1;
+    }
+    chunk = (group >> 1) * (TT * 128) + token * 128 + ((((group & 1) * 4 + 2 * flip) ^ (token & 7)) << 4);
   }
-}
-template <int NG>
-__device__ __forceinline__ int tree_flip(int lane) {
-  return NG == 2 ? 0 : ((lane >> 2) ^ (lane >> 1)) & 1;
-}
-
-// Stores the 16 bf16 of half h of a group (8 words) into a decoded tile.
-template <int TT>
-__device__ __forceinline__ void tree_store_half(uint32_t tile, int token, int group, int h, const uint32_t (&w)[8]) {
-  const uint32_t line = tile + (group >> 1) * (TT * 128) + token * 128;
-  const int c0 = (group & 1) * 4 + 2 * h, x = token & 7;
-  sts128(line + ((c0 ^ x) << 4), w[0], w[1], w[2], w[3]);
-  sts128(line + (((c0 + 1) ^ x) << 4), w[4], w[5], w[6], w[7]);
-}
+  // Stores half 0 or 1 (in the thread's order) of group i: two 16-byte pieces,
+  // whose places differ in the line's bits 5 (half) and 4 (piece).
+  __device__ __forceinline__ void store(uint32_t tile, int i, int half, const uint32_t (&w)[8]) const {
+    const uint32_t a = tile + i * (STEP * 128);
+    sts128(a + (chunk ^ (half << 5)), w[0], w[1], w[2], w[3]);
+    sts128(a + (chunk ^ (half << 5) ^ 16u), w[4], w[5], w[6], w[7]);
+  }
+};
 
 // The packed words of half h (16 codes of B bits, from bit 0 of w on) of the
 // group at `a`.
@@ -342,24 +346,24 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const int count = *reinterpret_cast<const int*>(ctl + kcCount);
-  constexpr int STEP = 8 / S::KWARPS;  // tiles from one of the warp's tiles to the next
-  const int wk = warp8 % S::KWARPS, flip = tree_flip<S::NGK>(lane);
+  const TreeUnit<D, S::NGK, S::KWARPS> u(warp8 % S::KWARPS, lane);
+  const uint32_t codes = sm + S::KR_OFF + u.token * X + u.group * (4 * KB);
+  const uint32_t scales = sm + S::KR_OFF + S::KR_SC + (u.token * S::NGK + u.group) * 2;
 #pragma unroll 1
-  for (int it = warp8 / S::KWARPS; it < count; it += STEP) {
+  for (int it = warp8 / S::KWARPS; it < count; it += 8 / S::KWARPS) {
     const int st = it % S::KS, rs = it % S::NR;
     if (!warp_wait(bars + kcKLoaded + 8 * rs, (it / S::NR) & 1, quit, p.err)) return;
     if (it >= S::KS && !warp_wait(bars + kcKEmpty + 8 * st, (it / S::KS - 1) & 1, quit, p.err)) return;
-    const uint32_t src = sm + S::KR_OFF + rs * S::KR_BYTES;
 #pragma unroll 1
-    for (int i = 0; i < 2 * S::KP; ++i) {
-      int token, group;
-      tree_unit<S::NGK, S::KWARPS>(i >> 1, wk, lane, token, group);
-      const int h = (i & 1) ^ flip;
+    for (int i = 0; i < S::KP; ++i) {
+      const uint32_t a = codes + rs * S::KR_BYTES + i * (u.STEP * X);
+      const uint32_t at = scales + rs * S::KR_BYTES + i * (u.STEP * S::NGK * 2);
+      const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at)))));
+      const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at + S::KR_ZP - S::KR_SC))));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
       uint32_t w[(KB + 1) / 2];
-      tree_words<KB>(src + token * X + group * (4 * KB), h, w);
-      const uint32_t at = src + (token * S::NGK + group) * 2;
-      const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at + S::KR_SC)))));
-      const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at + S::KR_ZP))));
+      tree_words<KB>(a, half ^ u.flip, w);
       uint32_t o[8];
       // RN(code + zero), RN(. * scale), bf16: the two forms of the decode
       // attention (code plus zero is exact in both: the zero point is an
@@ -386,7 +390,8 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
           o[j] = pack_bf16x2(a.x, a.y);
         }
       }
-      tree_store_half<S::TT>(sm + st * S::K_BYTES, token, group, h, o);
+      u.store(sm + st * S::K_BYTES, i, half, o);
+      }
     }
     fence_proxy_async();
     __syncwarp();
@@ -395,6 +400,18 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
       mbar_arrive(bars + kcKTaken + 8 * rs);
     }
   }
+}
+
+// Reads of the value table, free to move (the table never changes).
+__device__ __forceinline__ float table32(uint32_t a) {
+  float x;
+  asm("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(a));
+  return x;
+}
+__device__ __forceinline__ float2 table64(uint32_t a) {
+  float2 x;
+  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(a));
+  return x;
 }
 
 // The values' decoding warps. Tokens outside the sequence are decoded as zeros,
@@ -409,52 +426,55 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
   constexpr int X = S::DV * VB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
-  const uint8_t* tab = smem + S::T_OFF;
-  const uint32_t vlane = VT::PAIRS ? 8u * (lane & 15) : 4u * lane;  // the lane's copy of the table
+  // the lane's copy of the value table
+  const uint32_t tab = sm + S::T_OFF + (VT::PAIRS ? 8u * (lane & 15) : 4u * lane);
   const uint32_t vstride = p.vtab_stride;
   const int count = *reinterpret_cast<const int*>(ctl + kcCount);
-  const int wv = warp8 % S::VWARPS, flip = tree_flip<S::NGV>(lane);
+  const int wv = warp8 % S::VWARPS;
+  const TreeUnit<D, S::NGV, S::VWARPS> u(wv, lane);
+  const uint32_t codes = sm + S::VR_OFF + u.token * X + u.group * (4 * VB);
+  const uint32_t scales = sm + S::VR_OFF + S::VR_SC + (u.token * S::NGV + u.group) * 2;
 #pragma unroll 1
   for (int it = warp8 / S::VWARPS; it < count; it += 8 / S::VWARPS) {
     const int st = it % S::VS, rs = it % S::NR;
     if (!warp_wait(bars + kcVLoaded + 8 * rs, (it / S::NR) & 1, quit, p.err)) return;
     if (it >= S::VS && !warp_wait(bars + kcVEmpty + 8 * st, (it / S::VS - 1) & 1, quit, p.err)) return;
-    const uint32_t src = sm + S::VR_OFF + rs * S::VR_BYTES;
-    const uint2 span = lds64(src + S::VR_SPAN);
+    const uint2 span = lds64(sm + S::VR_OFF + rs * S::VR_BYTES + S::VR_SPAN);
     unsigned long long bad = 0;
 #pragma unroll 1
-    for (int i = 0; i < 2 * S::VP; ++i) {
-      int token, group;
-      tree_unit<S::NGV, S::VWARPS>(i >> 1, wv, lane, token, group);
-      const int h = (i & 1) ^ flip;
-      uint32_t w[(VB + 1) / 2];
-      tree_words<VB>(src + token * X + group * (4 * VB), h, w);
-      uint32_t bits = lds16(src + S::VR_SC + (token * S::NGV + group) * 2);
-      if (token < static_cast<int>(span.x) || token >= static_cast<int>(span.y)) bits = 0;
+    for (int i = 0; i < S::VP; ++i) {
+      const uint32_t a = codes + rs * S::VR_BYTES + i * (u.STEP * X);
+      uint32_t bits = lds16(scales + rs * S::VR_BYTES + i * (u.STEP * S::NGV * 2));
+      const int token = u.token + i * u.STEP;
+      if (static_cast<unsigned>(token) - span.x >= span.y - span.x) bits = 0;
       if ((bits & 0x7c00u) == 0x7c00u) {
         bad |= 1ull << token;
         bits = 0;
       }
       const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(bits))));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+      uint32_t w[(VB + 1) / 2];
+      tree_words<VB>(a, half ^ u.flip, w);
       uint32_t o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float2 cc;
         if constexpr (VB == 4) {
-          cc = *reinterpret_cast<const float2*>(tab + byte_field_addr(w, j, vstride, vlane));
+          cc = table64(byte_field_addr(w, j, vstride, tab));
         } else if constexpr (VT::PAIRS) {
-          cc = *reinterpret_cast<const float2*>(tab + field_addr<2 * VB, 7>(w, 2 * j * VB, vlane));
+          cc = table64(field_addr<2 * VB, 7>(w, 2 * j * VB, 0u) + tab);
         } else if constexpr (VB == 8) {
-          cc = make_float2(*reinterpret_cast<const float*>(tab + byte_field_addr(w, 2 * j, vstride, vlane)),
-                           *reinterpret_cast<const float*>(tab + byte_field_addr(w, 2 * j + 1, vstride, vlane)));
+          cc = make_float2(table32(byte_field_addr(w, 2 * j, vstride, tab)), table32(byte_field_addr(w, 2 * j + 1, vstride, tab)));
         } else {
-          cc = make_float2(*reinterpret_cast<const float*>(tab + field_addr<VB, 7>(w, 2 * j * VB, vlane)),
-                           *reinterpret_cast<const float*>(tab + field_addr<VB, 7>(w, (2 * j + 1) * VB, vlane)));
+          cc = make_float2(table32(field_addr<VB, 7>(w, 2 * j * VB, 0u) + tab),
+                           table32(field_addr<VB, 7>(w, (2 * j + 1) * VB, 0u) + tab));
         }
         const float2 x = mul2(cc, sc);
         o[j] = pack_bf16x2(x.x, x.y);
       }
-      tree_store_half<S::TT>(sm + S::V_OFF + st * S::V_BYTES, token, group, h, o);
+      u.store(sm + S::V_OFF + st * S::V_BYTES, i, half, o);
+      }
     }
     uint2 marks = make_uint2(0u, 0u);
     if (__any_sync(kFull, bad != 0)) {
@@ -513,14 +533,15 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
   }
 }
 
-// The weighted values' thread: O += P V, the weights as a high and a low part.
+// The weighted values' thread: O += P V, the weights as a high part and a
+// remainder to subtract.
 template <int D>
 __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
   using S = TreeShape<D>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem);
-  constexpr uint32_t kind = mma_kind(S::DV, true, false);
+  constexpr uint32_t kind = mma_kind(S::DV, true, false), kind_rest = mma_kind(S::DV, true, true);
   TreeWalk<D> w;
   w.init(p, ctl);
   int it = 0;
@@ -539,7 +560,7 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
 #pragma unroll
       for (int ks = 0; ks < S::TT / 16; ++ks) {
         mma_ts(o, pc + 16 * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0);
-        mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind, true);
+        mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind_rest, true);
       }
       mma_commit(bars + kcPFree + 8 * sb);
       mma_commit(bars + kcVEmpty + 8 * st);
@@ -551,6 +572,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// The bf16 in the low (HI = false) or high half of x minus c, rounded once.
+template <bool HI>
+__device__ __forceinline__ float sub_bf16_f32(uint32_t x, float c) {
+  float r;
+  if constexpr (HI) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tsub.rn.f32.bf16 %0, hi, %2;\n\t}" : "=f"(r) : "r"(x), "f"(c));
+  } else {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tsub.rn.f32.bf16 %0, lo, %2;\n\t}" : "=f"(r) : "r"(x), "f"(c));
+  }
+  return r;
 }
 
 // The softmax warps (group `which` of SW, every SW-th tile): a thread holds one
@@ -691,7 +724,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
         const float ref = m == kNegInf ? 0.0f : m;
         const float2 minus = f2(-ref), by = f2(p.scale_log2);
         float2 sum[2] = {f2(0.0f), f2(0.0f)};
-        // the weights as a bf16 high part plus a bf16 remainder: exact to 2^-18
+        // the weights as a bf16 high part minus a bf16 remainder: exact to 2^-18
 #pragma unroll 1
         for (int c = col0; c < col0 + W; c += 16) {
           uint32_t s[16], x[16];
@@ -703,8 +736,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
             const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             sum[i & 1] = add2(sum[i & 1], e);
             x[i] = pack_bf16x2(e.x, e.y);
-            const float2 rest = sub2(e, make_float2(bf16_lo(x[i]), bf16_hi(x[i])));
-            x[8 + i] = pack_bf16x2(rest.x, rest.y);
+            x[8 + i] = pack_bf16x2(sub_bf16_f32<false>(x[i], e.x), sub_bf16_f32<true>(x[i], e.y));
           }
           tmem_st16(buf + c, x);
         }
