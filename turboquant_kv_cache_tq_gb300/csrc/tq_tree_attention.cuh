@@ -27,11 +27,7 @@
 // lengths.
 #pragma once
 
-#include <type_traits>
-
-#include "tq_attention.cuh"
-#include "tq_ragged.cuh"
-#include "tq_tcgen05.cuh"
+#include "tq_ragged_tiles.cuh"
 
 namespace tq {
 
@@ -119,17 +115,12 @@ enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 
              kcCount = 204, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
              kcBad = 352 };
 
-// Tiles of the sequence of a batch row with tokens [lo, hi); they start at a
-// multiple of 16 tokens, which keeps every buffer's rows 16-byte aligned.
-template <int TT>
-__device__ __forceinline__ int tree_main_tiles(int lo, int hi) {
-  return hi > lo ? (hi - (lo & ~15) + TT - 1) / TT : 0;
-}
+// Tiles of a batch row: the sequence's and the tree's.
 template <int TT>
 __device__ __forceinline__ int tree_row_tiles(const TreeParams& p, int b) {
   int lo, hi;
   row_range(p.lens, p.left_pad, b, p.T, lo, hi);
-  return tree_main_tiles<TT>(lo, hi) + (p.N + TT - 1) / TT;
+  return sequence_tiles<TT>(lo, hi) + (p.N + TT - 1) / TT;
 }
 
 // A walk over the block's tiles, the same in every warp.
@@ -141,7 +132,7 @@ struct TreeWalk {
 
   __device__ __forceinline__ void row(const TreeParams& p) {
     row_range(p.lens, p.left_pad, b, p.T, lo, hi);
-    n_main = tree_main_tiles<TT>(lo, hi);
+    n_main = sequence_tiles<TT>(lo, hi);
     n = n_main + (p.N + TT - 1) / TT;
   }
   __device__ __forceinline__ void init(const TreeParams& p, const uint8_t* ctl) {
@@ -169,82 +160,6 @@ struct TreeWalk {
     end = min(TT, (t ? p.N : hi) - t0);
   }
 };
-
-// Where the groups of a decoding thread sit. Eight lanes take four groups of
-// two tokens (head_dim 64: two groups of four), and a thread decodes its
-// group's two halves of 16 elements in the order (flip, 1 - flip). So the eight
-// lanes' 16-byte reads of 8-bit codes and their 16-byte stores into the
-// swizzled tile each meet eight distinct places of a 128-byte line (64: the
-// stores only). The next group of a thread is the same one STEP tokens on
-// (a multiple of 8, so the swizzle stays).
-template <int D, int NG, int WARPS>
-struct TreeUnit {
-  static constexpr int TT = TreeShape<D>::TT;
-  static constexpr int STEP = NG == 2 ? 16 * WARPS : 32 * WARPS / NG;
-  int token, group, flip;
-  uint32_t chunk;  // byte offset of the first half's first 16 bytes in a decoded tile
-  __device__ __forceinline__ TreeUnit(int warp, int lane) {
-    const int c = warp * 4 + (lane >> 3);
-    if constexpr (NG == 2) {
-      token = c * 4 + ((lane >> 1) & 3);
-      group = lane & 1;
-      flip = 0;
-    } else {
-      token = c / (NG / 4) * 2 + ((lane >> 2) & 1);
-      group = c % (NG / 4) * 4 + (lane & 3);
-      flip = ((lane >> 2) ^ (lane >> 1)) & 1;
-    }
-    chunk = (group >> 1) * (TT * 128) + token * 128 + ((((group & 1) * 4 + 2 * flip) ^ (token & 7)) << 4);
-  }
-  // Stores half 0 or 1 (in the thread's order) of group i: two 16-byte pieces,
-  // whose places differ in the line's bits 5 (half) and 4 (piece).
-  __device__ __forceinline__ void store(uint32_t tile, int i, int half, const uint32_t (&w)[8]) const {
-    const uint32_t a = tile + i * (STEP * 128);
-    sts128(a + (chunk ^ (half << 5)), w[0], w[1], w[2], w[3]);
-    sts128(a + (chunk ^ (half << 5) ^ 16u), w[4], w[5], w[6], w[7]);
-  }
-};
-
-// The packed words of half h (16 codes of B bits, from bit 0 of w on) of the
-// group at `a`.
-template <int B>
-__device__ __forceinline__ void tree_words(uint32_t a, int h, uint32_t (&w)[(B + 1) / 2]) {
-  if constexpr (B == 8) {
-    const uint4 u = lds128(a + 16 * h);
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-  } else if constexpr (B == 4) {
-    const uint2 u = lds64(a + 8 * h);
-    w[0] = u.x; w[1] = u.y;
-  } else if constexpr (B == 2) {
-    w[0] = lds32(a + 4 * h);
-  } else if constexpr (B == 3) {
-    const uint32_t x = lds32(a + 4 * h), y = lds32(a + 4 * h + 4);
-    w[0] = __funnelshift_r(x, y, 16 * h);
-    w[1] = y >> (16 * h);
-  } else {
-    const uint32_t x = lds32(a + 8 * h), y = lds32(a + 8 * h + 4), z = lds32(a + 8 * h + 8);
-    w[0] = __funnelshift_r(x, y, 16 * h);
-    w[1] = __funnelshift_r(y, z, 16 * h);
-    w[2] = z >> (16 * h);
-  }
-}
-
-// One warp copies n rows of X bytes, src_pitch bytes apart, side by side, in
-// the widest pieces that the rows' alignment allows.
-__device__ __forceinline__ void tree_copy_rows(uint32_t dst, const uint8_t* src, int src_pitch, int X, int n, int lane) {
-  const int odd = X | src_pitch;
-  const int shift = (odd & 15) == 0 ? 4 : (odd & 7) == 0 ? 3 : 2;
-  const int per = X >> shift;
-#pragma unroll 1
-  for (int i = lane; i < n * per; i += 32) {
-    const int t = i / per, c = (i - t * per) << shift;
-    const uint8_t* from = src + static_cast<long long>(t) * src_pitch + c;
-    const uint32_t to = dst + t * X + c;
-    if (shift == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-    else if (shift == 3) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-  }
-}
 
 // The loading warps (keys and values): the packed rows of tile after tile into
 // the stages, by bulk copies where every tile of both caches starts on 16 bytes
@@ -304,9 +219,9 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
           }
         }
       } else {
-        tree_copy_rows(dst, codes, row_bytes, X, n, lane);
-        tree_copy_rows(dst + SC, scales, 2 * S::NGK, 2 * NG, n, lane);
-        if constexpr (KEYS) tree_copy_rows(dst + S::KR_ZP, zeros, 2 * NG, 2 * NG, n, lane);
+        copy_rows_any(dst, codes, row_bytes, X, n, lane);
+        copy_rows_any(dst + SC, scales, 2 * S::NGK, 2 * NG, n, lane);
+        if constexpr (KEYS) copy_rows_any(dst + S::KR_ZP, zeros, 2 * NG, 2 * NG, n, lane);
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -341,12 +256,11 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
 template <int D, int KMODE>
 __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp8, int lane) {
   using S = TreeShape<D>;
-  using M = KeySpec<KMODE>;
-  constexpr int KB = M::B, X = D * KB / 8;
+  constexpr int KB = KeySpec<KMODE>::B, X = D * KB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const int count = *reinterpret_cast<const int*>(ctl + kcCount);
-  const TreeUnit<D, S::NGK, S::KWARPS> u(warp8 % S::KWARPS, lane);
+  const TileUnit<S::TT, S::NGK, S::KWARPS> u(warp8 % S::KWARPS, lane);
   const uint32_t codes = sm + S::KR_OFF + u.token * X + u.group * (4 * KB);
   const uint32_t scales = sm + S::KR_OFF + S::KR_SC + (u.token * S::NGK + u.group) * 2;
 #pragma unroll 1
@@ -358,40 +272,7 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
     for (int i = 0; i < S::KP; ++i) {
       const uint32_t a = codes + rs * S::KR_BYTES + i * (u.STEP * X);
       const uint32_t at = scales + rs * S::KR_BYTES + i * (u.STEP * S::NGK * 2);
-      const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at)))));
-      const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(at + S::KR_ZP - S::KR_SC))));
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-      uint32_t w[(KB + 1) / 2];
-      tree_words<KB>(a, half ^ u.flip, w);
-      uint32_t o[8];
-      // RN(code + zero), RN(. * scale), bf16: the two forms of the decode
-      // attention (code plus zero is exact in both: the zero point is an
-      // integer)
-      if constexpr (KB == 8) {
-        const float z = __fsub_rn(zp, 1024.0f + (M::SIGNED ? 128.0f : 0.0f));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t x = M::SIGNED ? w[j] ^ 0x80808080u : w[j];
-          const uint32_t h01 = __byte_perm(x, 0x64646464u, 0x4140), h23 = __byte_perm(x, 0x64646464u, 0x4342);
-          const float2 a = mul2(make_float2(add_f16_f32<false>(h01, z), add_f16_f32<true>(h01, z)), sc);
-          const float2 b = mul2(make_float2(add_f16_f32<false>(h23, z), add_f16_f32<true>(h23, z)), sc);
-          o[2 * j] = pack_bf16x2(a.x, a.y);
-          o[2 * j + 1] = pack_bf16x2(b.x, b.y);
-        }
-      } else {
-        const float2 z = f2(__fsub_rn(zp, kMagic));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 a = mul2(add2(make_float2(__uint_as_float(kMagicBits | code_at<KB>(w, 2 * j)),
-                                                 __uint_as_float(kMagicBits | code_at<KB>(w, 2 * j + 1))),
-                                     z),
-                                sc);
-          o[j] = pack_bf16x2(a.x, a.y);
-        }
-      }
-      u.store(sm + st * S::K_BYTES, i, half, o);
-      }
+      decode_key_group<KMODE>(u, a, at, at + S::KR_ZP - S::KR_SC, sm + st * S::K_BYTES, i);
     }
     fence_proxy_async();
     __syncwarp();
@@ -431,7 +312,7 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
   const uint32_t vstride = p.vtab_stride;
   const int count = *reinterpret_cast<const int*>(ctl + kcCount);
   const int wv = warp8 % S::VWARPS;
-  const TreeUnit<D, S::NGV, S::VWARPS> u(wv, lane);
+  const TileUnit<S::TT, S::NGV, S::VWARPS> u(wv, lane);
   const uint32_t codes = sm + S::VR_OFF + u.token * X + u.group * (4 * VB);
   const uint32_t scales = sm + S::VR_OFF + S::VR_SC + (u.token * S::NGV + u.group) * 2;
 #pragma unroll 1
@@ -455,7 +336,7 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
       uint32_t w[(VB + 1) / 2];
-      tree_words<VB>(a, half ^ u.flip, w);
+      tile_words<VB>(a, half ^ u.flip, w);
       uint32_t o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
