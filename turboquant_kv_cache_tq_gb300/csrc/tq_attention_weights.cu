@@ -62,7 +62,7 @@ struct WeightsShape {
 constexpr int kWeightsThreads = 640;
 
 enum : int { wcKFull = 0, wcKEmpty = 16, wcSFull = 32, wcSFree = 48, wcQFull = 64, wcLoaded = 72, wcTaken = 104,
-             wcDrain = 136, wcTmem = 144, wcQuit = 148, wcTile = 152, wcB = 156, wcH = 160, wcCount = 164, wcOdd = 168 };
+             wcDrain = 136, wcTmem = 144, wcQuit = 148, wcTile = 152, wcB = 156, wcH = 160, wcCount = 164, wcOdd = 168, wcTurn = 176 };
 
 __device__ __forceinline__ int observers(const WeightsParams& p, int b) {
   return p.n_path != nullptr ? min(max(p.n_path[b], 0), p.P) : p.P;
@@ -254,9 +254,9 @@ __device__ void weights_sum(const WeightsParams& p, uint32_t sm, uint8_t* smem, 
   const int tid = warp * 32 + lane;
   WeightsWalk<S::TT, S::NB> w;
   w.init(p, ctl);
-  int it0 = 0, turn = 0;
+  int it0 = 0, turns = 0;
   for (; w.left > 0; w.next(p)) {
-    for (int round = 0; round < w.rounds; ++round, ++turn) {
+    for (int round = 0; round < w.rounds; ++round) {
       const int cols = min(S::NB, p.G * w.obs - round * S::NB);
       if (which == 0) {
         // the round's query rows and -lse log2(e), once the last round's scores
@@ -268,7 +268,9 @@ __device__ void weights_sum(const WeightsParams& p, uint32_t sm, uint8_t* smem, 
             if (!warp_wait(bars + wcSFree + 8, (last / 2) & 1, quit, p.err)) return;
           }
           if (tid == 0) *odd = 0;
-          asm volatile("bar.sync 1, 128;" ::: "memory");  // and by every warp of this one
+          warp_arrive(bars + wcTurn, lane);  // and by every warp of this one
+          if (!warp_wait(bars + wcTurn, turns & 1, quit, p.err)) return;
+          ++turns;
         }
         for (int c = tid; c < S::NB; c += 128) {
           float x = -kInf;  // no such row: nothing is added
@@ -378,6 +380,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
     }
     mbar_init(bars + wcQFull, 4);
     mbar_init(bars + wcDrain, 1);
+    mbar_init(bars + wcTurn, 4);
     *reinterpret_cast<int*>(ctl + wcQuit) = 0;
     *reinterpret_cast<int*>(ctl + wcOdd) = 0;
     mbar_fence_init();

@@ -32,7 +32,7 @@ __device__ __forceinline__ void row_range(const int* lens, const int* left_pad, 
 // The nodes that node i of a tree attends to, one bit each: i and its
 // ancestors, or none when i's chain of parents does not end at -1. A parent is
 // a lower number, so the walk ends.
-__device__ __forceinline__ unsigned long long node_ancestors(const int* parents, int i) {
+__device__ __forceinline__ unsigned long long node_ancestors(const volatile int* parents, int i) {
   if (parents == nullptr) return i == 63 ? ~0ull : (2ull << i) - 1ull;
   unsigned long long m = 0;
   for (;;) {

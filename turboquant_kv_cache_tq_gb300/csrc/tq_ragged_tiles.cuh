@@ -75,21 +75,26 @@ __device__ __forceinline__ void tile_words(uint32_t a, int h, uint32_t (&w)[(B +
   }
 }
 
-// One warp copies n rows of X bytes, src_pitch bytes apart, side by side, in
-// the widest pieces that the rows' alignment allows.
+// One warp copies n rows (at most 64) of X bytes, src_pitch bytes apart, side by
+// side, asynchronously and in the widest pieces that the rows' alignment allows.
 __device__ __forceinline__ void copy_rows_any(uint32_t dst, const uint8_t* src, int src_pitch, int X, int n, int lane) {
   const int odd = X | src_pitch;
   const int shift = (odd & 15) == 0 ? 4 : (odd & 7) == 0 ? 3 : 2;
   const int per = X >> shift;
-#pragma unroll 1
+  const unsigned inv = (1u << 20) / per + 1;  // i / per for i < 2^13 / per (n per pieces: at most 4096)
+#pragma unroll 2
   for (int i = lane; i < n * per; i += 32) {
-    const int t = i / per, c = (i - t * per) << shift;
+    const int t = static_cast<int>(i * inv >> 20), c = (i - t * per) << shift;
     const uint8_t* from = src + static_cast<long long>(t) * src_pitch + c;
     const uint32_t to = dst + t * X + c;
     if (shift == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
     else if (shift == 3) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
   }
+}
+// One arrival of this thread when its asynchronous copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Decodes group i of a thread's share of a tile of keys: the packed words at

@@ -21,7 +21,7 @@ bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, TreePla
   t->rows = (t->R + t->RB - 1) / t->RB;
   // (a lane's share is 16 tokens at least)
   t->copies = t->rows > 64 ? 1 : t->rows > 32 || t->TT == 32 ? 2 : 4;
-  t->slots = (t->copies * t->rows * (D <= 128 ? TreeShape<128>::SW : TreeShape<256>::SW) + 3) / 4 * 4;
+  t->slots = (t->copies * t->rows + 3) / 4 * 4;
   if (t->RB * (D / t->DV) > lim / Hkv) return false;
   t->HH = Hkv * t->RB * (D / t->DV);
   if (B > 0 && t->HH > lim / B) return false;

@@ -59,17 +59,21 @@ struct TreeParams {
 
 template <int D>
 struct TreeShape {
+  static constexpr int SW = D <= 128 ? 2 : 1;        // groups of softmax warps
   static constexpr int TT = D >= 256 ? 32 : 64;      // tokens of a tile
   static constexpr int DV = D == 512 ? 256 : D;      // value elements a block accumulates
   static constexpr int VH = D / DV;
   static constexpr int NGK = D / kGroup, NGV = DV / kGroup;
-  static constexpr int K_BYTES = TT * D * 2, V_BYTES = TT * DV * 2;
-  static constexpr int KS = D == 512 ? 1 : 2, VS = 2;  // decoded stages
-  // A group of four decoding warps owns a stage and takes every other tile;
-  // with one stage both groups share each tile (a barrier's parity tells
-  // neighbouring phases apart only, so a warp has to see every phase).
-  static constexpr int KWARPS = KS == 1 ? 8 : 4, VWARPS = 4;
-  static constexpr int KP = TT * NGK / (32 * KWARPS), VP = TT * NGV / (32 * VWARPS);  // groups a thread takes of a tile
+  // A key tile is decoded and multiplied in SUBS parts along head_dim (512: two
+  // halves, each the size of a stage).
+  static constexpr int SUBS = D == 512 ? 2 : 1, DS = D / SUBS, NGS = NGK / SUBS;
+  static constexpr int K_BYTES = TT * DS * 2, V_BYTES = TT * DV * 2;
+  static constexpr int KS = 2, VS = 2;  // decoded stages
+  // A group of four decoding warps owns a stage and takes every other part (a
+  // barrier's parity tells neighbouring phases apart only, so a warp has to see
+  // every phase of the barriers that it waits on).
+  static constexpr int KWARPS = 4, VWARPS = 4;
+  static constexpr int KP = TT * NGS / (32 * KWARPS), VP = TT * NGV / (32 * VWARPS);  // groups a thread takes of a part
   // Queries: the first QT elements of a row in tensor memory, the rest (head_dim
   // 512: no room beside 256 output columns) in shared memory.
   static constexpr int QT = D == 512 ? 256 : D;
@@ -80,23 +84,25 @@ struct TreeShape {
   static constexpr int NR = D == 512 ? 2 : 4;
   static constexpr int KR_SC = TT * D, KR_ZP = KR_SC + TT * NGK * 2, KR_BYTES = KR_ZP + TT * NGK * 2;
   static constexpr int VR_SC = TT * DV, VR_SPAN = VR_SC + TT * NGV * 2, VR_BYTES = VR_SPAN + 16;
-  // shared memory: K stages | V stages | queries | packed K | packed V | value table | control
+  // shared memory: K stages | V stages | queries | packed K | packed V | value table | control | softmax warps
   static constexpr int V_OFF = KS * K_BYTES;
   static constexpr int Q_OFF = V_OFF + VS * V_BYTES;
   static constexpr int KR_OFF = Q_OFF + Q_BYTES;
   static constexpr int VR_OFF = KR_OFF + NR * KR_BYTES;
   static constexpr int T_OFF = VR_OFF + NR * VR_BYTES;
   static constexpr int C_OFF = T_OFF + TAB;
-  static constexpr int SMEM = C_OFF + 512;
+  // a softmax warp's own: the tree's parents, and 32 rows of 20 floats on their way to a record
+  static constexpr int W_OFF = C_OFF + 512 + (SW > 1 ? 2048 : 0), W_BYTES = 256 + 32 * 80;
+  static constexpr int SMEM = W_OFF + 4 * SW * W_BYTES;
   // Tensor memory columns: SW outputs | NS score tiles | queries. The weights
   // of 16 tokens take the place of their scores: eight columns of high parts,
   // eight of remainders. With SW = 2 two groups of softmax warps take the tiles
   // in turn, each with an output of its own.
-  static constexpr int SW = D <= 128 ? 2 : 1;
   static constexpr int NS = D == 128 ? 3 : 4;
   static constexpr int O_COL = 0, S_COL = SW * DV, Q_COL = S_COL + NS * TT;
   static constexpr int THREADS = 640 + 128 * SW;
   static_assert(Q_COL + QT / 2 <= 512, "tensor memory");
+  static_assert(QT == DS, "the first part's queries are the ones in tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -113,7 +119,7 @@ constexpr int kTreeRows = 128;
 enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcPFull = 96, kcPFree = 128,
              kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcTile = 192, kcB = 196, kcHH = 200,
              kcCount = 204, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
-             kcBad = 352 };
+             kcBad = 352, kcMerge = 480, kcMerged = 488, kcMaxSum = 512 };
 
 // Tiles of a batch row: the sequence's and the tree's.
 template <int TT>
@@ -202,21 +208,19 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
       if (!KEYS && lane == 0)
         *reinterpret_cast<int2*>(smem + S::VR_OFF + st * STAGE + S::VR_SPAN) =
             make_int2(max(lo - t0, 0), min(hi - t0, S::TT));
-      if (p.bulk) {
-        if (lane == 0) {
-          mbar_expect_tx(bar, n * (X + (KEYS ? 4 : 2) * NG));
-          if (!ROWWISE && n > 0) {
-            bulk_load(dst, codes, n * X, bar);
-            bulk_load(dst + SC, scales, n * NG * 2, bar);
-            if constexpr (KEYS) bulk_load(dst + S::KR_ZP, zeros, n * NG * 2, bar);
-          }
-        }
-        if constexpr (ROWWISE) {
-          __syncwarp();
-          if (lane < n) {
-            bulk_load(dst + lane * X, codes + static_cast<long long>(lane) * row_bytes, X, bar);
-            bulk_load(dst + SC + lane * NG * 2, scales + lane * S::NGK * 2, NG * 2, bar);
-          }
+      if constexpr (ROWWISE) {
+        // (64 bulk copies of 64 to 256 bytes a tile measured slower: the copy
+        // engine takes about as long for each as for a whole tile's)
+        copy_rows_any(dst, codes, row_bytes, X, n, lane);
+        copy_rows_any(dst + SC, scales, 2 * S::NGK, 2 * NG, n, lane);
+        copies_arrive(bar);
+        if (lane == 0) mbar_arrive(bar);  // (releases the span too)
+      } else if (p.bulk) {
+        mbar_expect_tx(bar, n * (X + (KEYS ? 4 : 2) * NG));
+        if (n > 0) {
+          bulk_load(dst, codes, n * X, bar);
+          bulk_load(dst + SC, scales, n * NG * 2, bar);
+          if constexpr (KEYS) bulk_load(dst + S::KR_ZP, zeros, n * NG * 2, bar);
         }
       } else {
         copy_rows_any(dst, codes, row_bytes, X, n, lane);
@@ -245,7 +249,8 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
       w.next_segment(p);
     }
     // the last copies land before the block ends, whatever became of its other warps
-    if (p.bulk)
+    if (ROWWISE) asm volatile("cp.async.wait_all;" ::: "memory");
+    else if (p.bulk)
       for (int k = max(it - S::NR, 0); k < it; ++k) mbar_wait(bars + loaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
   }
   __syncwarp();
@@ -260,19 +265,22 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   const int count = *reinterpret_cast<const int*>(ctl + kcCount);
-  const TileUnit<S::TT, S::NGK, S::KWARPS> u(warp8 % S::KWARPS, lane);
-  const uint32_t codes = sm + S::KR_OFF + u.token * X + u.group * (4 * KB);
-  const uint32_t scales = sm + S::KR_OFF + S::KR_SC + (u.token * S::NGK + u.group) * 2;
+  const int which = warp8 / S::KWARPS;
+  const TileUnit<S::TT, S::NGS, S::KWARPS> u(warp8 % S::KWARPS, lane);
+  // (two parts a tile: a warp's part is always the same one)
+  const int group = u.group + (S::SUBS > 1 ? which * S::NGS : 0);
+  const uint32_t codes = sm + S::KR_OFF + u.token * X + group * (4 * KB);
+  const uint32_t scales = sm + S::KR_OFF + S::KR_SC + (u.token * S::NGK + group) * 2;
 #pragma unroll 1
-  for (int it = warp8 / S::KWARPS; it < count; it += 8 / S::KWARPS) {
-    const int st = it % S::KS, rs = it % S::NR;
+  for (int part = which; part < count * S::SUBS; part += S::KS) {
+    const int it = part / S::SUBS, st = part % S::KS, rs = it % S::NR;
     if (!warp_wait(bars + kcKLoaded + 8 * rs, (it / S::NR) & 1, quit, p.err)) return;
-    if (it >= S::KS && !warp_wait(bars + kcKEmpty + 8 * st, (it / S::KS - 1) & 1, quit, p.err)) return;
+    if (part >= S::KS && !warp_wait(bars + kcKEmpty + 8 * st, (part / S::KS - 1) & 1, quit, p.err)) return;
 #pragma unroll 1
     for (int i = 0; i < S::KP; ++i) {
-      const uint32_t a = codes + rs * S::KR_BYTES + i * (u.STEP * X);
       const uint32_t at = scales + rs * S::KR_BYTES + i * (u.STEP * S::NGK * 2);
-      decode_key_group<KMODE>(u, a, at, at + S::KR_ZP - S::KR_SC, sm + st * S::K_BYTES, i);
+      decode_key_group<KMODE>(u, codes + rs * S::KR_BYTES + i * (u.STEP * X), at, at + S::KR_ZP - S::KR_SC,
+                              sm + st * S::K_BYTES, i);
     }
     fence_proxy_async();
     __syncwarp();
@@ -391,25 +399,27 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
     if (!wait_or_quit(bars + kcQFull, seg & 1, quit, p.err)) return;
 #pragma unroll 1
     for (; it < end; ++it) {
-      const int st = it % S::KS, sb = it % S::NS;
-      const uint64_t k0 = smem_operand(sm + st * S::K_BYTES, 16, 1024);
+      const int sb = it % S::NS;
       // the weights that took the scores' place are used
       if (it >= S::NS && !wait_or_quit(bars + kcPFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
-      if (!wait_or_quit(bars + kcKFull + 8 * st, (it / S::KS) & 1, quit, p.err)) return;
-      tmem_fence_after();
+#pragma unroll 1
+      for (int sub = 0; sub < S::SUBS; ++sub) {
+        const int part = it * S::SUBS + sub, st = part % S::KS;
+        const uint64_t k0 = smem_operand(sm + st * S::K_BYTES, 16, 1024);
+        if (!wait_or_quit(bars + kcKFull + 8 * st, (part / S::KS) & 1, quit, p.err)) return;
+        tmem_fence_after();
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        // (operand addresses count 16 bytes)
-        const uint64_t b = k0 + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16;
-        if (ks < S::QT / 16) mma_ts(tm + S::S_COL + sb * S::TT, tm + S::Q_COL + 8 * ks, b, kind, ks > 0);
-        else
-          mma_ss(tm + S::S_COL + sb * S::TT,
-                 smem_operand(sm + S::Q_OFF, 16, 1024) +
-                     (((ks - S::QT / 16) >> 2) * (128 * 128) + (ks & 3) * 32) / 16,
-                 b, kind, true);
+        for (int ks = 0; ks < S::DS / 16; ++ks) {
+          // (operand addresses count 16 bytes)
+          const uint64_t b = k0 + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16;
+          if (sub == 0) mma_ts(tm + S::S_COL + sb * S::TT, tm + S::Q_COL + 8 * ks, b, kind, ks > 0);
+          else
+            mma_ss(tm + S::S_COL + sb * S::TT,
+                   smem_operand(sm + S::Q_OFF, 16, 1024) + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16, b, kind, true);
+        }
+        mma_commit(bars + kcKEmpty + 8 * st);
       }
       mma_commit(bars + kcSFull + 8 * sb);
-      mma_commit(bars + kcKEmpty + 8 * st);
     }
   }
 }
@@ -470,7 +480,7 @@ __device__ __forceinline__ float sub_bf16_f32(uint32_t x, float c) {
 // The softmax warps (group `which` of SW, every SW-th tile): a thread holds one
 // lane of tensor memory, i.e. one query row over its copy's share of the tokens.
 template <int D>
-__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int which, int warp, int lane) {
+__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int which, int warp, int lane) {
   using S = TreeShape<D>;
   constexpr int TT = S::TT;
   const int W = TT / p.copies;         // tokens of a tile that this lane takes: 16, 32 or 64
@@ -480,12 +490,14 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
   const uint32_t bars = sm + S::C_OFF;
   const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem) + (static_cast<uint32_t>(warp) << 21);
   const uint32_t oc = tm + S::O_COL + which * S::DV;
+  const int own_off = S::W_OFF + (which * 4 + warp) * S::W_BYTES;  // the warp's own shared memory
+  uint8_t* own = smem + own_off;
   const int copy = warp / QUADS, rl = (warp % QUADS) * 32 + lane, col0 = copy * W;
   auto s_full = [&](int it) { return warp_wait(bars + kcSFull + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
   auto weighed = [&](int it) { return warp_wait(bars + kcPFree + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
   TreeWalk<D> w;
   w.init(p, ctl);
-  int it0 = 0, anc_b = -1, anc_rb = -1;
+  int it0 = 0, seg = 0, anc_b = -1, anc_rb = -1;
   unsigned long long anc = 0;
   while (w.left > 0) {
     const int n = min(w.left, w.n - w.tile);
@@ -494,29 +506,41 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
     const bool row = rl < p.rows && r < p.R;
     const bool work = __any_sync(kFull, row);  // a warp whose lanes have no row only keeps the barriers going
     if (w.b != anc_b || rb != anc_rb) {
-      anc = row ? node_ancestors(p.parents == nullptr ? nullptr : p.parents + static_cast<long long>(w.b) * p.N, r % p.N)
-                : 0ull;
+      // (the walk up is one load after another: in shared memory)
+      volatile int* up = reinterpret_cast<volatile int*>(own);
+      if (p.parents != nullptr && w.b != anc_b) {
+        __syncwarp();
+        for (int i = lane; i < p.N; i += 32) up[i] = p.parents[static_cast<long long>(w.b) * p.N + i];
+        __syncwarp();
+      }
+      anc = row ? node_ancestors(p.parents == nullptr ? nullptr : up, r % p.N) : 0ull;
       anc_b = w.b;
       anc_rb = rb;
     }
-    // ---- the queries of the segment (every score of the last one is done)
-    if (which == 0) {
+    // ---- the queries of the segment (every score of the last one is done),
+    // each group its share of the columns, all loads of a round at once
+    {
       if (it0 > 0 && !s_full(it0 - 1)) return;
       tmem_fence_after();
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + ((static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N + (row ? r : 0)) * D);
+      constexpr int SHARE = S::QT / 2 / S::SW, STEP = SHARE < 32 ? SHARE : 32;
 #pragma unroll 1
-      for (int c = 0; c < S::QT / 2; c += 16) {
-        uint32_t x[16];
+      for (int c = which * SHARE; c < (which + 1) * SHARE; c += STEP) {
+        uint4 u[STEP / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 u = row ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
-          x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+        for (int i = 0; i < STEP / 4; ++i) u[i] = row ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < STEP / 16; ++i) {
+          const uint32_t x[16] = {u[4 * i].x,     u[4 * i].y,     u[4 * i].z,     u[4 * i].w,
+                                  u[4 * i + 1].x, u[4 * i + 1].y, u[4 * i + 1].z, u[4 * i + 1].w,
+                                  u[4 * i + 2].x, u[4 * i + 2].y, u[4 * i + 2].z, u[4 * i + 2].w,
+                                  u[4 * i + 3].x, u[4 * i + 3].y, u[4 * i + 3].z, u[4 * i + 3].w};
+          tmem_st16(tm + S::Q_COL + c + 16 * i, x);
         }
-        tmem_st16(tm + S::Q_COL + c, x);
       }
       if constexpr (S::QT < D) {
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < (D - S::QT) / 8; ++c) {
           const uint4 u = row ? __ldg(src + S::QT / 8 + c) : make_uint4(0u, 0u, 0u, 0u);
           sts128(sm + S::Q_OFF + (c >> 3) * (128 * 128) + (warp * 32 + lane) * 128 + (((c ^ lane) & 7) << 4), u.x, u.y,
@@ -648,34 +672,70 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* ctl, int
       if (!weighed(it0 + j - S::SW)) return;
       if (*any_bad != 0) spoil(it0 + j - S::SW, w.tile + j - S::SW);
     }
+    // A NaN row keeps a finite maximum, so that a merge takes it. The groups'
+    // results are merged here, a group half of the columns each.
+    float top = anc == 0 ? kNegInf : l != l ? 0.0f : m, sum = anc == 0 ? 0.0f : l, mine = 1.0f, other = 0.0f;
+    uint32_t oo = oc;  // the other group's output
+    if constexpr (S::SW > 1) {
+      const uint32_t ml = bars + kcMaxSum + (warp * 32 + lane) * 8;
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml + which * 1024), "f"(top), "f"(sum) : "memory");
+      tmem_fence_before();
+      warp_arrive(bars + kcMerge, lane);
+      if (!warp_wait(bars + kcMerge, seg & 1, quit, p.err)) return;
+      const uint2 u = lds64(ml + (which ^ 1) * 1024);
+      const float m2 = __uint_as_float(u.x), l2 = __uint_as_float(u.y), both = fmaxf(top, m2);
+      mine = top == kNegInf ? 0.0f : fast_exp2(__fsub_rn(top, both));
+      other = m2 == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m2, both));
+      sum = __fmaf_rn(sum, mine, __fmul_rn(l2, other));
+      top = both;
+      oo = tm + S::O_COL + (which ^ 1) * S::DV;
+    }
     if (work) {
       tmem_fence_after();
       const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(w.b) * p.HH + w.hh;
       float* rec = p.recs + slot * p.slots * (S::DV + 2);
-      const bool store = row && TQ_CHECK(slot < p.n_recs, p.err);
-      const int at = (which * p.copies + copy) * p.rows + rl;
-      if (store) {
-        // a NaN row keeps a finite maximum, so that the combine takes it
-        rec[at] = anc == 0 ? kNegInf : l != l ? 0.0f : m;
-        rec[p.slots + at] = anc == 0 ? 0.0f : l;
+      const bool store_ok = TQ_CHECK(slot < p.n_recs, p.err);
+      const int at = copy * p.rows + rl;
+      if (row && store_ok && which == 0) {
+        rec[at] = top;
+        rec[p.slots + at] = sum;
       }
-      if (j > j0) {
-        float4* dst = reinterpret_cast<float4*>(rec + 2 * p.slots + static_cast<long long>(at) * S::DV);
+      constexpr int SHARE = S::DV / S::SW;
 #pragma unroll 1
-        for (int c = 0; c < S::DV; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(oc + c, o);
-          tmem_wait_ld();
-          if (store) {
+      for (int c = which * SHARE; c < (which + 1) * SHARE; c += 16) {
+        uint32_t o[16], o2[16];
+        tmem_ld16(oc + c, o);
+        if constexpr (S::SW > 1) tmem_ld16(oo + c, o2);
+        tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          }
+        for (int i = 0; i < 16; ++i) {
+          // (an output that no weight went to may hold anything)
+          float x = mine == 0.0f ? 0.0f : S::SW > 1 ? __fmul_rn(__uint_as_float(o[i]), mine) : __uint_as_float(o[i]);
+          if constexpr (S::SW > 1) x = other == 0.0f ? x : __fmaf_rn(__uint_as_float(o2[i]), other, x);
+          o[i] = __float_as_uint(x);
+        }
+        // through shared memory: eight rows of 64 bytes a store, not 32 of 16
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sts128(sm + own_off + 256 + lane * 80 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = 8 * i + (lane >> 2), to = (warp % QUADS) * 32 + x;
+          const uint4 u = lds128(sm + own_off + 256 + x * 80 + (lane & 3) * 16);
+          if (to < p.rows && r - rl + to < p.R && store_ok)
+            *reinterpret_cast<uint4*>(rec + 2 * p.slots + static_cast<long long>(copy * p.rows + to) * S::DV + c +
+                                      (lane & 3) * 4) = u;
         }
       }
       tmem_fence_before();
     }
+    if constexpr (S::SW > 1) {  // both outputs are read
+      warp_arrive(bars + kcMerged, lane);
+      if (!warp_wait(bars + kcMerged, seg & 1, quit, p.err)) return;
+    }
+    ++seg;
     it0 += n;
     w.left -= n;
     w.next_segment(p);
@@ -707,7 +767,9 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
       mbar_init(bars + kcVEmpty + 8 * i, 1);
       mbar_init(bars + kcDrain + 8 * i, 1);
     }
-    mbar_init(bars + kcQFull, 4);
+    mbar_init(bars + kcQFull, 4 * S::SW);
+    mbar_init(bars + kcMerge, 4 * S::SW);
+    mbar_init(bars + kcMerged, 4 * S::SW);
     for (int i = 0; i < S::NS; ++i) {
       mbar_init(bars + kcSFull + 8 * i, 1);
       mbar_init(bars + kcPFull + 8 * i, 4);
@@ -715,8 +777,8 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
     }
     for (int i = 0; i < S::NR; ++i) {
       mbar_init(bars + kcKLoaded + 8 * i, 1);
-      mbar_init(bars + kcKTaken + 8 * i, S::KWARPS);
-      mbar_init(bars + kcVLoaded + 8 * i, 1);
+      mbar_init(bars + kcKTaken + 8 * i, S::KWARPS * S::SUBS);
+      mbar_init(bars + kcVLoaded + 8 * i, S::VH > 1 ? 33 : 1);
       mbar_init(bars + kcVTaken + 8 * i, S::VWARPS);
     }
     *reinterpret_cast<int*>(ctl + kcQuit) = 0;
@@ -728,8 +790,10 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
   if (warp == 0) {
     // the block's range of the line of all tiles: 32 batch rows at a time
     long long total = 0;
+    int n0 = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      long long c = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
+      n0 = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
+      long long c = n0;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
         const long long y = __shfl_up_sync(kFull, c, x);
@@ -748,7 +812,7 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
     long long before = 0;
     bool found = false;
     for (int b0 = 0; b0 < p.B && !found && first < end; b0 += 32) {
-      const int n = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
+      const int n = p.B <= 32 ? n0 : b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
       long long c = n;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
@@ -773,7 +837,7 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
   // 88 + 4 * 88 + 40 = 6 * 80, two 2 * 88 + 4 * 72 + 40 = 7 * 72.
   if (warp < 4 || warp >= 24) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
-    tree_softmax<D>(p, sm, ctl, warp >= 24 ? 1 : 0, warp & 3, lane);
+    tree_softmax<D>(p, sm, smem, ctl, warp >= 24 ? 1 : 0, warp & 3, lane);
   } else if (warp < 20) {
     if constexpr (S::SW == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int warp8 = (warp - 4) / 4 * 2 + (warp & 1);
@@ -845,41 +909,73 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   const long long ranges = min(total, static_cast<long long>(p.grid));
   const int c0 = static_cast<int>(((x0 + 1) * ranges - 1) / total), c1 = static_cast<int>(((x1 + 1) * ranges - 1) / total);
   const long long slot = static_cast<long long>(c0) + static_cast<long long>(b) * p.HH + hh;
-  const int parts_rec = p.copies * S::SW;
-  int parts = (c1 - c0 + 1) * parts_rec;
+  int parts = (c1 - c0 + 1) * p.copies;
   if (!TQ_CHECK(slot + (c1 - c0) < p.n_recs, p.err)) parts = 0;
   const long long rec_floats = static_cast<long long>(p.slots) * (S::DV + 2);
   const float* recs = p.recs + slot * rec_floats;
   float m = kNegInf, l = 0.0f, o[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.0f;
+  // The warp's partial results warp % W, warp % W + W, ... of each value half,
+  // LANES of them at a time: every lane looks at one maximum and sum, then all
+  // take the values with the factors known (no result waits for the last one).
+  constexpr int LANES = 32 / S::VH;
+  int most = parts;
+  if constexpr (S::VH > 1) most = max(parts, __shfl_xor_sync(kFull, parts, 16));
+  for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
+    const int mine = s0 + (lane % LANES) * W;
+    float m2 = kNegInf, l2 = 0.0f;
+    if (mine < parts) {
+      const float* rec = recs + (mine / p.copies) * rec_floats + (mine % p.copies) * p.rows + rl;
+      m2 = rec[0];
+      l2 = rec[p.slots];
+    }
+    float mn = m2;
+#pragma unroll
+    for (int x = LANES / 2; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, x));
+    mn = fmaxf(mn, m);
+    const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
+    float add = __fmul_rn(l2, fb);
+#pragma unroll
+    for (int x = LANES / 2; x > 0; x >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, x));
+    l = __fmaf_rn(l, fa, add);
+    m = mn;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
+    const int n_here = min(LANES, (most - s0 + W - 1) / W);
+#pragma unroll 4
+    for (int k = 0; k < n_here; ++k) {
+      const float f = __shfl_sync(kFull, fb, half * LANES + k);
+      const int s = s0 + k * W;
+      if (f != 0.0f) {  // (a part that saw no key is left out, whatever its values are; nor does one past the end count)
+        const int at = (s % p.copies) * p.rows + rl;
+        const float* src = recs + (s / p.copies) * rec_floats + 2 * p.slots + static_cast<long long>(at) * S::DV + lane * E -
+                           half * S::DV;
+#pragma unroll
+        for (int i = 0; i < E; i += V) {
+          if constexpr (V == 2) {
+            const float2 u = *reinterpret_cast<const float2*>(src + i);
+            o[i] = __fmaf_rn(u.x, f, o[i]);
+            o[i + 1] = __fmaf_rn(u.y, f, o[i + 1]);
+          } else {
+            const float4 u = *reinterpret_cast<const float4*>(src + i);
+            o[i] = __fmaf_rn(u.x, f, o[i]);
+            o[i + 1] = __fmaf_rn(u.y, f, o[i + 1]);
+            o[i + 2] = __fmaf_rn(u.z, f, o[i + 2]);
+            o[i + 3] = __fmaf_rn(u.w, f, o[i + 3]);
+          }
+        }
+      }
+    }
+  }
   auto merge = [&](float m2, float l2, const float (&x)[E]) {
     const float mn = fmaxf(m, m2);
     const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
     l = __fmaf_rn(l2, fb, __fmul_rn(l, fa));
-    // a part that saw no key is left out, whatever its values are
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(m2 == kNegInf ? 0.0f : x[i], fb, __fmul_rn(o[i], fa));
+    for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(x[i], fb, __fmul_rn(o[i], fa));
     m = mn;
   };
-#pragma unroll 2
-  for (int s = warp % W; s < parts; s += W) {
-    const float* rec = recs + (s / parts_rec) * rec_floats;
-    const int at = (s % parts_rec) * p.rows + rl;
-    const float* src = rec + 2 * p.slots + static_cast<long long>(at) * S::DV + lane * E - half * S::DV;
-    float x[E];
-#pragma unroll
-    for (int i = 0; i < E; i += V) {
-      if constexpr (V == 2) {
-        const float2 u = *reinterpret_cast<const float2*>(src + i);
-        x[i] = u.x; x[i + 1] = u.y;
-      } else {
-        const float4 u = *reinterpret_cast<const float4*>(src + i);
-        x[i] = u.x; x[i + 1] = u.y; x[i + 2] = u.z; x[i + 3] = u.w;
-      }
-    }
-    merge(rec[at], rec[p.slots + at], x);
-  }
   if constexpr (W > 1) {
 #pragma unroll
     for (int i = 0; i < E; ++i) s_part[warp][i][lane] = o[i];
@@ -952,7 +1048,7 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.N;
   // many partial results a row (few segments, many blocks): four warps a row
-  const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies * S::SW;
+  const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies;
   if (parts >= 8) return launch_pdl_block(tree_combine_kernel<D, 4>, static_cast<int>(rows), 128, p, s, 0);
   return launch_pdl_block(tree_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, p, s, 0);
 }
