@@ -211,7 +211,8 @@ __device__ void weights_matrix(const WeightsParams& p, uint32_t sm, uint8_t* ctl
   using S = WeightsShape<D>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + wcQuit);
   const uint32_t bars = sm + S::C_OFF;
-  const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + wcTmem);
+  constexpr uint32_t tm = 0;  // a block holds all of tensor memory (the kernel checks it)
+  const bool issue = elect_lane();
   WeightsWalk<S::TT, S::NB> w;
   w.init(p, ctl);
   int it = 0, turn = 0;
@@ -219,21 +220,21 @@ __device__ void weights_matrix(const WeightsParams& p, uint32_t sm, uint8_t* ctl
     for (int round = 0; round < w.rounds; ++round, ++turn) {
       const int cols = min(S::NB, p.G * w.obs - round * S::NB);
       const uint32_t kind = mma_kind((cols + 15) & ~15, false, false);
-      if (!wait_or_quit(bars + wcQFull, turn & 1, quit, p.err)) return;
+      if (!warp_wait(bars + wcQFull, turn & 1, quit, p.err)) return;
       const int end = it + w.tiles;
 #pragma unroll 1
       for (; it < end; ++it) {
         const int st = it % S::KS, sb = it & 1;
-        if (it >= 2 && !wait_or_quit(bars + wcSFree + 8 * sb, (it / 2 - 1) & 1, quit, p.err)) return;
-        if (!wait_or_quit(bars + wcKFull + 8 * st, (it / S::KS) & 1, quit, p.err)) return;
+        if (it >= 2 && !warp_wait(bars + wcSFree + 8 * sb, (it / 2 - 1) & 1, quit, p.err)) return;
+        if (!warp_wait(bars + wcKFull + 8 * st, (it / S::KS) & 1, quit, p.err)) return;
         tmem_fence_after();
         const uint64_t a = smem_operand(sm + st * S::K_BYTES, 16, 1024), b = smem_operand(sm + S::Q_OFF, 16, 1024);
 #pragma unroll 4
         for (int ks = 0; ks < D / 16; ++ks)
           mma_ss(tm + 256 * sb, a + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16,
-                 b + ((ks >> 2) * (S::NB * 128) + (ks & 3) * 32) / 16, kind, ks > 0);
-        mma_commit(bars + wcSFull + 8 * sb);
-        mma_commit(bars + wcKEmpty + 8 * st);
+                 b + ((ks >> 2) * (S::NB * 128) + (ks & 3) * 32) / 16, kind, ks > 0, issue);
+        mma_commit(bars + wcSFull + 8 * sb, issue);
+        mma_commit(bars + wcKEmpty + 8 * st, issue);
       }
     }
   }
@@ -366,7 +367,6 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
   uint8_t* ctl = smem + S::C_OFF;
   const uint32_t sm = smem_u32(smem), bars = sm + S::C_OFF;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 16) tmem_alloc(bars + wcTmem, 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + wcKFull + 8 * i, S::DWARPS);
@@ -384,6 +384,14 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
     *reinterpret_cast<int*>(ctl + wcQuit) = 0;
     *reinterpret_cast<int*>(ctl + wcOdd) = 0;
     mbar_fence_init();
+  }
+  __syncthreads();
+  if (warp == 16) {
+    tmem_alloc(bars + wcTmem, 512);
+    if (*reinterpret_cast<const volatile uint32_t*>(ctl + wcTmem) != 0) {  // (cannot be: all of it was asked for)
+      *reinterpret_cast<volatile int*>(ctl + wcQuit) = 1;
+      if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrTimeout);
+    }
   }
   pdl_launch_dependents();
   pdl_wait();
@@ -433,12 +441,10 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
       default: weights_decode<D, kK8Signed>(p, sm, ctl, warp - 8, lane); break;
     }
   } else if (warp == 16) {
-    if (lane == 0) {
-      weights_matrix<D>(p, sm, ctl);
-      if (*reinterpret_cast<volatile int*>(ctl + wcQuit) != 0) {  // gave up: let the matrix work in flight end
-        mma_commit(bars + wcDrain);
-        mbar_wait(bars + wcDrain, 0, kBulkWaitLimit);
-      }
+    weights_matrix<D>(p, sm, ctl);
+    if (*reinterpret_cast<volatile int*>(ctl + wcQuit) != 0) {  // gave up: let the matrix work in flight end
+      mma_commit(bars + wcDrain, elect_lane());
+      mbar_wait(bars + wcDrain, 0, kBulkWaitLimit);
     }
   } else if (warp == 17) {
     weights_load<D>(p, sm, ctl, lane);

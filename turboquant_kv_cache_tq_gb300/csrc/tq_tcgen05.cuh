@@ -116,22 +116,36 @@ constexpr uint32_t mma_kind(int n, bool b_mn_major, bool negate_a) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (negate_a ? 1u << 13 : 0u) | (b_mn_major ? 1u << 16 : 0u) |
          static_cast<uint32_t>(n >> 3) << 17 | 128u >> 4 << 24;
 }
-// One step of 16 along the contraction; A in tensor memory or shared memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+// One step of 16 along the contraction; A in tensor memory or shared memory. A
+// whole warp calls these and one lane (`issue`) issues: with the control flow
+// uniform the operands stay in uniform registers, where the instruction takes
+// them from.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+  return x != 0;
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add, bool issue) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kind), "r"(add ? 1u : 0u), "r"(issue ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add, bool issue) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"(add ? 1u : 0u), "r"(issue ? 1u : 0u)
       : "memory");
 }
-// Arrives at the barrier when this thread's matrix work so far is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Arrives at the barrier when the issuing thread's matrix work so far is done.
+__device__ __forceinline__ void mma_commit(uint32_t bar, bool issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(issue ? 1u : 0u)
+      : "memory");
 }
 
 }  // namespace tq
