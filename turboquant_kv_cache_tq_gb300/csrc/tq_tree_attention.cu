@@ -19,8 +19,7 @@ bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, TreePla
   t->R = Hq / Hkv * N;
   t->RB = (t->R + kTreeRows - 1) / kTreeRows;
   t->rows = (t->R + t->RB - 1) / t->RB;
-  // (a lane's share is 16 tokens at least)
-  t->copies = t->rows > 64 ? 1 : t->rows > 32 || t->TT == 32 ? 2 : 4;
+  t->copies = t->rows > 64 || t->TT == 32 ? 1 : 2;  // (a lane's share is 32 tokens at least)
   t->slots = (t->copies * t->rows + 3) / 4 * 4;
   if (t->RB * (D / t->DV) > lim / Hkv) return false;
   t->HH = Hkv * t->RB * (D / t->DV);

@@ -13,11 +13,11 @@
 // memory. What then bounds the kernel is the decoding itself (see the figures
 // in tree_split_kernel's comment), as in the decode attention of few rows.
 //
-// The rows are padded to 128 lanes of tensor memory. With at most 64 (32) rows
-// each row takes two (four) lanes, and lane copy c takes every tile's c-th half
-// (quarter) of the tokens: its weights for the other tokens are zeros that are
-// written once. So the softmax work is spread over all four warps whatever the
-// number of rows, and each copy is one more partial result for the combine.
+// The rows are padded to 128 lanes of tensor memory. With at most 64 rows (and
+// tiles of 64 tokens) each row takes two lanes, and lane copy c takes every
+// tile's c-th half of the tokens, with zero weights for the other half. So the
+// softmax work is spread over twice the warps, and each copy is one more partial
+// result for the combine.
 //
 // Work split: the tiles of all (batch row, kv head, row block, value half) in
 // one line, cut evenly into one range per SM; a range's part of one
@@ -45,7 +45,7 @@ struct TreeParams {
   long long n_recs;   // records the workspace holds (debug checks)
   int B, Hq, Hkv, G, N, T;
   int R, RB, rows;    // query rows of a kv head, row blocks, rows of a block
-  int copies;         // lanes per row: 1, 2 or 4
+  int copies;         // lanes per row: 1 or 2
   int slots;          // rows a record holds (copies * rows, a multiple of 4)
   int HH;             // segments of a batch row: Hkv * RB * value halves
   int kmode, vb, out_f32, grid;
@@ -381,13 +381,15 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
   }
 }
 
-// The scores' thread: S = Q K^T, tile after tile.
+// The scores' warp: S = Q K^T, tile after tile. (A block holds all of tensor
+// memory, so its first column is column 0; the kernel checks that.)
 template <int D>
 __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
   using S = TreeShape<D>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
-  const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem);
+  constexpr uint32_t tm = 0;
+  const bool issue = elect_lane();
   const uint32_t kind = mma_kind(S::TT, false, p.negate != 0);
   TreeWalk<D> w;
   w.init(p, ctl);
@@ -396,42 +398,43 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
     const int end = it + min(w.left, w.n - w.tile);
     w.left -= end - it;
     w.next_segment(p);
-    if (!wait_or_quit(bars + kcQFull, seg & 1, quit, p.err)) return;
+    if (!warp_wait(bars + kcQFull, seg & 1, quit, p.err)) return;
 #pragma unroll 1
     for (; it < end; ++it) {
       const int sb = it % S::NS;
       // the weights that took the scores' place are used
-      if (it >= S::NS && !wait_or_quit(bars + kcPFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
+      if (it >= S::NS && !warp_wait(bars + kcPFree + 8 * sb, (it / S::NS - 1) & 1, quit, p.err)) return;
 #pragma unroll 1
       for (int sub = 0; sub < S::SUBS; ++sub) {
         const int part = it * S::SUBS + sub, st = part % S::KS;
         const uint64_t k0 = smem_operand(sm + st * S::K_BYTES, 16, 1024);
-        if (!wait_or_quit(bars + kcKFull + 8 * st, (part / S::KS) & 1, quit, p.err)) return;
+        if (!warp_wait(bars + kcKFull + 8 * st, (part / S::KS) & 1, quit, p.err)) return;
         tmem_fence_after();
 #pragma unroll
         for (int ks = 0; ks < S::DS / 16; ++ks) {
           // (operand addresses count 16 bytes)
           const uint64_t b = k0 + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16;
-          if (sub == 0) mma_ts(tm + S::S_COL + sb * S::TT, tm + S::Q_COL + 8 * ks, b, kind, ks > 0);
+          if (sub == 0) mma_ts(tm + S::S_COL + sb * S::TT, tm + S::Q_COL + 8 * ks, b, kind, ks > 0, issue);
           else
             mma_ss(tm + S::S_COL + sb * S::TT,
-                   smem_operand(sm + S::Q_OFF, 16, 1024) + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16, b, kind, true);
+                   smem_operand(sm + S::Q_OFF, 16, 1024) + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16, b, kind, true, issue);
         }
-        mma_commit(bars + kcKEmpty + 8 * st);
+        mma_commit(bars + kcKEmpty + 8 * st, issue);
       }
-      mma_commit(bars + kcSFull + 8 * sb);
+      mma_commit(bars + kcSFull + 8 * sb, issue);
     }
   }
 }
 
-// The weighted values' thread: O += P V, the weights as a high part and a
+// The weighted values' warp: O += P V, the weights as a high part and a
 // remainder to subtract.
 template <int D>
 __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
   using S = TreeShape<D>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
-  const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem);
+  constexpr uint32_t tm = 0;
+  const bool issue = elect_lane();
   constexpr uint32_t kind = mma_kind(S::DV, true, false), kind_rest = mma_kind(S::DV, true, true);
   TreeWalk<D> w;
   w.init(p, ctl);
@@ -445,16 +448,16 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
       const int st = it % S::VS, sb = it % S::NS;
       const uint64_t v0 = smem_operand(sm + S::V_OFF + st * S::V_BYTES, S::TT * 128, 1024);
       const uint32_t pc = tm + S::S_COL + sb * S::TT, o = tm + S::O_COL + (it % S::SW) * S::DV;
-      if (!wait_or_quit(bars + kcVFull + 8 * st, (it / S::VS) & 1, quit, p.err)) return;
-      if (!wait_or_quit(bars + kcPFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
+      if (!warp_wait(bars + kcVFull + 8 * st, (it / S::VS) & 1, quit, p.err)) return;
+      if (!warp_wait(bars + kcPFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
       tmem_fence_after();
 #pragma unroll
       for (int ks = 0; ks < S::TT / 16; ++ks) {
-        mma_ts(o, pc + 16 * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0);
-        mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind_rest, true);
+        mma_ts(o, pc + 16 * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0, issue);
+        mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind_rest, true, issue);
       }
-      mma_commit(bars + kcPFree + 8 * sb);
-      mma_commit(bars + kcVEmpty + 8 * st);
+      mma_commit(bars + kcPFree + 8 * sb, issue);
+      mma_commit(bars + kcVEmpty + 8 * st, issue);
     }
   }
 }
@@ -483,7 +486,7 @@ template <int D>
 __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int which, int warp, int lane) {
   using S = TreeShape<D>;
   constexpr int TT = S::TT;
-  const int W = TT / p.copies;         // tokens of a tile that this lane takes: 16, 32 or 64
+  const int W = TT / p.copies;         // tokens of a tile that this lane takes: 32 or 64
   const int QUADS = 4 / p.copies;      // warps per copy
   const float kNegInf = -__int_as_float(0x7f800000);
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
@@ -758,7 +761,6 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
     case 5: fill_value_table<5>(smem + S::T_OFF); break;
     default: fill_value_table<8>(smem + S::T_OFF); break;
   }
-  if (warp == 20) tmem_alloc(bars + kcTmem, 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + kcKFull + 8 * i, S::KWARPS);
@@ -784,6 +786,14 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
     *reinterpret_cast<int*>(ctl + kcQuit) = 0;
     *reinterpret_cast<int*>(ctl + kcAnyBad) = 0;
     mbar_fence_init();
+  }
+  __syncthreads();
+  if (warp == 20) {
+    tmem_alloc(bars + kcTmem, 512);
+    if (*reinterpret_cast<const volatile uint32_t*>(ctl + kcTmem) != 0) {  // (cannot be: all of it was asked for)
+      *reinterpret_cast<volatile int*>(ctl + kcQuit) = 1;
+      if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrTimeout);
+    }
   }
   pdl_launch_dependents();
   pdl_wait();
@@ -833,13 +843,16 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  // Registers per thread, in all those of the launch: one softmax group
-  // 88 + 4 * 88 + 40 = 6 * 80, two 2 * 88 + 4 * 72 + 40 = 7 * 72.
+  // Registers a thread, in all those of the launch: two softmax groups
+  // 2 * 104 + 4 * 56 + 72 = 7 * 72, one 120 + 4 * 72 + 72 = 6 * 80. Nothing
+  // spills.
   if (warp < 4 || warp >= 24) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    if constexpr (S::SW == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     tree_softmax<D>(p, sm, smem, ctl, warp >= 24 ? 1 : 0, warp & 3, lane);
   } else if (warp < 20) {
-    if constexpr (S::SW == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    if constexpr (S::SW == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int warp8 = (warp - 4) / 4 * 2 + (warp & 1);
     if ((warp & 2) == 0) {
       switch (p.kmode) {
@@ -859,16 +872,16 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (S::SW == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 22) {
       tree_load<D, true>(p, sm, smem, ctl, lane);
     } else if (warp == 23) {
       tree_load<D, false>(p, sm, smem, ctl, lane);
-    } else if (lane == 0) {
+    } else {
       if (warp == 20) tree_scores<D>(p, sm, ctl);
       else tree_weigh<D>(p, sm, ctl);
       if (*reinterpret_cast<volatile int*>(ctl + kcQuit) != 0) {  // gave up: let the matrix work in flight end
-        mma_commit(bars + kcDrain + 8 * (warp - 20));
+        mma_commit(bars + kcDrain + 8 * (warp - 20), elect_lane());
         mbar_wait(bars + kcDrain + 8 * (warp - 20), 0, kBulkWaitLimit);
       }
     }
