@@ -384,25 +384,51 @@ class TQPackedCache(ctypes.Structure):
 _BUFFERS = ("k_codes", "k_scales", "k_zeros", "v_codes", "v_scales")
 
 
-def _cache_shape(cache: dict, B, H, D, k_bits, v_bits, device, names=_BUFFERS) -> int:
-    """Checks the buffers of a packed cache [B,H,t_cap,X]; returns t_cap."""
+def _refuse_cache(cache, B, H, D, k_bits, v_bits, device, names):
     t_cap = cache["k_codes"].shape[2] if cache["k_codes"].dim() == 4 else -1
-    G = D // GROUP
     for name in names:
         t = cache[name]
-        x = G if name[2:] in ("scales", "zeros") else D * (k_bits if name == "k_codes" else v_bits) // 8
+        x = D // GROUP if name[2:] in ("scales", "zeros") else D * (k_bits if name == "k_codes" else v_bits) // 8
         dtype = torch.uint8 if name[2:] == "codes" else torch.float16
         if t.dtype != dtype or tuple(t.shape) != (B, H, t_cap, x) or not t.is_contiguous() or t.device != device:
             raise ValueError("cache buffer %s must be a contiguous [%d,%d,t_cap,%d] %s tensor on %s"
                              % (name, B, H, x, dtype, device))
-    return t_cap
+    raise ValueError("not a packed cache on %s" % device)
+
+
+def _keys_ok(cache, B, H, D, k_bits, dev):
+    """The key buffers, or None where they are not [B,H,t_cap,X] on GPU dev."""
+    c, s, z = cache["k_codes"], cache["k_scales"], cache["k_zeros"]
+    if c.dim() != 4:
+        return None
+    t_cap = c.shape[2]
+    g = (B, H, t_cap, D // GROUP)
+    if (c.shape == (B, H, t_cap, D * k_bits // 8) and s.shape == g and z.shape == g and c.dtype is torch.uint8
+            and s.dtype is torch.float16 and z.dtype is torch.float16 and c.is_contiguous() and s.is_contiguous()
+            and z.is_contiguous() and c.get_device() == dev and s.get_device() == dev and z.get_device() == dev):
+        return c, s, z, t_cap
+    return None
+
+
+def _packed(cache: dict, B, H, D, k_bits, v_bits, device) -> TQPackedCache:
+    """The checked buffers of a packed cache as the library takes them."""
+    dev = device.index
+    keys = _keys_ok(cache, B, H, D, k_bits, dev)
+    if keys is not None:
+        c, s, z, t_cap = keys
+        v, w = cache["v_codes"], cache["v_scales"]
+        if (v.shape == (B, H, t_cap, D * v_bits // 8) and w.shape == s.shape and v.dtype is torch.uint8
+                and w.dtype is torch.float16 and v.is_contiguous() and w.is_contiguous() and v.get_device() == dev
+                and w.get_device() == dev):
+            return TQPackedCache(c.data_ptr(), s.data_ptr(), z.data_ptr(), v.data_ptr(), w.data_ptr(), t_cap)
+    _refuse_cache(cache, B, H, D, k_bits, v_bits, device, _BUFFERS)
 
 
 def _int_ptr(t, shape, what, device):
     """Device pointer of an optional int32 tensor of a given shape."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be a contiguous int32 tensor %s on %s" % (what, list(shape), device))
     return t.data_ptr()
 
@@ -410,13 +436,9 @@ def _int_ptr(t, shape, what, device):
 def _float_ptr(t, shape, what, device):
     if t is None:
         return None
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be a contiguous float32 tensor %s on %s" % (what, list(shape), device))
     return t.data_ptr()
-
-
-def _view(cache: dict, t_cap: int) -> TQPackedCache:
-    return TQPackedCache(*(cache[n].data_ptr() for n in _BUFFERS), t_cap)
 
 
 @contextlib.contextmanager
@@ -425,16 +447,18 @@ def _switched(device, stream):
         yield
 
 
-def _launching(device, stream):
-    """A context for allocations and one or more calls: the tensors' device is
-    current (the library asks the current device for its size and error word)
-    and so is the stream the work goes to (the allocator gives memory back in
-    that stream's order)."""
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to switch to another device or stream than the current
+    one: for its allocations (the allocator gives memory back in the current
+    stream's order) and because the library asks the current device for its size
+    and error word."""
     if device.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device, got %s" % device)
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _switched(device, stream)
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _current_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def tq_tree_attention_workspace_size(B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
@@ -460,30 +484,33 @@ def tq_tree_attention(q: torch.Tensor, cache: dict, T: int, tree: dict, k_bits: 
         raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
     if out_dtype not in _DTYPE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    B, Hq, N, D = q.shape
     dev = q.device
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_tree_attention(q, cache, T, tree, k_bits, k_signed, v_bits, parents, lens, left_pad, scale,
+                                     out_dtype, out, lse, workspace)
+    B, Hq, N, D = q.shape
     Hkv = cache["k_codes"].shape[1]
-    views = []
-    for c in (cache, tree):
-        views.append(_view(c, _cache_shape(c, B, Hkv, D, k_bits, v_bits, dev)))
-    parents_p = _int_ptr(parents, (B, N), "parents", dev)
-    lens_p, pad_p = _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev)
-    if out is not None and (out.dtype != out_dtype or out.shape != q.shape or not out.is_contiguous()
-                            or out.device != dev):
+    cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
+    tv = _packed(tree, B, Hkv, D, k_bits, v_bits, dev)
+    if out is None:
+        out = torch.empty((B, Hq, N, D), dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous [B,Hq,N,D] tensor of out_dtype on q's device")
-    with _launching(dev, stream):
-        if out is None:
-            out = torch.empty((B, Hq, N, D), dtype=out_dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev)
-        if workspace is None:
-            need = tq_tree_attention_workspace_size(B, Hq, Hkv, N, D)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        st = lib().tq_tree_attention(
-            q.data_ptr(), B, Hq, N, ctypes.byref(views[0]), Hkv, int(T), D, ctypes.byref(views[1]), parents_p,
-            int(k_bits), int(bool(k_signed)), int(v_bits), lens_p, pad_p, D ** -0.5 if scale is None else float(scale),
-            out.data_ptr(), _DTYPE[out_dtype], _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    if lse is None:
+        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = tq_tree_attention_workspace_size(B, Hq, Hkv, N, D)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    st = lib().tq_tree_attention(
+        q.data_ptr(), B, Hq, N, ctypes.byref(cv), Hkv, int(T), D, ctypes.byref(tv),
+        _int_ptr(parents, (B, N), "parents", dev), int(k_bits), int(bool(k_signed)), int(v_bits),
+        _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
+        D ** -0.5 if scale is None else float(scale), out.data_ptr(), _DTYPE[out_dtype],
+        _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _current_stream(dev))
     _check(st, "tq_tree_attention")
     return out, lse
 
@@ -500,23 +527,28 @@ def tq_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: dict, T: int
     in place."""
     if q.dtype != torch.bfloat16 or q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
-    B, Hq, N, D = q.shape
     dev = q.device
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_attention_weights(q, lse, cache, T, k_bits, k_signed, path, n_path, lens, left_pad, scale,
+                                        weights, out)
+    B, Hq, N, D = q.shape
     Hkv = cache["k_codes"].shape[1]
-    t_cap = _cache_shape(cache, B, Hkv, D, k_bits, 0, dev, _BUFFERS[:3])
+    keys = _keys_ok(cache, B, Hkv, D, k_bits, dev.index)
+    if keys is None:
+        _refuse_cache(cache, B, Hkv, D, k_bits, 0, dev, _BUFFERS[:3])
     P = N if path is None else path.shape[-1]
-    with _launching(dev, stream):
-        if out is None:
-            w_cap = int(T) if weights is None else weights.shape[-1]
-            out = torch.empty((B, Hkv, w_cap), dtype=torch.float32, device=dev)
-        w_cap = out.shape[-1]
-        st = lib().tq_attention_weights(
-            q.data_ptr(), _float_ptr(lse, (B, Hq, N), "lse", dev), B, Hq, N, cache["k_codes"].data_ptr(),
-            cache["k_scales"].data_ptr(), cache["k_zeros"].data_ptr(), Hkv, int(T), D, t_cap, int(k_bits),
-            int(bool(k_signed)), _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
-            _int_ptr(path, (B, P), "path", dev), _int_ptr(n_path, (B,), "n_path", dev), P,
-            D ** -0.5 if scale is None else float(scale), _float_ptr(weights, (B, Hkv, w_cap), "weights", dev),
-            _float_ptr(out, (B, Hkv, w_cap), "out", dev), w_cap, _stream_handle(stream, dev))
+    if out is None:
+        w_cap = int(T) if weights is None else weights.shape[-1]
+        out = torch.empty((B, Hkv, w_cap), dtype=torch.float32, device=dev)
+    w_cap = out.shape[-1]
+    st = lib().tq_attention_weights(
+        q.data_ptr(), _float_ptr(lse, (B, Hq, N), "lse", dev), B, Hq, N, keys[0].data_ptr(), keys[1].data_ptr(),
+        keys[2].data_ptr(), Hkv, int(T), D, keys[3], int(k_bits), int(bool(k_signed)),
+        _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
+        _int_ptr(path, (B, P), "path", dev), _int_ptr(n_path, (B,), "n_path", dev), P,
+        D ** -0.5 if scale is None else float(scale), _float_ptr(weights, (B, Hkv, w_cap), "weights", dev),
+        _float_ptr(out, (B, Hkv, w_cap), "out", dev), w_cap, _current_stream(dev))
     _check(st, "tq_attention_weights")
     return out
 
@@ -529,20 +561,22 @@ def tq_evict_select(weights: torch.Tensor, T: int, keep: int, recent: int, lens=
     ascending, then -1; count int32 [B])."""
     if weights.dim() != 3:
         raise ValueError("weights must be a [B,H,w_cap] tensor")
-    B, H, w_cap = weights.shape
-    dev = weights.device
     if keep < 0:
         raise ValueError("keep must not be negative")
-    with _launching(dev, stream):
-        if index is None:
-            index = torch.empty((B, H, int(keep)), dtype=torch.int32, device=dev)
-        if count is None:
-            count = torch.empty((B,), dtype=torch.int32, device=dev)
-        st = lib().tq_evict_select(
-            _float_ptr(weights, (B, H, w_cap), "weights", dev), B, H, int(T), w_cap, _int_ptr(lens, (B,), "lens", dev),
-            _int_ptr(left_pad, (B,), "left_pad", dev), int(keep), int(recent),
-            _int_ptr(index, (B, H, int(keep)), "index", dev), _int_ptr(count, (B,), "count", dev),
-            _stream_handle(stream, dev))
+    dev = weights.device
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_evict_select(weights, T, keep, recent, lens, left_pad, index, count)
+    B, H, w_cap = weights.shape
+    keep = int(keep)
+    if index is None:
+        index = torch.empty((B, H, keep), dtype=torch.int32, device=dev)
+    if count is None:
+        count = torch.empty((B,), dtype=torch.int32, device=dev)
+    st = lib().tq_evict_select(
+        _float_ptr(weights, (B, H, w_cap), "weights", dev), B, H, int(T), w_cap, _int_ptr(lens, (B,), "lens", dev),
+        _int_ptr(left_pad, (B,), "left_pad", dev), keep, int(recent), _int_ptr(index, (B, H, keep), "index", dev),
+        _int_ptr(count, (B,), "count", dev), _current_stream(dev))
     _check(st, "tq_evict_select")
     return index, count
 
@@ -553,22 +587,22 @@ def tq_cache_gather(src: dict, dst: dict, index: torch.Tensor, count=None, dst_o
     tokens dst_off[b] + j, j < count[b], of dst (with their weights, or zero
     weights, when dst_weights is given). Returns (dst, dst_len), dst_len int32
     [B] = min(dst_off + count, capacity)."""
-    B, H, _, D, kb, vb = _cache_geometry(src)
     dev = src["k_codes"].device
-    s_cap = _cache_shape(src, B, H, D, kb, vb, dev)
-    d_cap = _cache_shape(dst, B, H, D, kb, vb, dev)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_cache_gather(src, dst, index, count, dst_off, src_weights, dst_weights, dst_len)
+    B, H, _, D, kb, vb = _cache_geometry(src)
+    sv, dv = _packed(src, B, H, D, kb, vb, dev), _packed(dst, B, H, D, kb, vb, dev)
     heads = index.dim() == 3
     n = index.shape[-1]
-    sv, dv = _view(src, s_cap), _view(dst, d_cap)
-    with _launching(dev, stream):
-        if dst_len is None:
-            dst_len = torch.empty((B,), dtype=torch.int32, device=dev)
-        st = lib().tq_cache_gather(
-            ctypes.byref(sv), ctypes.byref(dv), B, H, D, kb, vb,
-            _int_ptr(index, (B, H, n) if heads else (B, n), "index", dev), n, int(heads),
-            _int_ptr(count, (B,), "count", dev), _int_ptr(dst_off, (B,), "dst_off", dev),
-            _int_ptr(dst_len, (B,), "dst_len", dev), _float_ptr(src_weights, (B, H, s_cap), "src_weights", dev),
-            _float_ptr(dst_weights, (B, H, d_cap), "dst_weights", dev), _stream_handle(stream, dev))
+    if dst_len is None:
+        dst_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    st = lib().tq_cache_gather(
+        ctypes.byref(sv), ctypes.byref(dv), B, H, D, kb, vb,
+        _int_ptr(index, (B, H, n) if heads else (B, n), "index", dev), n, int(heads),
+        _int_ptr(count, (B,), "count", dev), _int_ptr(dst_off, (B,), "dst_off", dev),
+        _int_ptr(dst_len, (B,), "dst_len", dev), _float_ptr(src_weights, (B, H, sv.t_cap), "src_weights", dev),
+        _float_ptr(dst_weights, (B, H, dv.t_cap), "dst_weights", dev), _current_stream(dev))
     _check(st, "tq_cache_gather")
     return dst, dst_len
 
@@ -589,11 +623,13 @@ def evict_rows(cache: dict, weights: torch.Tensor, T: int, keep: int, recent: in
     B, H, cap = cache["k_codes"].shape[:3]
     if weights.shape[-1] != cap:
         raise ValueError("weights must be [B,H,%d], the cache's capacity" % cap)
-    with _launching(weights.device, stream):
-        dst = _alloc_like(cache, B, keep if t_cap is None else t_cap)
-        new = torch.zeros((B, H, dst["k_codes"].shape[2]), dtype=torch.float32, device=weights.device)
-        index, count = tq_evict_select(weights, T, keep, recent, lens=lens, left_pad=left_pad)
-        _, length = tq_cache_gather(cache, dst, index, count=count, src_weights=weights, dst_weights=new)
+    if _elsewhere(weights.device, stream):
+        with _switched(weights.device, stream):
+            return evict_rows(cache, weights, T, keep, recent, lens, left_pad, t_cap)
+    dst = _alloc_like(cache, B, keep if t_cap is None else t_cap)
+    new = torch.zeros((B, H, dst["k_codes"].shape[2]), dtype=torch.float32, device=weights.device)
+    index, count = tq_evict_select(weights, T, keep, recent, lens=lens, left_pad=left_pad)
+    _, length = tq_cache_gather(cache, dst, index, count=count, src_weights=weights, dst_weights=new)
     return dst, new, length
 
 

@@ -12,8 +12,23 @@ namespace {
 // k-th largest key comes from a radix selection, eight bits a pass from the
 // top: a histogram of the next digit over the keys that agree with the prefix
 // found so far, then the digit in which the k-th largest lies. What stays is
-// every key above it and, of the keys equal to it, the first ones.
-constexpr int kSelectThreads = 1024;
+// every key above it and, of the keys equal to it, the first ones: a kept
+// token's place is (keys above before it) + min(equal keys before it, places
+// left for equal ones).
+//
+// The kernel reads each weight once, so its floor is that read; what it spends
+// is latency (four passes over keys in shared memory and their barriers). So a
+// row belongs to a cluster of 1 to 8 blocks, each with a slice of its keys in
+// shared memory, whose histograms and counts meet through distributed shared
+// memory. The histogram is kept once per half-warp lane (bin b of lane L at
+// 16 b + L % 16): two lanes of a warp meet at most, whatever the keys (sums of
+// attention weights have many equal ones, zeros above all). Measured, 256 rows
+// of up to 8192 tokens: one histogram a block and 1024 threads 40 us, a copy a
+// lane 24 (1024 threads) and 19 us (512).
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectCopies = 16;    // of the histogram
+constexpr int kSelectKeys = 16384;  // of a slice that shared memory holds; a longer one is read again each pass
+constexpr int kSelectSlice = 8192;  // keys of a block before a row gets more blocks
 
 struct SelectParams {
   const float* w;
@@ -23,6 +38,8 @@ struct SelectParams {
   int* count;
   long long w_cap;
   int B, H, T, keep, recent;
+  int cluster;    // blocks per row
+  int held;       // keys of a slice in shared memory: all (slice <= kSelectKeys) or none
 };
 
 __device__ __forceinline__ uint32_t rank_key(float x) {
@@ -32,46 +49,106 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(SelectParams p) {
-  __shared__ int s_hist[256];
-  __shared__ int s_warp[2][kSelectThreads / 32];
+__device__ __forceinline__ void cluster_sync(int cluster) {
+  if (cluster > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+// The word at shared address a of block `rank` of the cluster.
+__device__ __forceinline__ int cluster_read(uint32_t a, int rank, int cluster) {
+  int v;
+  if (cluster > 1) {
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
+                 : "=r"(v)
+                 : "r"(a), "r"(rank)
+                 : "memory");
+  } else {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ int select_smem[];
+  int* s_hist = select_smem;                       // [256][kSelectCopies]
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(select_smem + 256 * kSelectCopies);
+  __shared__ int s_bins[2][256];                   // this block's digit counts, by pass parity
   __shared__ int s_digit, s_left;
+  __shared__ int s_warp[2][kSelectWarps];          // above and equal keys of each warp's part
+  __shared__ int s_total[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long bh = blockIdx.x;
+  const int rank = static_cast<int>(blockIdx.x % p.cluster);
+  const long long bh = blockIdx.x / p.cluster;
   const int b = static_cast<int>(bh / p.H);
   int lo, hi;
   row_range(p.lens, p.left_pad, b, p.T, lo, hi);
   const int n = hi - lo;
   const int kept = min(n, p.keep);
-  if (tid == 0 && bh % p.H == 0) p.count[b] = kept;
+  if (tid == 0 && rank == 0 && bh % p.H == 0) p.count[b] = kept;
   if (p.keep == 0) return;
   int* out = p.index + bh * p.keep;
-  for (int j = kept + tid; j < p.keep; j += kSelectThreads) out[j] = -1;
+  const int all = p.cluster * kSelectThreads, at = rank * kSelectThreads + tid;
+  for (int j = kept + at; j < p.keep; j += all) out[j] = -1;
   if (n <= p.keep) {
-    for (int j = tid; j < n; j += kSelectThreads) out[j] = lo + j;
+    for (int j = at; j < n; j += all) out[j] = lo + j;
     return;
   }
   const float* w = p.w + bh * p.w_cap;
   const int rest = hi - p.recent;  // tokens [lo, rest) compete for k places
   const int k = p.keep - p.recent;
-  for (int j = tid; j < p.recent; j += kSelectThreads) out[k + j] = rest + j;
+  for (int j = at; j < p.recent; j += all) out[k + j] = rest + j;
   if (k == 0) return;
+  // this block's slice [t0, t1), a warp's part a run of it
+  const int slice = (rest - lo + p.cluster - 1) / p.cluster;
+  const int t0 = min(lo + rank * slice, rest), m = min(slice, rest - t0);
+  const int part = (m + kSelectWarps - 1) / kSelectWarps;
+  const int w0 = min(warp * part, m), w1 = min(w0 + part, m);
+  const int copy = lane % kSelectCopies;
   uint32_t prefix = 0;
   int left = k;  // places left among the keys that agree with the prefix
 #pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
+  for (int shift = 24, pass = 0; shift >= 0; shift -= 8, ++pass) {
+    for (int i = tid; i < 64 * kSelectCopies; i += kSelectThreads) reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int t = lo + tid; t < rest; t += kSelectThreads) {
-      const uint32_t key = rank_key(w[t]);
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[key >> shift & 255u], 1);
+    if (pass == 0) {
+#pragma unroll 4
+      for (int i = tid; i < m; i += kSelectThreads) {
+        const uint32_t key = rank_key(__ldg(w + t0 + i));
+        if (p.held) s_key[i] = key;
+        atomicAdd(&s_hist[(key >> 24) * kSelectCopies + copy], 1);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < m; i += kSelectThreads) {
+        const uint32_t key = p.held ? s_key[i] : rank_key(__ldg(w + t0 + i));
+        if ((key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(key >> shift & 255u) * kSelectCopies + copy], 1);
+      }
     }
     __syncthreads();
+    // two threads a bin add up its copies
+    {
+      static_assert(kSelectCopies == 16 && kSelectThreads == 512, "eight counts a thread");
+      const int4* h = reinterpret_cast<const int4*>(s_hist) + 2 * tid;
+      const int4 u = h[0], v = h[1];
+      int c = u.x + u.y + u.z + u.w + v.x + v.y + v.z + v.w;
+      c += __shfl_xor_sync(kFull, c, 1);
+      if ((tid & 1) == 0) s_bins[pass & 1][tid >> 1] = c;
+    }
+    cluster_sync(p.cluster);
     if (warp == 0) {
       // lane L takes digits 255 - 8 L .. 248 - 8 L, from the top
+      const uint32_t bins = static_cast<uint32_t>(__cvta_generic_to_shared(&s_bins[pass & 1][0]));
       int c[8], sum = 0;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) sum += c[x] = s_hist[255 - 8 * lane - x];
+      for (int x = 0; x < 8; ++x) c[x] = 0;
+      for (int r = 0; r < p.cluster; ++r) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) c[x] += cluster_read(bins + (255 - 8 * lane - x) * 4, r, p.cluster);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sum += c[x];
       int above = sum;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
@@ -80,9 +157,17 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(SelectPara
       }
       above -= sum;
       if (above < left && above + sum >= left) {
-        int a = above, x = 0;
-        while (a + c[x] < left) a += c[x++];
-        s_digit = 255 - 8 * lane - x;
+        int a = above, d = 255 - 8 * lane;
+        bool found = false;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          if (!found && a + c[x] >= left) {
+            found = true;
+            d -= x;
+          }
+          if (!found) a += c[x];
+        }
+        s_digit = d;
         s_left = left - a;
       }
     }
@@ -90,46 +175,67 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(SelectPara
     prefix |= static_cast<uint32_t>(s_digit) << shift;
     left = s_left;
   }
-  // tokens in order: a key above the k-th stays, an equal one while `left` lasts
-  int placed = 0, equals = 0;
-  for (int t0 = lo; t0 < rest; t0 += kSelectThreads) {
-    const int t = t0 + tid;
-    const uint32_t key = t < rest ? rank_key(w[t]) : 0u;
-    const bool above = t < rest && key > prefix, equal = t < rest && key == prefix;
-    const unsigned be = __ballot_sync(kFull, equal), below = (1u << lane) - 1u;
-    if (lane == 0) s_warp[0][warp] = __popc(be);
-    __syncthreads();
-    int before = equals, total = 0;
-    for (int x = 0; x < kSelectThreads / 32; ++x) {
-      const int c = s_warp[0][x];
-      before += x < warp ? c : 0;
-      total += c;
-    }
-    equals += total;
-    const bool stays = above || (equal && before + __popc(be & below) < left);
-    const unsigned bs = __ballot_sync(kFull, stays);
-    if (lane == 0) s_warp[1][warp] = __popc(bs);
-    __syncthreads();
-    int at = placed;
-    total = 0;
-    for (int x = 0; x < kSelectThreads / 32; ++x) {
-      const int c = s_warp[1][x];
-      at += x < warp ? c : 0;
-      total += c;
-    }
-    placed += total;
-    if (stays) out[at + __popc(bs & below)] = t;
+  // counts of the warps' parts, then of the lower blocks
+  auto key_at = [&](int i) { return p.held ? s_key[i] : rank_key(__ldg(w + t0 + i)); };
+  int above = 0, equal = 0;
+#pragma unroll 4
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
+    above += __popc(__ballot_sync(kFull, i + lane < w1 && key > prefix));
+    equal += __popc(__ballot_sync(kFull, i + lane < w1 && key == prefix));
   }
+  if (lane == 0) {
+    s_warp[0][warp] = above;
+    s_warp[1][warp] = equal;
+  }
+  __syncthreads();
+  if (tid < 2) {
+    int t = 0;
+    for (int x = 0; x < kSelectWarps; ++x) t += s_warp[tid][x];
+    s_total[tid] = t;
+  }
+  cluster_sync(p.cluster);
+  above = equal = 0;
+  const uint32_t totals = static_cast<uint32_t>(__cvta_generic_to_shared(&s_total[0]));
+  for (int r = 0; r < rank; ++r) {
+    above += cluster_read(totals, r, p.cluster);
+    equal += cluster_read(totals + 4, r, p.cluster);
+  }
+  for (int x = 0; x < warp; ++x) {
+    above += s_warp[0][x];
+    equal += s_warp[1][x];
+  }
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll 2
+  for (int i = w0; i < w1; i += 32) {
+    const bool real = i + lane < w1;
+    const uint32_t key = real ? key_at(i + lane) : 0u;
+    const unsigned ba = __ballot_sync(kFull, real && key > prefix), be = __ballot_sync(kFull, real && key == prefix);
+    const int a = above + __popc(ba & below), e = equal + __popc(be & below);
+    if (real && (key > prefix || (key == prefix && e < left))) out[a + min(e, left)] = t0 + i + lane;
+    above += __popc(ba);
+    equal += __popc(be);
+  }
+  cluster_sync(p.cluster);  // no block leaves while another may read its counts
 }
 
 // ---- copy -----------------------------------------------------------------------
+// A token is a row of each of the five buffers, cut into pieces as wide as the
+// row's alignment allows (16, 8 or 4 bytes). A block moves kGatherTokens tokens
+// in rounds; in each a thread has the loads of two pieces of key codes, one of
+// value codes and one of the scales on their way before it stores the first:
+// bytes in flight are what a copy from scattered rows lives on. (One list of all
+// pieces, four a thread: 68 us for the long-context compaction; one buffer after
+// another: 59 us.)
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 64;  // tokens of one (batch row, head) per block
 
 struct GatherParams {
   const uint8_t* src[5];
   uint8_t* dst[5];
-  int X[5];  // bytes of one token row of each buffer
+  int X[5];           // bytes of one token row of each buffer
+  int per[3];         // pieces of a row of key codes, value codes, scales
+  unsigned inv[3];    // 2^20 / per + 1: i / per for i < 64 per (per <= 64)
   const int* index;
   const int* count;
   const int* dst_off;
@@ -142,18 +248,26 @@ struct GatherParams {
 };
 
 template <typename V>
-__device__ __forceinline__ void copy_tokens(const uint8_t* src, uint8_t* dst, int X, int m, const int* s_from,
-                                            const int* s_to) {
-  const int pieces = X / static_cast<int>(sizeof(V));
-  for (int i = threadIdx.x; i < m * pieces; i += kGatherThreads) {
-    const int j = i / pieces, c = i - j * pieces;
-    const long long from = s_from[j], to = s_to[j];
-    if (from >= 0)
-      *reinterpret_cast<V*>(dst + to * X + c * sizeof(V)) = *reinterpret_cast<const V*>(src + from * X + c * sizeof(V));
+struct Piece {
+  V v;
+  V* to;
+  __device__ __forceinline__ void load(const uint8_t* src, uint8_t* dst, int X, int i, int pieces, int per, unsigned inv,
+                                       const int* s_from, const int* s_to) {
+    to = nullptr;
+    if (i >= pieces) return;
+    const int j = static_cast<int>(i * inv >> 20), at = (i - j * per) * static_cast<int>(sizeof(V));
+    const int from = s_from[j];
+    if (from < 0) return;
+    v = __ldg(reinterpret_cast<const V*>(src + static_cast<long long>(from) * X + at));
+    to = reinterpret_cast<V*>(dst + static_cast<long long>(s_to[j]) * X + at);
   }
-}
+  __device__ __forceinline__ void store() const {
+    if (to != nullptr) *to = v;
+  }
+};
 
-__global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(GatherParams p) {
+template <typename VK, typename VV, typename VS>
+__global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const __grid_constant__ GatherParams p) {
   __shared__ int s_from[kGatherTokens], s_to[kGatherTokens];
   const long long bh = blockIdx.x / p.chunks;
   const int chunk = static_cast<int>(blockIdx.x - bh * p.chunks);
@@ -172,19 +286,35 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(GatherPara
     const bool ok = from >= 0 && from < p.s_cap && to < p.d_cap;
     s_from[threadIdx.x] = ok ? from : -1;
     s_to[threadIdx.x] = ok ? static_cast<int>(to) : 0;
+    if (ok && p.dst_w != nullptr)
+      p.dst_w[bh * p.d_cap + to] = p.src_w != nullptr ? p.src_w[bh * p.s_cap + from] : 0.0f;
   }
   __syncthreads();
-#pragma unroll 1
+  const uint8_t* src[5];
+  uint8_t* dst[5];
+#pragma unroll
   for (int k = 0; k < 5; ++k) {
-    const int X = p.X[k];
-    const uint8_t* src = p.src[k] + bh * p.s_cap * X;
-    uint8_t* dst = p.dst[k] + bh * p.d_cap * X;
-    if (X % 16 == 0) copy_tokens<uint4>(src, dst, X, m, s_from, s_to);
-    else if (X % 8 == 0) copy_tokens<uint2>(src, dst, X, m, s_from, s_to);
-    else copy_tokens<uint32_t>(src, dst, X, m, s_from, s_to);
+    src[k] = p.src[k] + bh * p.s_cap * p.X[k];
+    dst[k] = p.dst[k] + bh * p.d_cap * p.X[k];
   }
-  if (p.dst_w != nullptr && threadIdx.x < m && s_from[threadIdx.x] >= 0)
-    p.dst_w[bh * p.d_cap + s_to[threadIdx.x]] = p.src_w != nullptr ? p.src_w[bh * p.s_cap + s_from[threadIdx.x]] : 0.0f;
+  const int nk = m * p.per[0], nv = m * p.per[1], ns = m * p.per[2];
+  for (int r = 0; r * 2 * kGatherThreads < nk || r * kGatherThreads < nv || r * kGatherThreads < 3 * ns; ++r) {
+    const int i = r * kGatherThreads + threadIdx.x, ik = 2 * r * kGatherThreads + threadIdx.x;
+    // the three scale buffers (key scales, zero points, value scales) one after another
+    const int w = i < ns ? 0 : i < 2 * ns ? 1 : 2;
+    Piece<VK> a, c;
+    Piece<VV> v;
+    Piece<VS> s;
+    a.load(src[0], dst[0], p.X[0], ik, nk, p.per[0], p.inv[0], s_from, s_to);
+    c.load(src[0], dst[0], p.X[0], ik + kGatherThreads, nk, p.per[0], p.inv[0], s_from, s_to);
+    v.load(src[3], dst[3], p.X[3], i, nv, p.per[1], p.inv[1], s_from, s_to);
+    s.load(w == 0 ? src[1] : w == 1 ? src[2] : src[4], w == 0 ? dst[1] : w == 1 ? dst[2] : dst[4], p.X[1], i - w * ns, ns,
+           p.per[2], p.inv[2], s_from, s_to);
+    a.store();
+    c.store();
+    v.store();
+    s.store();
+  }
 }
 
 }  // namespace
@@ -198,7 +328,9 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   const int64_t lim = 0x7fffffffLL;
   if (B < 0 || H < 0 || T < 0 || w_cap < T || keep < 0 || recent < 0 || recent > keep || keep > lim)
     return TQ_ERR_INVALID_ARG;
-  if (!ragged_sizes_ok(B, H, w_cap) || !ragged_sizes_ok(B, H, keep)) return TQ_ERR_INVALID_ARG;
+  if (!ragged_sizes_ok(B, H, w_cap) || !ragged_sizes_ok(B, H, keep) || !ragged_sizes_ok(B, H, 8) ||
+      (B > 0 && H > (lim >> 3) / B))  // (at most 8 blocks a row)
+    return TQ_ERR_INVALID_ARG;
   if (B == 0 || H == 0) return TQ_OK;
   if (!weights || !count || (!index && keep > 0)) return TQ_ERR_INVALID_ARG;
   for (const void* x : {static_cast<const void*>(weights), static_cast<const void*>(lens),
@@ -217,8 +349,25 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   p.T = static_cast<int>(T);
   p.keep = static_cast<int>(keep);
   p.recent = static_cast<int>(recent);
-  evict_select_kernel<<<static_cast<unsigned>(B * H), kSelectThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  p.cluster = 1;
+  while (p.cluster < 8 && T > static_cast<int64_t>(p.cluster) * kSelectSlice) p.cluster *= 2;
+  const int64_t slice = (T + p.cluster - 1) / p.cluster;
+  p.held = slice <= kSelectKeys;
+  const int smem = (256 * kSelectCopies + (p.held ? static_cast<int>(slice) : 0)) * 4;
+  if (allow_smem(evict_select_kernel, (256 * kSelectCopies + kSelectKeys) * 4) != cudaSuccess) return TQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B * H * p.cluster));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed_cache* dst, int64_t B, int64_t H,
@@ -250,6 +399,12 @@ extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed
     p.dst[k] = static_cast<uint8_t*>(d[k]);
     p.X[k] = X[k];
   }
+  auto width = [](int bytes) { return bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4; };
+  const int wk = width(X[0]), wv = width(X[3]), ws = width(X[1]);  // key and value codes: 16, or 8 at head_dim 64
+  p.per[0] = X[0] / wk;
+  p.per[1] = X[3] / wv;
+  p.per[2] = X[1] / ws;
+  for (int k = 0; k < 3; ++k) p.inv[k] = (1u << 20) / p.per[k] + 1;
   if (n == 0 && dst_len == nullptr) return TQ_OK;
   const int64_t chunks = n > 0 ? (n + kGatherTokens - 1) / kGatherTokens : 1;
   if (B * H > 0x7fffffffLL / chunks) return TQ_ERR_INVALID_ARG;
@@ -265,6 +420,13 @@ extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed
   p.n = static_cast<int>(n);
   p.heads = index_heads != 0;
   p.chunks = static_cast<unsigned>(chunks);
-  cache_gather_kernel<<<static_cast<unsigned>(chunks * B * H), kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const unsigned grid = static_cast<unsigned>(chunks * B * H);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (ws == 16) cache_gather_kernel<uint4, uint4, uint4><<<grid, kGatherThreads, 0, st>>>(p);
+  else if (ws == 8) cache_gather_kernel<uint4, uint4, uint2><<<grid, kGatherThreads, 0, st>>>(p);
+  else if (wk == 16 && wv == 16) cache_gather_kernel<uint4, uint4, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
+  else if (wk == 16) cache_gather_kernel<uint4, uint2, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
+  else if (wv == 16) cache_gather_kernel<uint2, uint4, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
+  else cache_gather_kernel<uint2, uint2, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

@@ -410,7 +410,7 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
         const uint64_t k0 = smem_operand(sm + st * S::K_BYTES, 16, 1024);
         if (!warp_wait(bars + kcKFull + 8 * st, (part / S::KS) & 1, quit, p.err)) return;
         tmem_fence_after();
-#pragma unroll
+#pragma unroll (S::SUBS == 1 ? 4 : 16)
         for (int ks = 0; ks < S::DS / 16; ++ks) {
           // (operand addresses count 16 bytes)
           const uint64_t b = k0 + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16;
@@ -451,7 +451,7 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
       if (!warp_wait(bars + kcVFull + 8 * st, (it / S::VS) & 1, quit, p.err)) return;
       if (!warp_wait(bars + kcPFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
       tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int ks = 0; ks < S::TT / 16; ++ks) {
         mma_ts(o, pc + 16 * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0, issue);
         mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind_rest, true, issue);
