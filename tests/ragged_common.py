@@ -89,7 +89,8 @@ def ranges(B, T, lens, left_pad):
     return out
 
 
-def tree_reference(q, cache, T, tree, kb, ks, vb, parents=None, lens=None, left_pad=None, scale=None):
+def tree_reference(q, cache, T, tree, kb, ks, vb, parents=None, lens=None, left_pad=None, scale=None,
+                   dtype=torch.float32):
     """-> (out, lse, tolerance of a row's 2-norm, tolerance of lse), float64.
 
     Tolerances. With exact products of bf16 operands, what the kernels round is
@@ -98,7 +99,8 @@ def tree_reference(q, cache, T, tree, kb, ks, vb, parents=None, lens=None, left_
     exponent is off by ds = (D / 16 + 4) 2^-23 scale sum |q K|, and the
     multiplication by scale log2(e), the subtraction of the running maximum
     and exp2 add 2^-22 of the largest |score| and 2^-21; (2) the weights, as
-    two bf16 parts: 2^-18; (3) the sums over tokens, at most one step for each
+    two bf16 parts for a bf16 output (2^-18), as three for an fp32 one (2^-27);
+    (3) the sums over tokens, at most one step for each
     of T / 16 + 32 partial sums and merges; the weights' own sum the same; the
     inverse rotation one step a stage. A relative error e of the weights moves
     the output by at most 2 e max_t |V_t| (2-norm, which the rotation keeps),
@@ -141,7 +143,7 @@ def tree_reference(q, cache, T, tree, kb, ks, vb, parents=None, lens=None, left_
                     mag = abs(scale) * (np.abs(k) @ np.abs(q[b, hq, i])).max()
                 e = (D / 16 + 4) * 2 * HALF * mag + np.abs(s).max() * 2.0 ** -22 + 2.0 ** -21
                 steps = (len(s) / 16 + 32 + math.log2(D)) * 2 * HALF
-                tol[b, hq, i] = (2 * (e + 2.0 ** -18) + 2 * steps) * np.sqrt((v * v).sum(-1)).max()
+                tol[b, hq, i] = (2 * (e + (2.0 ** -27 if dtype == torch.float32 else 2.0 ** -18)) + 2 * steps) * np.sqrt((v * v).sum(-1)).max()
                 ltol[b, hq, i] = e + steps + abs(lse[b, hq, i]) * 4 * HALF + 2.0 ** -21
     return out, lse, tol, ltol
 

@@ -52,18 +52,19 @@ def run_tree(B, Hkv, G, N, T, D, kb, ks, vb, seed=0, lens=None, left_pad=None, p
     got, lse = tq.tq_tree_attention(q.cuda(), rc.to_gpu(main), T, rc.to_gpu(tree), kb, ks, vb, parents=_int(par),
                                     lens=_int(lens), left_pad=_int(left_pad), out_dtype=out_dtype, **kw)
     torch.cuda.synchronize()
-    ref = rc.tree_reference(q, main, T, tree, kb, ks, vb, par, lens, left_pad)
+    ref = rc.tree_reference(q, main, T, tree, kb, ks, vb, par, lens, left_pad, dtype=out_dtype)
     return got, lse, ref
 
 
 # ---- tree attention ---------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("kb,ks", KEY_MODES)
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
-def test_tree_all_formats(D, kb, ks):
+def test_tree_all_formats(D, kb, ks, dtype):
     T = {64: 201, 128: 141, 256: 77, 512: 53}[D]
     for vb in (2, 3, 4, 5, 8):
         got, lse, ref = run_tree(2, 2, 3, 5, T, D, kb, ks, vb, seed=D + 10 * kb + vb, lens=[T, T // 2 + 1],
-                                 left_pad=[0, 5], out_dtype=torch.float32 if vb != 4 else torch.bfloat16)
+                                 left_pad=[0, 5], out_dtype=dtype)
         rc.check_tree(got, lse, ref, "D%d k%d%s v%d" % (D, kb, "s" if ks else "", vb))
 
 
@@ -80,14 +81,17 @@ def test_tree_shapes(B, Hkv, G, N, T, D, dtype):
     rc.check_tree(got, lse, ref)
 
 
-def test_tree_long_ragged():
-    got, lse, ref = run_tree(3, 2, 2, 6, 3000, 128, 8, True, 4, seed=5, lens=[3000, 0, 1411], left_pad=[17, 3, 1409],
-                             qscale=2.0)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tree_long_ragged(D, dtype):
+    got, lse, ref = run_tree(3, 2, 2, 6, 2500, D, 8, True, 4, seed=5, lens=[2500, 0, 1411], left_pad=[17, 3, 1409],
+                             qscale=2.0, out_dtype=dtype)
     rc.check_tree(got, lse, ref)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
-def test_tree_sharp_rows_and_rising_maximum(D):
+def test_tree_sharp_rows_and_rising_maximum(D, dtype):
     """Rows whose weight sits on few keys, and keys that grow along the cache,
     so that a running maximum rises at nearly every tile."""
     def edit(main, tree):
@@ -95,7 +99,7 @@ def test_tree_sharp_rows_and_rising_maximum(D):
         s = main["k_scales"].view(np.float16)
         s[...] = (s.astype(np.float32) * ramp).astype(np.float16)
 
-    got, lse, ref = run_tree(1, 2, 4, 4, 300, D, 8, True, 8, seed=3, qscale=4.0, edit=edit)
+    got, lse, ref = run_tree(1, 2, 4, 4, 300, D, 8, True, 8, seed=3, qscale=4.0, edit=edit, out_dtype=dtype)
     rc.check_tree(got, lse, ref)
 
 
@@ -107,6 +111,9 @@ def test_tree_scales(scale):
     got, lse = tq.tq_tree_attention(q.cuda(), rc.to_gpu(main), 150, rc.to_gpu(tree), 8, True, 3, parents=_int(par),
                                     left_pad=_int([5]), scale=scale, out_dtype=torch.float32)
     rc.check_tree(got, lse, rc.tree_reference(q, main, 150, tree, 8, True, 3, par, None, [5], scale))
+    got, lse = tq.tq_tree_attention(q.cuda(), rc.to_gpu(main), 150, rc.to_gpu(tree), 8, True, 3, parents=_int(par),
+                                    left_pad=_int([5]), scale=scale)
+    rc.check_tree(got, lse, rc.tree_reference(q, main, 150, tree, 8, True, 3, par, None, [5], scale, torch.bfloat16))
 
 
 def test_tree_lengths_outside_the_range_are_clamped():
@@ -126,8 +133,9 @@ def test_tree_rows_without_a_key():
     assert torch.isneginf(lse[1, :, 2:5]).all() and torch.isfinite(lse[1, :, [0, 1, 5]]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
-def test_tree_masked_places_hold_nan_and_infinity(D):
+def test_tree_masked_places_hold_nan_and_infinity(D, dtype):
     """Scales and zero points of NaN and infinity outside [left_pad, lens) and
     in branches that a node is not on: nothing of them reaches a row; a row
     that attends to one is NaN as a whole."""
@@ -142,30 +150,34 @@ def test_tree_masked_places_hold_nan_and_infinity(D):
         tree["k_scales"][0, :, 2, -1] = 0x7E00  # a NaN key: nodes 2 and 4
         tree["v_scales"][1, :, 5, -1] = 0xFE00  # a NaN value group: node 5
 
-    got, lse, ref = run_tree(2, 2, 2, N, T, D, 8, True, 3, parents=par, lens=[70, 66], left_pad=[7, 9], edit=edit)
+    got, lse, ref = run_tree(2, 2, 2, N, T, D, 8, True, 3, parents=par, lens=[70, 66], left_pad=[7, 9], edit=edit,
+                             out_dtype=dtype)
     rc.check_tree(got, lse, ref)
     assert torch.isnan(lse[0, :, 1:5]).all() and torch.isfinite(lse[0, :, [0, 5]]).all()
     assert torch.isnan(lse[1, :, 5]).all() and torch.isfinite(lse[1, :, :5]).all()
 
 
-def test_tree_bad_values_in_the_sequence():
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tree_bad_values_in_the_sequence(dtype):
     """A value group with an infinite scale and a constant key group inside the
     range: every row of that batch row and head is NaN, no other."""
     def edit(main, tree):
         main["v_scales"][0, 0, 33, 1] = 0x7C00
         main["k_zeros"][1, 1, 99, 2] = 0xFC00
 
-    got, lse, ref = run_tree(2, 2, 2, 3, 128, 128, 8, True, 3, parents=None, edit=edit)
+    got, lse, ref = run_tree(2, 2, 2, 3, 128, 128, 8, True, 3, parents=None, edit=edit, out_dtype=dtype)
     rc.check_tree(got, lse, ref)
     assert torch.isnan(lse[0, :2]).all() and torch.isfinite(lse[0, 2:]).all()
     assert torch.isnan(lse[1, 2:]).all() and torch.isfinite(lse[1, :2]).all()
 
 
 def test_tree_capacities_that_no_tile_divides():
-    got, lse, ref = run_tree(2, 3, 2, 5, 61, 64, 8, True, 3, t_cap=67, tree_cap=11, lens=[61, 47])
-    rc.check_tree(got, lse, ref)
-    got, lse, ref = run_tree(2, 3, 2, 5, 61, 64, 5, False, 5, t_cap=67, tree_cap=11, lens=[61, 47])
-    rc.check_tree(got, lse, ref)
+    for D in (64, 128, 256, 512):
+        for kb, ks, vb in ((8, True, 3), (5, False, 5), (2, False, 2)):
+            for dtype in (torch.float32, torch.bfloat16):
+                got, lse, ref = run_tree(2, 3, 2, 5, 61, D, kb, ks, vb, t_cap=67, tree_cap=11, lens=[61, 47],
+                                         out_dtype=dtype)
+                rc.check_tree(got, lse, ref, "D%d k%d v%d" % (D, kb, vb))
 
 
 def test_tree_equals_decode_attention_on_the_appended_cache():
@@ -463,7 +475,8 @@ def test_a_decoding_step_of_all_of_them():
         for k in rc.CACHE_KEYS:
             assert np.array_equal(got[k], kept[k]), k
         out2, lse2 = tq.tq_tree_attention(q, cut, keep, tree, kb, ks, vb, parents=par, lens=cl)
-        rc.check_tree(out2, lse2, rc.tree_reference(q, kept, keep, tn, kb, ks, vb, par.cpu().numpy(), cl.tolist()))
+        rc.check_tree(out2, lse2, rc.tree_reference(q, kept, keep, tn, kb, ks, vb, par.cpu().numpy(), cl.tolist(),
+                                                    dtype=torch.bfloat16))
 
     state = lambda: (cache_to_numpy(main), lens.clone(), weights.cpu().clone())  # noqa: E731
     s = state()

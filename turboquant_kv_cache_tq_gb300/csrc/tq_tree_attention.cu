@@ -4,7 +4,30 @@
 #include "tq_tree_attention.cuh"
 
 namespace tq {
+
+extern template cudaError_t launch_tree_split<64, true>(const TreeParams&, cudaStream_t);
+extern template cudaError_t launch_tree_split<128, true>(const TreeParams&, cudaStream_t);
+extern template cudaError_t launch_tree_split<256, true>(const TreeParams&, cudaStream_t);
+extern template cudaError_t launch_tree_split<512, true>(const TreeParams&, cudaStream_t);
+
 namespace {
+
+template <int D>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
+  const cudaError_t e = p.out_f32 ? launch_tree_split<D, true>(p, s) : launch_tree_split<D, false>(p, s);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(p.B) * p.Hq * p.N;
+  // many partial results a row (few segments, many blocks): four warps a row
+  const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies;
+  if (parts >= 8) return launch_pdl_block(tree_combine_kernel<D, 4>, static_cast<int>(rows), 128, p, s, 0);
+  return launch_pdl_block(tree_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, p, s, 0);
+}
+
+template <bool F32>
+int tile_tokens(int64_t D) {
+  return D == 64 ? TreeShape<64, F32>::TT : D == 128 ? TreeShape<128, F32>::TT : D == 256 ? TreeShape<256, F32>::TT
+                                                                             : TreeShape<512, F32>::TT;
+}
 
 // How the query rows of a kv head are laid out, and the scratch that follows.
 struct TreePlan {
@@ -12,14 +35,15 @@ struct TreePlan {
   int TT, DV;
 };
 
-bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, TreePlan* t) {
+bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, bool f32, TreePlan* t) {
   const long long lim = 0x7fffffffLL;
-  t->TT = D == 512 ? TreeShape<512>::TT : D == 256 ? TreeShape<256>::TT : D == 128 ? TreeShape<128>::TT : TreeShape<64>::TT;
-  t->DV = static_cast<int>(D == 512 ? TreeShape<512>::DV : D);
+  t->TT = f32 ? tile_tokens<true>(D) : tile_tokens<false>(D);
+  t->DV = static_cast<int>(D == 512 ? TreeShape<512, false>::DV : D);
   t->R = Hq / Hkv * N;
   t->RB = (t->R + kTreeRows - 1) / kTreeRows;
   t->rows = (t->R + t->RB - 1) / t->RB;
-  t->copies = t->rows > 64 || t->TT == 32 ? 1 : 2;  // (a lane's share is 32 tokens at least)
+  // (a lane's share is 32 tokens at least; three parts of a weight need the room)
+  t->copies = f32 || t->rows > 64 || t->TT == 32 ? 1 : 2;
   t->slots = (t->copies * t->rows + 3) / 4 * 4;
   if (t->RB * (D / t->DV) > lim / Hkv) return false;
   t->HH = Hkv * t->RB * (D / t->DV);
@@ -40,8 +64,8 @@ extern "C" int64_t tq_tree_attention_workspace_size(int64_t B, int64_t Hq, int64
   if (B < 0 || Hq < 1 || Hkv < 1 || N < 1 || N > TQ_TREE_MAX_NODES || Hq % Hkv != 0 || !ragged_sizes_ok(B, Hq, 1))
     return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
   if (!ragged_head_dim_ok(D)) return -static_cast<int64_t>(TQ_ERR_HEAD_DIM);
-  TreePlan t;
-  if (!tree_plan(B, Hq, Hkv, N, D, &t)) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
+  TreePlan t;  // (fp32 outputs need less)
+  if (!tree_plan(B, Hq, Hkv, N, D, false, &t)) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
   return t.bytes;
 }
 
@@ -65,7 +89,7 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   const int64_t need = tq_tree_attention_workspace_size(B, Hq, Hkv, N, D);
   if (need < 0) return static_cast<tq_status>(-need);
   TreePlan t;
-  tree_plan(B, Hq, Hkv, N, D, &t);
+  tree_plan(B, Hq, Hkv, N, D, out_dtype == TQ_F32, &t);
   // tiles in all, of which a block counts its own in 32 bits
   const long long tiles = (T + t.TT - 1) / t.TT + 1 + (N + t.TT - 1) / t.TT;
   if (tiles > (1LL << 36) / (B * t.HH)) return TQ_ERR_INVALID_ARG;

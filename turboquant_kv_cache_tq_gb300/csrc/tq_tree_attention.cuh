@@ -57,10 +57,10 @@ struct TreeParams {
   float rot_scale;
 };
 
-template <int D>
+template <int D, bool F32>
 struct TreeShape {
   static constexpr int SW = D <= 128 ? 2 : 1;        // groups of softmax warps
-  static constexpr int TT = D >= 256 ? 32 : 64;      // tokens of a tile
+  static constexpr int TT = D >= 256 || (F32 && D > 64) ? 32 : 64;  // tokens of a tile
   static constexpr int DV = D == 512 ? 256 : D;      // value elements a block accumulates
   static constexpr int VH = D / DV;
   static constexpr int NGK = D / kGroup, NGV = DV / kGroup;
@@ -94,12 +94,18 @@ struct TreeShape {
   // a softmax warp's own: the tree's parents, and 32 rows of 20 floats on their way to a record
   static constexpr int W_OFF = C_OFF + 512 + (SW > 1 ? 2048 : 0), W_BYTES = 256 + 32 * 80;
   static constexpr int SMEM = W_OFF + 4 * SW * W_BYTES;
-  // Tensor memory columns: SW outputs | NS score tiles | queries. The weights
-  // of 16 tokens take the place of their scores: eight columns of high parts,
-  // eight of remainders. With SW = 2 two groups of softmax warps take the tiles
-  // in turn, each with an output of its own.
-  static constexpr int NS = D == 128 ? 3 : 4;
-  static constexpr int O_COL = 0, S_COL = SW * DV, Q_COL = S_COL + NS * TT;
+  // Tensor memory columns: SW outputs | NS score tiles of BUF columns | queries.
+  // The weights of 16 tokens take the place of their scores: eight columns of
+  // high parts, eight of remainders. A weight as two bf16 is exact to 2^-18,
+  // which an fp32 output would show, so for those (F32) a third part follows
+  // (2^-27), and tiles are half as long for the room it takes. With SW = 2 two
+  // groups of softmax warps take the tiles in turn, each with an output of its
+  // own.
+  static constexpr int PARTS = F32 ? 3 : 2, PSTEP = 8 * PARTS;  // columns of 16 tokens' weights
+  static constexpr int BUF = F32 ? 2 * TT : TT;
+  static constexpr int NS = !F32 ? (D == 128 ? 3 : 4) : D == 128 ? 3 : 2;
+  static_assert(TT / 16 * PSTEP <= BUF, "the weights fit");
+  static constexpr int O_COL = 0, S_COL = SW * DV, Q_COL = S_COL + NS * BUF;
   static constexpr int THREADS = 640 + 128 * SW;
   static_assert(Q_COL + QT / 2 <= 512, "tensor memory");
   static_assert(QT == DS, "the first part's queries are the ones in tensor memory");
@@ -130,9 +136,9 @@ __device__ __forceinline__ int tree_row_tiles(const TreeParams& p, int b) {
 }
 
 // A walk over the block's tiles, the same in every warp.
-template <int D>
+template <int D, bool F32>
 struct TreeWalk {
-  static constexpr int TT = TreeShape<D>::TT;
+  static constexpr int TT = TreeShape<D, F32>::TT;
   int b, hh, tile, n, n_main, lo, hi;
   int left;  // tiles still to come, this one included
 
@@ -173,9 +179,9 @@ struct TreeWalk {
 // 4- to 16-byte copies. Rows are copied as far as the cache goes; which of them
 // belong to the sequence goes to the values' warps with the tile. A warp's
 // steps are in one chain, so pointers move on instead of being computed anew.
-template <int D, bool KEYS>
+template <int D, bool F32, bool KEYS>
 __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int lane) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, F32>;
   constexpr int NG = KEYS ? S::NGK : S::NGV;
   constexpr bool ROWWISE = !KEYS && S::VH > 1;  // half of each row
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
@@ -238,7 +244,7 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
     }
   };
   if (!p.bulk || ROWWISE || lane == 0) {
-    TreeWalk<D> w;
+    TreeWalk<D, F32> w;
     w.init(p, ctl);
     while (w.left > 0 && going) {
       const int n = min(w.left, w.n - w.tile), main = max(min(n, w.n_main - w.tile), 0);
@@ -258,9 +264,9 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
 
 // The keys' decoding warps: tile after tile from the packed stages into the
 // key stages.
-template <int D, int KMODE>
+template <int D, bool F32, int KMODE>
 __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp8, int lane) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, F32>;
   constexpr int KB = KeySpec<KMODE>::B, X = D * KB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
@@ -308,9 +314,9 @@ __device__ __forceinline__ float2 table64(uint32_t a) {
 // softmax warps make NaN every row that attends to it, and the matrix product
 // never meets a non-finite value that a row with weight zero would turn into
 // NaN.
-template <int D, int VB>
+template <int D, bool F32, int VB>
 __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int warp8, int lane) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, F32>;
   using VT = ValueTable<VB>;
   constexpr int X = S::DV * VB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
@@ -383,15 +389,15 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
 
 // The scores' warp: S = Q K^T, tile after tile. (A block holds all of tensor
 // memory, so its first column is column 0; the kernel checks that.)
-template <int D>
+template <int D, bool F32>
 __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, F32>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   constexpr uint32_t tm = 0;
   const bool issue = elect_lane();
   const uint32_t kind = mma_kind(S::TT, false, p.negate != 0);
-  TreeWalk<D> w;
+  TreeWalk<D, F32> w;
   w.init(p, ctl);
   int it = 0;
   for (unsigned seg = 0; w.left > 0; ++seg) {
@@ -414,9 +420,9 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
         for (int ks = 0; ks < S::DS / 16; ++ks) {
           // (operand addresses count 16 bytes)
           const uint64_t b = k0 + ((ks >> 2) * (S::TT * 128) + (ks & 3) * 32) / 16;
-          if (sub == 0) mma_ts(tm + S::S_COL + sb * S::TT, tm + S::Q_COL + 8 * ks, b, kind, ks > 0, issue);
+          if (sub == 0) mma_ts(tm + S::S_COL + sb * S::BUF, tm + S::Q_COL + 8 * ks, b, kind, ks > 0, issue);
           else
-            mma_ss(tm + S::S_COL + sb * S::TT,
+            mma_ss(tm + S::S_COL + sb * S::BUF,
                    smem_operand(sm + S::Q_OFF, 16, 1024) + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16, b, kind, true, issue);
         }
         mma_commit(bars + kcKEmpty + 8 * st, issue);
@@ -426,17 +432,17 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
   }
 }
 
-// The weighted values' warp: O += P V, the weights as a high part and a
-// remainder to subtract.
-template <int D>
+// The weighted values' warp: O += P V, the weights as a high part, a remainder
+// to subtract (and what that leaves).
+template <int D, bool F32>
 __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, F32>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   constexpr uint32_t tm = 0;
   const bool issue = elect_lane();
   constexpr uint32_t kind = mma_kind(S::DV, true, false), kind_rest = mma_kind(S::DV, true, true);
-  TreeWalk<D> w;
+  TreeWalk<D, F32> w;
   w.init(p, ctl);
   int it = 0;
   while (w.left > 0) {
@@ -447,14 +453,15 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
     for (; it < end; ++it) {
       const int st = it % S::VS, sb = it % S::NS;
       const uint64_t v0 = smem_operand(sm + S::V_OFF + st * S::V_BYTES, S::TT * 128, 1024);
-      const uint32_t pc = tm + S::S_COL + sb * S::TT, o = tm + S::O_COL + (it % S::SW) * S::DV;
+      const uint32_t pc = tm + S::S_COL + sb * S::BUF, o = tm + S::O_COL + (it % S::SW) * S::DV;
       if (!warp_wait(bars + kcVFull + 8 * st, (it / S::VS) & 1, quit, p.err)) return;
       if (!warp_wait(bars + kcPFull + 8 * sb, (it / S::NS) & 1, quit, p.err)) return;
       tmem_fence_after();
 #pragma unroll 1
       for (int ks = 0; ks < S::TT / 16; ++ks) {
-        mma_ts(o, pc + 16 * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0, issue);
-        mma_ts(o, pc + 16 * ks + 8, v0 + ks * 128, kind_rest, true, issue);
+        mma_ts(o, pc + S::PSTEP * ks, v0 + ks * 128, kind, it - begin >= S::SW || ks > 0, issue);
+        mma_ts(o, pc + S::PSTEP * ks + 8, v0 + ks * 128, kind_rest, true, issue);
+        if constexpr (F32) mma_ts(o, pc + S::PSTEP * ks + 16, v0 + ks * 128, kind, true, issue);
       }
       mma_commit(bars + kcPFree + 8 * sb, issue);
       mma_commit(bars + kcVEmpty + 8 * st, issue);
@@ -482,9 +489,9 @@ __device__ __forceinline__ float sub_bf16_f32(uint32_t x, float c) {
 
 // The softmax warps (group `which` of SW, every SW-th tile): a thread holds one
 // lane of tensor memory, i.e. one query row over its copy's share of the tokens.
-template <int D>
+template <int D, bool F32>
 __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int which, int warp, int lane) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, F32>;
   constexpr int TT = S::TT;
   const int W = TT / p.copies;         // tokens of a tile that this lane takes: 32 or 64
   const int QUADS = 4 / p.copies;      // warps per copy
@@ -498,7 +505,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
   const int copy = warp / QUADS, rl = (warp % QUADS) * 32 + lane, col0 = copy * W;
   auto s_full = [&](int it) { return warp_wait(bars + kcSFull + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
   auto weighed = [&](int it) { return warp_wait(bars + kcPFree + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
-  TreeWalk<D> w;
+  TreeWalk<D, F32> w;
   w.init(p, ctl);
   int it0 = 0, seg = 0, anc_b = -1, anc_rb = -1;
   unsigned long long anc = 0;
@@ -558,7 +565,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     float m = kNegInf, l = 0.0f;
     // which of a tile's tokens the row attends to
     auto attended = [&](int tile) -> unsigned long long {
-      TreeWalk<D> x = w;
+      TreeWalk<D, F32> x = w;
       x.tile = tile;
       int t0, first, end;
       x.span(p, t0, first, end);
@@ -582,7 +589,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 #pragma unroll 1
     for (; j < n; j += S::SW) {
       const int it = it0 + j, tile = w.tile + j;
-      const uint32_t buf = tm + S::S_COL + (it % S::NS) * TT;
+      const uint32_t buf = tm + S::S_COL + (it % S::NS) * S::BUF;
       if (!s_full(it)) return;
       bool raised = false;
       float f = 1.0f;
@@ -622,20 +629,15 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
           f = fast_exp2(__fsub_rn(m, mt));
           m = mt;
         }
-        // the weights of the other copies' tokens are zero
-        uint32_t z[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = 0;
-#pragma unroll 1
-        for (int c = 0; c < TT; c += 16)
-          if (c < col0 || c >= col0 + W) tmem_st16(buf + c, z);
         const float ref = m == kNegInf ? 0.0f : m;
         const float2 minus = f2(-ref), by = f2(p.scale_log2);
         float2 sum[2] = {f2(0.0f), f2(0.0f)};
-        // the weights as a bf16 high part minus a bf16 remainder: exact to 2^-18
+        // the weights as a bf16 high part minus a bf16 remainder (exact to 2^-18;
+        // F32: plus the remainder of that), from the last 16 tokens on: three
+        // parts take the next tokens' columns too
 #pragma unroll 1
-        for (int c = col0; c < col0 + W; c += 16) {
-          uint32_t s[16], x[16];
+        for (int c = col0 + W - 16; c >= col0; c -= 16) {
+          uint32_t s[16], x[24];
           tmem_ld16(buf + c, s);
           tmem_wait_ld();
 #pragma unroll
@@ -644,9 +646,21 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
             const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             sum[i & 1] = add2(sum[i & 1], e);
             x[i] = pack_bf16x2(e.x, e.y);
-            x[8 + i] = pack_bf16x2(sub_bf16_f32<false>(x[i], e.x), sub_bf16_f32<true>(x[i], e.y));
+            const float2 r = make_float2(sub_bf16_f32<false>(x[i], e.x), sub_bf16_f32<true>(x[i], e.y));
+            x[8 + i] = pack_bf16x2(r.x, r.y);
+            if constexpr (F32)
+              x[16 + i] = pack_bf16x2(sub_bf16_f32<false>(x[8 + i], r.x), sub_bf16_f32<true>(x[8 + i], r.y));
           }
-          tmem_st16(buf + c, x);
+          tmem_st16(buf + c / 16 * S::PSTEP, x);
+          if constexpr (F32) tmem_st8(buf + c / 16 * S::PSTEP + 16, x + 16);
+        }
+        // the weights of the other copy's tokens are zero (two copies: two parts)
+        if (W < TT) {
+          uint32_t z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0;
+          tmem_st16(buf + (col0 ^ W), z);
+          tmem_st16(buf + (col0 ^ W) + 16, z);
         }
         l = __fmaf_rn(l, f, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
       }
@@ -745,9 +759,9 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(const __grid_constant__ TreeParams p) {
-  using S = TreeShape<D>;
+template <int D, bool F32>
+__global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kernel(const __grid_constant__ TreeParams p) {
+  using S = TreeShape<D, F32>;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* smem = tree_smem;
   uint8_t* ctl = smem + S::C_OFF;
@@ -849,37 +863,37 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
   if (warp < 4 || warp >= 24) {
     if constexpr (S::SW == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-    tree_softmax<D>(p, sm, smem, ctl, warp >= 24 ? 1 : 0, warp & 3, lane);
+    tree_softmax<D, F32>(p, sm, smem, ctl, warp >= 24 ? 1 : 0, warp & 3, lane);
   } else if (warp < 20) {
     if constexpr (S::SW == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int warp8 = (warp - 4) / 4 * 2 + (warp & 1);
     if ((warp & 2) == 0) {
       switch (p.kmode) {
-        case kK2: tree_decode_keys<D, kK2>(p, sm, ctl, warp8, lane); break;
-        case kK4: tree_decode_keys<D, kK4>(p, sm, ctl, warp8, lane); break;
-        case kK5: tree_decode_keys<D, kK5>(p, sm, ctl, warp8, lane); break;
-        case kK8: tree_decode_keys<D, kK8>(p, sm, ctl, warp8, lane); break;
-        default: tree_decode_keys<D, kK8Signed>(p, sm, ctl, warp8, lane); break;
+        case kK2: tree_decode_keys<D, F32, kK2>(p, sm, ctl, warp8, lane); break;
+        case kK4: tree_decode_keys<D, F32, kK4>(p, sm, ctl, warp8, lane); break;
+        case kK5: tree_decode_keys<D, F32, kK5>(p, sm, ctl, warp8, lane); break;
+        case kK8: tree_decode_keys<D, F32, kK8>(p, sm, ctl, warp8, lane); break;
+        default: tree_decode_keys<D, F32, kK8Signed>(p, sm, ctl, warp8, lane); break;
       }
     } else {
       switch (p.vb) {
-        case 2: tree_decode_values<D, 2>(p, sm, smem, ctl, warp8, lane); break;
-        case 3: tree_decode_values<D, 3>(p, sm, smem, ctl, warp8, lane); break;
-        case 4: tree_decode_values<D, 4>(p, sm, smem, ctl, warp8, lane); break;
-        case 5: tree_decode_values<D, 5>(p, sm, smem, ctl, warp8, lane); break;
-        default: tree_decode_values<D, 8>(p, sm, smem, ctl, warp8, lane); break;
+        case 2: tree_decode_values<D, F32, 2>(p, sm, smem, ctl, warp8, lane); break;
+        case 3: tree_decode_values<D, F32, 3>(p, sm, smem, ctl, warp8, lane); break;
+        case 4: tree_decode_values<D, F32, 4>(p, sm, smem, ctl, warp8, lane); break;
+        case 5: tree_decode_values<D, F32, 5>(p, sm, smem, ctl, warp8, lane); break;
+        default: tree_decode_values<D, F32, 8>(p, sm, smem, ctl, warp8, lane); break;
       }
     }
   } else {
     if constexpr (S::SW == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 22) {
-      tree_load<D, true>(p, sm, smem, ctl, lane);
+      tree_load<D, F32, true>(p, sm, smem, ctl, lane);
     } else if (warp == 23) {
-      tree_load<D, false>(p, sm, smem, ctl, lane);
+      tree_load<D, F32, false>(p, sm, smem, ctl, lane);
     } else {
-      if (warp == 20) tree_scores<D>(p, sm, ctl);
-      else tree_weigh<D>(p, sm, ctl);
+      if (warp == 20) tree_scores<D, F32>(p, sm, ctl);
+      else tree_weigh<D, F32>(p, sm, ctl);
       if (*reinterpret_cast<volatile int*>(ctl + kcQuit) != 0) {  // gave up: let the matrix work in flight end
         mma_commit(bars + kcDrain + 8 * (warp - 20), elect_lane());
         mbar_wait(bars + kcDrain + 8 * (warp - 20), 0, kBulkWaitLimit);
@@ -900,7 +914,7 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1) tree_split_kernel(co
 // Lane L holds elements [L D/32, (L+1) D/32).
 template <int D, int W>
 __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeParams p) {
-  using S = TreeShape<D>;
+  using S = TreeShape<D, false>;  // (what is read here is the same for both)
   constexpr int E = D / 32;
   constexpr int V = E < 4 ? E : 4;
   const float kNegInf = -__int_as_float(0x7f800000);
@@ -1052,18 +1066,12 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
     p.lse[row] = empty ? kNegInf : __fmul_rn(__fadd_rn(m, log2f(l)), 0.693147180559945309f);
 }
 
-template <int D>
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
-  using S = TreeShape<D>;
-  cudaError_t e = allow_smem(tree_split_kernel<D>, S::SMEM);
+template <int D, bool F32>
+cudaError_t launch_tree_split(const TreeParams& p, cudaStream_t s) {
+  using S = TreeShape<D, F32>;
+  cudaError_t e = allow_smem(tree_split_kernel<D, F32>, S::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl_block(tree_split_kernel<D>, p.grid, S::THREADS, p, s, S::SMEM);
-  if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(p.B) * p.Hq * p.N;
-  // many partial results a row (few segments, many blocks): four warps a row
-  const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies;
-  if (parts >= 8) return launch_pdl_block(tree_combine_kernel<D, 4>, static_cast<int>(rows), 128, p, s, 0);
-  return launch_pdl_block(tree_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, p, s, 0);
+  return launch_pdl_block(tree_split_kernel<D, F32>, p.grid, S::THREADS, p, s, S::SMEM);
 }
 
 }  // namespace tq
