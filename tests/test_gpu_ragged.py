@@ -256,6 +256,63 @@ def test_tree_on_two_streams_at_once():
         assert torch.equal(a, b)
 
 
+def test_tree_many_batch_rows():
+    """More rows than a warp counts at a time, many of them short or empty."""
+    lens = [(7 * b) % 41 for b in range(70)]
+    for dtype in (torch.float32, torch.bfloat16):
+        got, lse, ref = run_tree(70, 1, 2, 2, 40, 128, 8, True, 3, lens=lens, out_dtype=dtype)
+        rc.check_tree(got, lse, ref)
+
+
+def test_tree_caches_in_pinned_host_memory():
+    """Buffers in pinned host memory give the same bits as in device memory."""
+    B, Hkv, G, N, T, D = 2, 2, 2, 4, 150, 128
+    main, tree = (rc.to_gpu(rc.random_cache(B, Hkv, n, D, 8, True, 3, n)) for n in (T, N))
+    q = _q((B, Hkv * G, N, D), 4).cuda()
+    want, wl = tq.tq_tree_attention(q, main, T, tree, 8, True, 3)
+    ww = tq.tq_attention_weights(q, wl, main, T, 8, True)
+    hm, ht = ({k: v.cpu().pin_memory() for k, v in c.items()} for c in (main, tree))
+    out, lse, w = torch.empty_like(want), torch.empty_like(wl), torch.empty_like(ww)
+    ws = torch.empty(tq.tq_tree_attention_workspace_size(B, Hkv * G, Hkv, N, D), dtype=torch.uint8, device="cuda")
+    views = [tq.TQPackedCache(*(c[n].data_ptr() for n in rc.CACHE_KEYS), c["k_codes"].shape[2]) for c in (hm, ht)]
+    s = torch.cuda.current_stream().cuda_stream
+    assert tq.lib().tq_tree_attention(q.data_ptr(), B, Hkv * G, N, ctypes.byref(views[0]), Hkv, T, D,
+                                      ctypes.byref(views[1]), None, 8, 1, 3, None, None, ctypes.c_float(D ** -0.5),
+                                      out.data_ptr(), 1, lse.data_ptr(), ws.data_ptr(), ws.numel(), s) == 0
+    assert tq.lib().tq_attention_weights(q.data_ptr(), lse.data_ptr(), B, Hkv * G, N, hm["k_codes"].data_ptr(),
+                                         hm["k_scales"].data_ptr(), hm["k_zeros"].data_ptr(), Hkv, T, D, T, 8, 1, None,
+                                         None, None, None, N, ctypes.c_float(D ** -0.5), None, w.data_ptr(), T, s) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl) and torch.equal(w, ww)
+
+
+def test_offsets_past_32_bits():
+    """The last head of a cache whose buffers pass 2^32 bytes: the bits that the
+    same tokens give in a small cache (equal lengths are cut the same way)."""
+    B, Hkv, N, T, D, cap = 1, 4, 3, 200, 128, 9 << 20
+    small, tree = (rc.to_gpu(rc.random_cache(B, Hkv, n, D, 8, True, 8, n)) for n in (208, N))
+    big = tq.alloc_cache(B, Hkv, cap, D, 8, 8)
+    assert big["k_codes"].numel() > 1 << 32
+    for k in rc.CACHE_KEYS:
+        big[k][:, :, :208] = small[k]
+    q, lens = _q((B, 2 * Hkv, N, D), 4).cuda(), _int([T])
+    for dtype in (torch.float32, torch.bfloat16):
+        a = tq.tq_tree_attention(q, small, T, tree, 8, True, 8, lens=lens, out_dtype=dtype)
+        b = tq.tq_tree_attention(q, big, T, tree, 8, True, 8, lens=lens, out_dtype=dtype)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    wa, wb = (tq.tq_attention_weights(q, a[1], c, T, 8, True, lens=lens) for c in (small, big))
+    assert torch.equal(wa, wb)
+    # tokens at the far end of every head, there and back
+    index = torch.arange(N, dtype=torch.int32, device="cuda")[None]
+    far = _int([cap - N])
+    _, length = tq.tq_cache_gather(tree, big, index, dst_off=far)
+    assert length.tolist() == [cap]
+    back = tq.alloc_cache(B, Hkv, N, D, 8, 8)
+    tq.tq_cache_gather(big, back, index + (cap - N))
+    for k in rc.CACHE_KEYS:
+        assert torch.equal(back[k].view(torch.uint8), tree[k].view(torch.uint8))
+
+
 # ---- weight sums ------------------------------------------------------------------
 def run_weights(B, Hkv, G, N, T, D, kb, ks, seed=0, lens=None, left_pad=None, path=None, n_path=None, t_cap=None,
                 w_cap=None, start=False, in_place=False, lse=None, edit=None, qscale=1.0):
@@ -293,6 +350,17 @@ def test_weights_all_formats(D, kb, ks):
 ])
 def test_weights_shapes(B, Hkv, G, N, T, D):
     run_weights(B, Hkv, G, N, T, D, 8, True, seed=T + N, lens=None if B == 1 else [max(0, T - 11 * b) for b in range(B)])
+
+
+def test_weights_many_batch_rows():
+    run_weights(70, 1, 2, 3, 40, 128, 8, True, lens=[(7 * b) % 41 for b in range(70)],
+                n_path=[b % 4 for b in range(70)], path=[[0, 1, 2]] * 70, start=True)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_weights_capacities_that_no_tile_divides(D):
+    for kb, ks in ((8, True), (5, False)):
+        run_weights(2, 3, 2, 5, 61, D, kb, ks, t_cap=67, lens=[61, 40])
 
 
 def test_weights_paths():

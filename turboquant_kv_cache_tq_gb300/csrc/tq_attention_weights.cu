@@ -188,8 +188,7 @@ __device__ void weights_load(const WeightsParams& p, uint32_t sm, uint8_t* ctl, 
             copy_rows_any(dst, codes, p.x_keys, p.x_keys, n, lane);
             copy_rows_any(dst + S::R_SC, scales, 2 * S::NG, 2 * S::NG, n, lane);
             copy_rows_any(dst + S::R_ZP, zeros, 2 * S::NG, 2 * S::NG, n, lane);
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
+            copies_arrive(bar);
             if (lane == 0) mbar_arrive(bar);
           }
           t0 += S::TT;
@@ -200,7 +199,8 @@ __device__ void weights_load(const WeightsParams& p, uint32_t sm, uint8_t* ctl, 
       }
     }
     // the last copies land before the block ends, whatever became of its other warps
-    if (p.bulk)
+    if (!p.bulk) asm volatile("cp.async.wait_all;" ::: "memory");
+    else
       for (int k = max(it - S::NR, 0); k < it; ++k) mbar_wait(bars + wcLoaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
   }
   __syncwarp();
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
       mbar_init(bars + wcSFree + 8 * i, 4);
     }
     for (int i = 0; i < S::NR; ++i) {
-      mbar_init(bars + wcLoaded + 8 * i, 1);
+      mbar_init(bars + wcLoaded + 8 * i, p.bulk ? 1 : 33);
       mbar_init(bars + wcTaken + 8 * i, S::DWARPS);
     }
     mbar_init(bars + wcQFull, 4);
@@ -393,6 +393,10 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
       if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrTimeout);
     }
   }
+  // Dependent kernels may start once every block has its tensor memory: one of
+  // theirs that took it first, and then waited for this kernel to end, would
+  // wait for ever.
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
@@ -539,7 +543,8 @@ extern "C" tq_status tq_attention_weights(const void* q, const float* lse, int64
   p.P = static_cast<int>(P);
   p.kmode = kmode;
   p.x_keys = static_cast<int>(D * k_bits / 8);
-  p.bulk = t_cap * (D / 16) % 16 == 0 && t_cap * p.x_keys % 16 == 0;
+  p.bulk = t_cap * (D / 16) % 16 == 0 && t_cap * p.x_keys % 16 == 0 &&
+           ragged_device_memory({k_codes, k_scales, k_zeros});
   p.scale = scale;
   p.err = device_error_word();
   cudaStream_t s = static_cast<cudaStream_t>(stream);

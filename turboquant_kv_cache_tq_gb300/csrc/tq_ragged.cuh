@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -66,6 +67,20 @@ inline cudaError_t allow_smem(void (*kernel)(Params), int bytes) {
   return e;
 }
 
+// Whether every buffer (a cache without room has none) is device memory: bulk
+// copies are only used between device and shared memory.
+inline bool ragged_device_memory(std::initializer_list<const void*> ptrs) {
+  for (const void* x : ptrs) {
+    cudaPointerAttributes a{};
+    if (x == nullptr) continue;
+    if (cudaPointerGetAttributes(&a, x) != cudaSuccess) {
+      cudaGetLastError();  // leave no sticky error behind
+      return false;
+    }
+    if (a.type != cudaMemoryTypeDevice) return false;
+  }
+  return true;
+}
 inline bool ragged_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ragged_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool ragged_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }

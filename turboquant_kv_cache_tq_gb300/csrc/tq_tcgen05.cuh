@@ -8,12 +8,12 @@
 namespace tq {
 
 // ---- waits ----------------------------------------------------------------------
-// Completion of phase `parity` of a barrier. Each try may sleep up to 20 us in
+// Completion of phase `parity` of a barrier. Each try may sleep up to 1 us in
 // hardware (a poll that returns at once takes issue slots from the working
-// warps); 2^14 of them end a wait that nothing answers after a third of a
-// second, with the library's device error word set and *quit, which ends every
-// other wait of the block too.
-constexpr unsigned kTryNs = 20000, kTries = 1u << 14;
+// warps); 2^20 of them end a wait that nothing answers after a second at most,
+// with the library's device error word set and *quit, which ends every other
+// wait of the block too.
+constexpr unsigned kTryNs = 1000, kTries = 1u << 20;
 __device__ __forceinline__ bool try_wait(uint32_t bar, unsigned parity) {
   unsigned done;
   asm volatile(

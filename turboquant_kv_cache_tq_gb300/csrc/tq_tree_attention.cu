@@ -137,9 +137,12 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   p.x_keys = static_cast<int>(D * k_bits / 8);
   p.x_values = static_cast<int>(D * v_bits / 8);
   p.vtab_stride = 128;
-  p.bulk = 1;
-  for (const int64_t cap : {cache->t_cap, tree->t_cap})
-    if (cap * (D / 16) % 16 != 0 || cap * p.x_keys % 16 != 0 || cap * p.x_values % 16 != 0) p.bulk = 0;
+  auto bulk = [&](const tq_packed_cache* c) {
+    return c->t_cap * (D / 16) % 16 == 0 && c->t_cap * p.x_keys % 16 == 0 && c->t_cap * p.x_values % 16 == 0 &&
+           ragged_device_memory({c->k_codes, c->k_scales, c->k_zeros, c->v_codes, c->v_scales});
+  };
+  p.bulk = bulk(cache);
+  p.bulk_tree = bulk(tree);
   p.out_f32 = out_dtype == TQ_F32;
   p.err = device_error_word();
   // one range of tiles per SM (a block holds all of an SM's tensor memory)

@@ -51,7 +51,7 @@ struct TreeParams {
   int kmode, vb, out_f32, grid;
   int x_keys, x_values;  // bytes of a token's packed codes
   unsigned vtab_stride;  // 128: bytes between entries of the value table
-  int bulk;              // every tile of both caches starts on 16 bytes in every buffer
+  int bulk, bulk_tree;   // every tile of the cache, the tree's cache starts on 16 bytes in every buffer
   float scale_log2;   // |scale| * log2(e)
   int negate;         // scale < 0
   float rot_scale;
@@ -174,12 +174,14 @@ struct TreeWalk {
 };
 
 // The loading warps (keys and values): the packed rows of tile after tile into
-// the stages, by bulk copies where every tile of both caches starts on 16 bytes
-// in every buffer (p.bulk: t_cap times a row's bytes a multiple of 16), else by
-// 4- to 16-byte copies. Rows are copied as far as the cache goes; which of them
-// belong to the sequence goes to the values' warps with the tile. A warp's
-// steps are in one chain, so pointers move on instead of being computed anew.
-template <int D, bool F32, bool KEYS>
+// the stages, by bulk copies where every tile of the cache starts on 16 bytes in
+// every buffer (t_cap times a row's bytes a multiple of 16, all of it device
+// memory), else by 4- to 16-byte copies of the whole warp (ALONE: one lane, as
+// both caches take bulk copies). Rows are copied as far as the cache goes; which
+// of them belong to the sequence goes to the values' warps with the tile. A
+// warp's steps are in one chain, so pointers move on instead of being computed
+// anew.
+template <int D, bool F32, bool KEYS, bool ALONE>
 __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int lane) {
   using S = TreeShape<D, F32>;
   constexpr int NG = KEYS ? S::NGK : S::NGV;
@@ -193,7 +195,7 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
   int it = 0;
   bool going = true;
   // `tiles` tiles of head h from token t0 on; tokens [lo, hi) are real
-  auto part = [&](const PackedView& c, int b, int h, int half, int t0, int tiles, int lo, int hi) {
+  auto part = [&](const PackedView& c, bool bulk, int b, int h, int half, int t0, int tiles, int lo, int hi) {
     const long long row = (static_cast<long long>(b) * p.Hkv + h) * c.t_cap + t0;
     const uint8_t* codes = (KEYS ? c.k_codes : c.v_codes) + row * row_bytes + half * X;
     const uint8_t* scales = reinterpret_cast<const uint8_t*>((KEYS ? c.k_scales : c.v_scales) + row * S::NGK + half * NG);
@@ -205,8 +207,8 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
       const uint32_t bar = bars + loaded + 8 * st, dst = ring + st * STAGE;
       if (it >= S::NR) {
         const unsigned parity = (it / S::NR - 1) & 1;
-        going = p.bulk && !ROWWISE ? wait_or_quit(bars + taken + 8 * st, parity, quit, p.err)
-                                   : warp_wait(bars + taken + 8 * st, parity, quit, p.err);
+        going = ALONE ? wait_or_quit(bars + taken + 8 * st, parity, quit, p.err)
+                      : warp_wait(bars + taken + 8 * st, parity, quit, p.err);
         if (!going) break;
       }
       int n = min(S::TT, room);
@@ -214,27 +216,24 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
       if (!KEYS && lane == 0)
         *reinterpret_cast<int2*>(smem + S::VR_OFF + st * STAGE + S::VR_SPAN) =
             make_int2(max(lo - t0, 0), min(hi - t0, S::TT));
-      if constexpr (ROWWISE) {
-        // (64 bulk copies of 64 to 256 bytes a tile measured slower: the copy
-        // engine takes about as long for each as for a whole tile's)
-        copy_rows_any(dst, codes, row_bytes, X, n, lane);
-        copy_rows_any(dst + SC, scales, 2 * S::NGK, 2 * NG, n, lane);
-        copies_arrive(bar);
-        if (lane == 0) mbar_arrive(bar);  // (releases the span too)
-      } else if (p.bulk) {
-        mbar_expect_tx(bar, n * (X + (KEYS ? 4 : 2) * NG));
-        if (n > 0) {
-          bulk_load(dst, codes, n * X, bar);
-          bulk_load(dst + SC, scales, n * NG * 2, bar);
-          if constexpr (KEYS) bulk_load(dst + S::KR_ZP, zeros, n * NG * 2, bar);
+      // (ROWWISE: 64 bulk copies of 64 to 256 bytes a tile measured slower: the
+      // copy engine takes about as long for each as for a whole tile's)
+      if (!ROWWISE && (ALONE || bulk)) {
+        if (ALONE || lane == 0) {
+          mbar_expect_tx(bar, n * (X + (KEYS ? 4 : 2) * NG));
+          if (n > 0) {
+            bulk_load(dst, codes, n * X, bar);
+            bulk_load(dst + SC, scales, n * NG * 2, bar);
+            if constexpr (KEYS) bulk_load(dst + S::KR_ZP, zeros, n * NG * 2, bar);
+          }
         }
+        if (!ALONE) mbar_arrive(bar);  // (33 arrivals, as below)
       } else {
         copy_rows_any(dst, codes, row_bytes, X, n, lane);
         copy_rows_any(dst + SC, scales, 2 * S::NGK, 2 * NG, n, lane);
         if constexpr (KEYS) copy_rows_any(dst + S::KR_ZP, zeros, 2 * NG, 2 * NG, n, lane);
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
+        copies_arrive(bar);
+        if (lane == 0) mbar_arrive(bar);  // (releases the span too)
       }
       t0 += S::TT;
       room -= S::TT;
@@ -243,20 +242,20 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
       if constexpr (KEYS) zeros += S::TT * S::NGK * 2;
     }
   };
-  if (!p.bulk || ROWWISE || lane == 0) {
+  if (!ALONE || lane == 0) {
     TreeWalk<D, F32> w;
     w.init(p, ctl);
     while (w.left > 0 && going) {
       const int n = min(w.left, w.n - w.tile), main = max(min(n, w.n_main - w.tile), 0);
       const int h = p.HH == p.Hkv ? w.hh : w.hh / (p.RB * S::VH), half = KEYS || S::VH == 1 ? 0 : w.hh % S::VH;
-      if (main > 0) part(p.cache, w.b, h, half, (w.lo & ~15) + w.tile * S::TT, main, w.lo, w.hi);
-      if (n > main) part(p.tree, w.b, h, half, max(w.tile - w.n_main, 0) * S::TT, n - main, 0, p.N);
+      if (main > 0) part(p.cache, p.bulk, w.b, h, half, (w.lo & ~15) + w.tile * S::TT, main, w.lo, w.hi);
+      if (n > main) part(p.tree, p.bulk_tree, w.b, h, half, max(w.tile - w.n_main, 0) * S::TT, n - main, 0, p.N);
       w.left -= n;
       w.next_segment(p);
     }
     // the last copies land before the block ends, whatever became of its other warps
-    if (ROWWISE) asm volatile("cp.async.wait_all;" ::: "memory");
-    else if (p.bulk)
+    if (!ALONE) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ROWWISE)
       for (int k = max(it - S::NR, 0); k < it; ++k) mbar_wait(bars + loaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
   }
   __syncwarp();
@@ -792,9 +791,9 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
       mbar_init(bars + kcPFree + 8 * i, 1);
     }
     for (int i = 0; i < S::NR; ++i) {
-      mbar_init(bars + kcKLoaded + 8 * i, 1);
+      mbar_init(bars + kcKLoaded + 8 * i, p.bulk && p.bulk_tree ? 1 : 33);
       mbar_init(bars + kcKTaken + 8 * i, S::KWARPS * S::SUBS);
-      mbar_init(bars + kcVLoaded + 8 * i, S::VH > 1 ? 33 : 1);
+      mbar_init(bars + kcVLoaded + 8 * i, S::VH == 1 && p.bulk && p.bulk_tree ? 1 : 33);
       mbar_init(bars + kcVTaken + 8 * i, S::VWARPS);
     }
     *reinterpret_cast<int*>(ctl + kcQuit) = 0;
@@ -809,6 +808,10 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
       if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrTimeout);
     }
   }
+  // Dependent kernels may start once every block has its tensor memory: one of
+  // theirs that took it first, and then waited for this kernel to end, would
+  // wait for ever.
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
@@ -887,10 +890,13 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
     }
   } else {
     if constexpr (S::SW == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const bool alone = p.bulk && p.bulk_tree;
     if (warp == 22) {
-      tree_load<D, F32, true>(p, sm, smem, ctl, lane);
+      if (alone) tree_load<D, F32, true, true>(p, sm, smem, ctl, lane);
+      else tree_load<D, F32, true, false>(p, sm, smem, ctl, lane);
     } else if (warp == 23) {
-      tree_load<D, F32, false>(p, sm, smem, ctl, lane);
+      if (alone && S::VH == 1) tree_load<D, F32, false, S::VH == 1>(p, sm, smem, ctl, lane);
+      else tree_load<D, F32, false, false>(p, sm, smem, ctl, lane);
     } else {
       if (warp == 20) tree_scores<D, F32>(p, sm, ctl);
       else tree_weigh<D, F32>(p, sm, ctl);
