@@ -313,7 +313,9 @@ TQ_API int64_t tq_lloyd_max_fit_workspace_size(int levels);
  * device arrays [B] read while the call runs, so one captured graph serves
  * every step. Values outside [0, T] count as the nearer end of that range;
  * lens == NULL stands for T everywhere, left_pad == NULL for 0. T, known to the
- * host, bounds lens.
+ * host, bounds lens. An array that a call writes shares no memory with another
+ * one that it reads or writes, unless its text says so; overlaps that the host
+ * can see among the large ones are refused (TQ_ERR_INVALID_ARG).
  *
  * One decode step with drafted tokens: encode the draft's keys and values into
  * a small cache of their own (tq_encode_kv, tokens [0, N)); attend with
@@ -346,8 +348,8 @@ typedef struct {
  *            itself. Node i attends to itself and to its ancestors. A node
  *            whose chain of parents does not end at -1 (any other negative
  *            value, or a value >= i) is absent: its output rows are zero, its
- *            lse is -inf and no present node attends to it. NULL: a chain, node i - 1
- *            before node i.
+ *            lse is -inf and no present node attends to it. NULL: a chain,
+ *            node i - 1 before node i.
  *   scale    the softmax scale.
  *   out      [B, Hq, N, D] of out_dtype, contiguous.
  *   lse      NULL, or [B, Hq, N] fp32: the natural logarithm of the sum over
@@ -361,8 +363,15 @@ typedef struct {
  *            bytes (16-byte aligned), not in use by another call still
  *            running; it needs no initialisation.
  * Limits: D in {64, 128, 256, 512}; Hq a multiple of Hkv; 1 <= N <= 64; T at
- * most cache->t_cap. B == 0 is a no-op. No buffer needs t_cap to be a multiple
- * of 16. */
+ * most cache->t_cap. B == 0 is a no-op. Any t_cap will do; a cache whose rows
+ * of every buffer are a multiple of 16 bytes long (t_cap * D / 16, t_cap * D *
+ * bits / 8) is read by bulk copies, others more slowly.
+ * Arithmetic: scores in fp32 from bf16 products. The weights enter their product
+ * with V as sums of bf16 parts: two (2^-18 of the weight) for a bf16 output,
+ * three (2^-27) for an fp32 one; all sums are fp32. Equal calls give equal
+ * bits on GPUs of one size.
+ * The kernels bound their waits: one that gives up is reported by
+ * tq_device_status, and the outputs of that call are incomplete. */
 #define TQ_TREE_MAX_NODES 64
 TQ_API tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int64_t N,
                                    const tq_packed_cache* cache, int64_t Hkv, int64_t T, int64_t D,
@@ -398,7 +407,7 @@ TQ_API int64_t tq_tree_attention_workspace_size(int64_t B, int64_t Hq, int64_t H
  *            only those that an observer attends to.
  * The sum over a token's observers has a fixed order: equal calls give equal
  * bits. Limits as for tq_tree_attention, but N and P are bounded only by
- * (Hq / Hkv) * P <= 65536. */
+ * (Hq / Hkv) * P <= 65536. The kernel bounds its waits (tq_device_status). */
 TQ_API tq_status tq_attention_weights(const void* q, const float* lse, int64_t B, int64_t Hq, int64_t N,
                                       const void* k_codes, const void* k_scales, const void* k_zeros,
                                       int64_t Hkv, int64_t T, int64_t D, int64_t t_cap, int k_bits, int k_signed,
@@ -413,7 +422,7 @@ TQ_API tq_status tq_attention_weights(const void* q, const float* lse, int64_t B
  *   weights  fp32 [B, H, w_cap], w_cap >= T.
  *   index    int32 [B, H, keep]: the kept tokens in ascending order, then -1.
  *   count    int32 [B]: min(keep, lens[b] - left_pad[b]), the kept tokens of
- *            every head of row b.
+ *            every head of row b; not lens or left_pad itself.
  * Limits: 0 <= recent <= keep, B * H < 2^31. keep == 0 writes count alone. */
 TQ_API tq_status tq_evict_select(const float* weights, int64_t B, int64_t H, int64_t T, int64_t w_cap,
                                  const int32_t* lens, const int32_t* left_pad, int64_t keep, int64_t recent,
@@ -442,7 +451,8 @@ TQ_API tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed_cac
 
 /* Device-side failures of the library's kernels on the current device (no
  * counterpart on the pages: failure detection of this library). Kernels that
- * wait on an asynchronous copy (the decode's bulk-copy path) bound the wait;
+ * wait on an asynchronous copy or a matrix product (the decode's bulk-copy path,
+ * tq_tree_attention, tq_attention_weights) bound the wait;
  * one that gives up sets the device error word, stops early and leaves its
  * outputs incomplete. A debug build of the library (compiled with
  * -DTQ_DEBUG_CHECKS) also checks the row and record indices of its kernels'

@@ -125,6 +125,27 @@ def test_gather_refusals(tq):
     assert tq.lib().tq_cache_gather(None, None, 1, 2, 128, 8, 3, P, 4, 0, None, None, None, None, None, None) == INVALID
 
 
+def test_overlaps_are_refused(tq):
+    """Arrays that share memory, where the call does not allow it."""
+    far = [P + (i << 30) for i in range(16)]
+    distinct = dict(q=far[0], out=far[1], lse=far[2], ws=far[3], cache=_cache(tq), tree=_cache(tq, 8))
+    for kw in (dict(out=far[0]), dict(out=far[0] + 4 * 8 * 128 * 2 - 16), dict(lse=far[0] + 4), dict(lse=far[1] + 8),
+               dict(ws=far[0] - 16), dict(ws=far[1] - 16), dict(ws=far[2] - 16)):
+        assert _tree(tq, **dict(distinct, **kw)) == INVALID, kw
+    assert _weights(tq, w_in=far[1], w_out=far[1] + 4, q=far[0], lse=far[2]) == INVALID
+    assert _weights(tq, w_in=far[1] + 2 * 64 * 4 - 4, w_out=far[1], q=far[0], lse=far[2]) == INVALID
+    assert _weights(tq, w_out=far[2] + 4, q=far[0], lse=far[2]) == INVALID
+    for kw in (dict(index=far[0]), dict(count=far[0]), dict(count=far[1] + 4), dict(lens=far[2]), dict(pad=far[2]),
+               dict(lens=far[1] + 60)):
+        assert _select(tq, **dict(dict(w=far[0], index=far[1], count=far[2]), **kw)) == INVALID, kw
+    src = _cache(tq, 64, **{n: far[i] for i, n in enumerate(rc.CACHE_KEYS)})
+    dst = {n: far[5 + i] for i, n in enumerate(rc.CACHE_KEYS)}
+    apart = dict(src=src, dst=_cache(tq, 64, **dst), index=far[10], length=far[11], sw=far[12], dw=far[13])
+    for kw in (dict(dst=src), dict(dst=_cache(tq, 64, **dict(dst, v_codes=far[1] + 16))), dict(dw=far[12] + 4),
+               dict(off=far[11]), dict(count=far[11]), dict(length=far[10] + 12)):
+        assert _gather(tq, **dict(apart, **kw)) == INVALID, kw
+
+
 def test_binding_refuses_wrong_tensors(tq):
     """Shapes, types and devices are checked before the library is called."""
     G = 4

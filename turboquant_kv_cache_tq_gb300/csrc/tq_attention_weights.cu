@@ -520,6 +520,10 @@ extern "C" tq_status tq_attention_weights(const void* q, const float* lse, int64
                         static_cast<const void*>(n_path), static_cast<const void*>(weights_in),
                         static_cast<const void*>(weights_out)})
     if (!ragged_aligned4(x)) return TQ_ERR_ALIGNMENT;
+  const long long sums = B * Hkv * w_cap * 4;
+  if ((weights_in != weights_out && ragged_overlap(weights_in, sums, weights_out, sums)) ||
+      ragged_overlap(lse, B * Hq * N * 4, weights_out, sums))
+    return TQ_ERR_INVALID_ARG;
   WeightsParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.lse = lse;

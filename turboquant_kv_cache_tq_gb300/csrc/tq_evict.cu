@@ -337,6 +337,12 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
                         static_cast<const void*>(left_pad), static_cast<const void*>(index),
                         static_cast<const void*>(count)})
     if (!ragged_aligned4(x)) return TQ_ERR_ALIGNMENT;
+  const long long kept = B * H * keep * 4;
+  if (ragged_overlap(index, kept, count, B * 4) || ragged_overlap(index, kept, weights, B * H * w_cap * 4) ||
+      ragged_overlap(count, B * 4, weights, B * H * w_cap * 4))
+    return TQ_ERR_INVALID_ARG;
+  for (const int32_t* x : {lens, left_pad})
+    if (ragged_overlap(x, B * 4, index, kept) || ragged_overlap(x, B * 4, count, B * 4)) return TQ_ERR_INVALID_ARG;
   SelectParams p{};
   p.w = weights;
   p.lens = lens;
@@ -399,6 +405,14 @@ extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed
     p.dst[k] = static_cast<uint8_t*>(d[k]);
     p.X[k] = X[k];
   }
+  for (int k = 0; k < 5; ++k)
+    for (int j = 0; j < 5; ++j)
+      if (n > 0 && ragged_overlap(s[k], B * H * src->t_cap * X[k], d[j], B * H * dst->t_cap * X[j]))
+        return TQ_ERR_INVALID_ARG;
+  if (ragged_overlap(src_weights, B * H * src->t_cap * 4, dst_weights, B * H * dst->t_cap * 4) ||
+      ragged_overlap(dst_len, B * 4, dst_off, B * 4) || ragged_overlap(dst_len, B * 4, count, B * 4) ||
+      ragged_overlap(dst_len, B * 4, index, B * (index_heads ? H : 1) * n * 4))
+    return TQ_ERR_INVALID_ARG;
   auto width = [](int bytes) { return bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4; };
   const int wk = width(X[0]), wv = width(X[3]), ws = width(X[1]);  // key and value codes: 16, or 8 at head_dim 64
   p.per[0] = X[0] / wk;

@@ -81,6 +81,12 @@ inline bool ragged_device_memory(std::initializer_list<const void*> ptrs) {
   }
   return true;
 }
+// Whether two arrays (null: none) share memory.
+inline bool ragged_overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) &&
+         y < x + static_cast<uintptr_t>(a_bytes);
+}
 inline bool ragged_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ragged_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool ragged_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }

@@ -103,6 +103,11 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
                         static_cast<const void*>(left_pad), static_cast<const void*>(lse)})
     if (!ragged_aligned4(x)) return TQ_ERR_ALIGNMENT;
   if (workspace_bytes < need) return TQ_ERR_INVALID_ARG;
+  const long long rows = B * Hq * N, out_bytes = rows * D * (out_dtype == TQ_F32 ? 4 : 2);
+  if (ragged_overlap(q, rows * D * 2, out, out_bytes) || ragged_overlap(q, rows * D * 2, lse, rows * 4) ||
+      ragged_overlap(q, rows * D * 2, workspace, need) || ragged_overlap(out, out_bytes, lse, rows * 4) ||
+      ragged_overlap(out, out_bytes, workspace, need) || ragged_overlap(lse, rows * 4, workspace, need))
+    return TQ_ERR_INVALID_ARG;
   auto view = [](const tq_packed_cache* c) {
     return PackedView{static_cast<const uint8_t*>(c->k_codes), static_cast<const uint16_t*>(c->k_scales),
                       static_cast<const uint16_t*>(c->k_zeros), static_cast<const uint8_t*>(c->v_codes),

@@ -348,26 +348,26 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
       const float2 sc = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(bits))));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-      uint32_t w[(VB + 1) / 2];
-      tile_words<VB>(a, half ^ u.flip, w);
-      uint32_t o[8];
+        uint32_t w[(VB + 1) / 2];
+        tile_words<VB>(a, half ^ u.flip, w);
+        uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float2 cc;
-        if constexpr (VB == 4) {
-          cc = table64(byte_field_addr(w, j, vstride, tab));
-        } else if constexpr (VT::PAIRS) {
-          cc = table64(field_addr<2 * VB, 7>(w, 2 * j * VB, 0u) + tab);
-        } else if constexpr (VB == 8) {
-          cc = make_float2(table32(byte_field_addr(w, 2 * j, vstride, tab)), table32(byte_field_addr(w, 2 * j + 1, vstride, tab)));
-        } else {
-          cc = make_float2(table32(field_addr<VB, 7>(w, 2 * j * VB, 0u) + tab),
-                           table32(field_addr<VB, 7>(w, (2 * j + 1) * VB, 0u) + tab));
+        for (int j = 0; j < 8; ++j) {
+          float2 cc;
+          if constexpr (VB == 4) {
+            cc = table64(byte_field_addr(w, j, vstride, tab));
+          } else if constexpr (VT::PAIRS) {
+            cc = table64(field_addr<2 * VB, 7>(w, 2 * j * VB, 0u) + tab);
+          } else if constexpr (VB == 8) {
+            cc = make_float2(table32(byte_field_addr(w, 2 * j, vstride, tab)), table32(byte_field_addr(w, 2 * j + 1, vstride, tab)));
+          } else {
+            cc = make_float2(table32(field_addr<VB, 7>(w, 2 * j * VB, 0u) + tab),
+                             table32(field_addr<VB, 7>(w, (2 * j + 1) * VB, 0u) + tab));
+          }
+          const float2 x = mul2(cc, sc);
+          o[j] = pack_bf16x2(x.x, x.y);
         }
-        const float2 x = mul2(cc, sc);
-        o[j] = pack_bf16x2(x.x, x.y);
-      }
-      u.store(sm + S::V_OFF + st * S::V_BYTES, i, half, o);
+        u.store(sm + S::V_OFF + st * S::V_BYTES, i, half, o);
       }
     }
     uint2 marks = make_uint2(0u, 0u);
