@@ -31,7 +31,7 @@ int tile_tokens(int64_t D) {
 
 // How the query rows of a kv head are laid out, and the scratch that follows.
 struct TreePlan {
-  long long R, RB, rows, copies, slots, HH, n_recs, rec_floats, prefix_bytes, bytes;
+  long long R, RB, rows, copies, slots, HH, n_recs, rec_floats, cut_bytes, bytes;
   int TT, DV;
 };
 
@@ -50,8 +50,8 @@ bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, bool f3
   if (B > 0 && t->HH > lim / B) return false;
   t->n_recs = sm_count() + B * t->HH;
   t->rec_floats = t->slots * (t->DV + 2);
-  t->prefix_bytes = ((B + 1) * 8 + 255) / 256 * 256;
-  t->bytes = t->prefix_bytes + t->n_recs * t->rec_floats * 4;
+  t->cut_bytes = ((kCutRows + B + 1) * 4 + 255) / 256 * 256;
+  t->bytes = t->cut_bytes + t->n_recs * t->rec_floats * 4;
   return true;
 }
 
@@ -84,15 +84,15 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   if (Hq % Hkv != 0 || cache->t_cap < T || tree->t_cap < N) return TQ_ERR_INVALID_ARG;
   if (!ragged_sizes_ok(B, Hkv, cache->t_cap) || !ragged_sizes_ok(B, Hkv, tree->t_cap) || !ragged_sizes_ok(B, Hq, N))
     return TQ_ERR_INVALID_ARG;
-  if (B * Hq > 0x7fffffffLL / N) return TQ_ERR_INVALID_ARG;
+  if (B * Hq > 0x7ffffff0LL / N) return TQ_ERR_INVALID_ARG;
   if (B == 0) return TQ_OK;
   const int64_t need = tq_tree_attention_workspace_size(B, Hq, Hkv, N, D);
   if (need < 0) return static_cast<tq_status>(-need);
   TreePlan t;
   tree_plan(B, Hq, Hkv, N, D, out_dtype == TQ_F32, &t);
-  // tiles in all, of which a block counts its own in 32 bits
+  // tiles in all (and what the turns count for) are counted in 32 bits
   const long long tiles = (T + t.TT - 1) / t.TT + 1 + (N + t.TT - 1) / t.TT;
-  if (tiles > (1LL << 36) / (B * t.HH)) return TQ_ERR_INVALID_ARG;
+  if (tiles + 16 > 0x7fffffffLL / (B * t.HH)) return TQ_ERR_INVALID_ARG;
   const void* ptrs[] = {q, out, workspace, tree->k_codes, tree->k_scales, tree->k_zeros, tree->v_codes, tree->v_scales,
                         cache->k_codes, cache->k_scales, cache->k_zeros, cache->v_codes, cache->v_scales};
   for (int i = 0; i < 13; ++i) {
@@ -128,8 +128,8 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   p.G = static_cast<int>(Hq / Hkv);
   p.N = static_cast<int>(N);
   p.T = static_cast<int>(T);
-  p.prefix = static_cast<long long*>(workspace);
-  p.recs = reinterpret_cast<float*>(static_cast<char*>(workspace) + t.prefix_bytes);
+  p.cut = static_cast<int*>(workspace);
+  p.recs = reinterpret_cast<float*>(static_cast<char*>(workspace) + t.cut_bytes);
   p.n_recs = t.n_recs;
   p.R = static_cast<int>(t.R);
   p.RB = static_cast<int>(t.RB);

@@ -37,7 +37,7 @@ struct TreeParams {
   const int* parents;
   const int* lens;
   const int* left_pad;
-  long long* prefix;  // [B + 1] tiles of one head before batch row b (written by block 0)
+  int* cut;           // how the line of tiles is cut (written by block 0, see kCutRows)
   float* recs;        // partial records
   void* out;
   float* lse;
@@ -60,6 +60,11 @@ struct TreeParams {
 template <int D, bool F32>
 struct TreeShape {
   static constexpr int SW = D <= 128 ? 2 : 1;        // groups of softmax warps
+  // What a segment's begin and end cost, in tiles. The cut counts it, so blocks
+  // that change segments get fewer tiles. Measured with 0 / 4 / 8 / 12: head_dim
+  // 128, 8 x 8192 tokens 57 / 56 / 53 / 55 us; 256, 4 x 8192 48 / 45 / 42 / 42;
+  // 512, 2 x 16384 71 / 64 / 64 / 65.
+  static constexpr int TURN = 8;
   static constexpr int TT = D >= 256 || (F32 && D > 64) ? 32 : 64;  // tokens of a tile
   static constexpr int DV = D == 512 ? 256 : D;      // value elements a block accumulates
   static constexpr int VH = D / DV;
@@ -125,7 +130,22 @@ constexpr int kTreeRows = 128;
 enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcPFull = 96, kcPFree = 128,
              kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcTile = 192, kcB = 196, kcHH = 200,
              kcCount = 204, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
-             kcBad = 352, kcMerge = 480, kcMerged = 488, kcMaxSum = 512 };
+             kcBad = 352, kcMerge = 480, kcMerged = 488, kcFrom = 496, kcTo = 500, kcMaxSum = 512 };
+
+// Words of TreeParams::cut: the turn's weight in tiles, a range's length, how
+// many ranges have one more; from kCutRows on [B + 1] the tiles of one segment a
+// row before batch row b.
+constexpr int kCutRows = 4;
+
+// Sum of the lanes' x up to this one.
+__device__ __forceinline__ int warp_prefix(int x, int lane) {
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, i);
+    if (lane >= i) x += y;
+  }
+  return x;
+}
 
 // Tiles of a batch row: the sequence's and the tree's.
 template <int TT>
@@ -514,18 +534,6 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     const int r = rb * p.rows + rl;
     const bool row = rl < p.rows && r < p.R;
     const bool work = __any_sync(kFull, row);  // a warp whose lanes have no row only keeps the barriers going
-    if (w.b != anc_b || rb != anc_rb) {
-      // (the walk up is one load after another: in shared memory)
-      volatile int* up = reinterpret_cast<volatile int*>(own);
-      if (p.parents != nullptr && w.b != anc_b) {
-        __syncwarp();
-        for (int i = lane; i < p.N; i += 32) up[i] = p.parents[static_cast<long long>(w.b) * p.N + i];
-        __syncwarp();
-      }
-      anc = row ? node_ancestors(p.parents == nullptr ? nullptr : up, r % p.N) : 0ull;
-      anc_b = w.b;
-      anc_rb = rb;
-    }
     // ---- the queries of the segment (every score of the last one is done),
     // each group its share of the columns, all loads of a round at once
     {
@@ -560,6 +568,19 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
       tmem_wait_st();
       tmem_fence_before();
       warp_arrive(bars + kcQFull, lane);
+    }
+    // ---- the rows' ancestors (while the first scores are on their way)
+    if (w.b != anc_b || rb != anc_rb) {
+      // (the walk up is one load after another: in shared memory)
+      volatile int* up = reinterpret_cast<volatile int*>(own);
+      if (p.parents != nullptr && w.b != anc_b) {
+        __syncwarp();
+        for (int i = lane; i < p.N; i += 32) up[i] = p.parents[static_cast<long long>(w.b) * p.N + i];
+        __syncwarp();
+      }
+      anc = row ? node_ancestors(p.parents == nullptr ? nullptr : up, r % p.N) : 0ull;
+      anc_b = w.b;
+      anc_rb = rb;
     }
     float m = kNegInf, l = 0.0f;
     // which of a tile's tokens the row attends to
@@ -816,46 +837,61 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
   pdl_wait();
   if (warp == 0) {
     // the block's range of the line of all tiles: 32 batch rows at a time
-    long long total = 0;
-    int n0 = 0;
+    int sum = 0, n0 = 0;  // tiles of one segment a row
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       n0 = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
-      long long c = n0;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(kFull, c, x);
-        if (lane >= x) c += y;
-      }
-      if (blockIdx.x == 0 && b0 + lane < p.B) p.prefix[b0 + lane + 1] = total + c;
-      total += __shfl_sync(kFull, c, 31);
+      const int c = warp_prefix(n0, lane);
+      if (blockIdx.x == 0 && b0 + lane < p.B) p.cut[kCutRows + b0 + lane + 1] = sum + c;
+      sum += __shfl_sync(kFull, c, 31);
     }
-    if (blockIdx.x == 0 && lane == 0) p.prefix[0] = 0;
-    // no more ranges than tiles: between a segment's first and last block
-    // every block has a part of it
-    total *= p.HH;
-    const long long ranges = min(total, static_cast<long long>(gridDim.x));
-    const long long first = min(blockIdx.x * total / ranges, total), end = min((blockIdx.x + 1) * total / ranges, total);
-    if (lane == 0) *reinterpret_cast<int*>(ctl + kcCount) = static_cast<int>(end - first);
-    long long before = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < p.B && !found && first < end; b0 += 32) {
+    // a segment's first tile counts for `turn` more, what its begin and end cost;
+    // no more ranges than tiles: between a segment's first and last block every
+    // block has a part of it
+    const unsigned all = static_cast<unsigned>(sum) * p.HH, ranges = min(all, gridDim.x);
+    const int turn = min(S::TURN, static_cast<int>(all / ranges));
+    const unsigned line = all + static_cast<unsigned>(turn) * p.B * p.HH, per = line / ranges, more = line - per * ranges;
+    if (blockIdx.x == 0 && lane == 0) {
+      p.cut[0] = turn;
+      p.cut[1] = static_cast<int>(per);
+      p.cut[2] = static_cast<int>(more);
+      p.cut[kCutRows] = 0;
+    }
+    const unsigned first = blockIdx.x < ranges ? blockIdx.x * per + min(blockIdx.x, more) : line;
+    const unsigned end = blockIdx.x < ranges ? first + per + (blockIdx.x < more ? 1u : 0u) : line;
+    volatile int* out = reinterpret_cast<volatile int*>(ctl);
+    if (lane == 0) {  // (tiles before the range's ends, when an end is the line's)
+      out[kcFrom / 4] = static_cast<int>(all);
+      out[kcTo / 4] = static_cast<int>(all);
+    }
+    __syncwarp();
+    int before = 0;
+    bool found = first >= line;
+    for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
       const int n = p.B <= 32 ? n0 : b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
-      long long c = n;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(kFull, c, x);
-        if (lane >= x) c += y;
+      const int c = before + warp_prefix(n, lane) - n;  // tiles of a segment before row b0 + lane
+      const unsigned start = (static_cast<unsigned>(c) + turn * (b0 + lane)) * p.HH, length = n + turn;
+      const bool real = b0 + lane < p.B;
+      // where a place of the line lies
+      auto find = [&](unsigned x, int& hh, int& tile) {
+        if (!real || x < start || x - start >= length * p.HH) return false;
+        hh = static_cast<int>((x - start) / length);
+        tile = max(static_cast<int>(x - start - hh * length) - turn, 0);
+        return true;
+      };
+      int hh, tile;
+      if (find(first, hh, tile)) {
+        out[kcB / 4] = b0 + lane;
+        out[kcHH / 4] = hh;
+        out[kcTile / 4] = tile;
+        out[kcFrom / 4] = c * p.HH + hh * n + tile;
       }
-      const long long start = (before + c - n) * p.HH, stop = (before + c) * p.HH;
-      const bool here = start <= first && first < stop;
-      if (here) {
-        *reinterpret_cast<int*>(ctl + kcB) = b0 + lane;
-        *reinterpret_cast<int*>(ctl + kcHH) = static_cast<int>((first - start) / n);
-        *reinterpret_cast<int*>(ctl + kcTile) = static_cast<int>((first - start) % n);
-      }
-      found = __any_sync(kFull, here);
-      before += __shfl_sync(kFull, c, 31);
+      const bool last = find(end, hh, tile);
+      if (last) out[kcTo / 4] = c * p.HH + hh * n + tile;
+      found = __any_sync(kFull, last);
+      before = __shfl_sync(kFull, c + n, 31);
     }
+    __syncwarp();
+    if (lane == 0) out[kcCount / 4] = out[kcTo / 4] - out[kcFrom / 4];
   }
   tmem_fence_before();
   __syncthreads();
@@ -928,19 +964,21 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(p.B) * p.Hq * p.N;
-  const long long row0 = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
-  const long long row = row0 < rows ? row0 : rows - 1;
-  const long long per_b = static_cast<long long>(p.Hq) * p.N;
-  const int b = static_cast<int>(row / per_b);
-  const int in_b = static_cast<int>(row - b * per_b);
+  const int rows = p.B * p.Hq * p.N, row0 = blockIdx.x * (4 / W) + warp / W, row = min(row0, rows - 1);
+  const int b = row / (p.Hq * p.N), in_b = row - b * (p.Hq * p.N);
   const int h = in_b / p.R, r = in_b - h * p.R, rb = r / p.rows, rl = r - rb * p.rows;
   const int half = S::VH == 1 ? 0 : lane >> 4;
   const int hh = (h * p.RB + rb) * S::VH + half;
-  const long long before = p.prefix[b], n = p.prefix[b + 1] - before, total = p.prefix[p.B] * p.HH;
-  const long long x0 = before * p.HH + hh * n, x1 = x0 + n - 1;
-  const long long ranges = min(total, static_cast<long long>(p.grid));
-  const int c0 = static_cast<int>(((x0 + 1) * ranges - 1) / total), c1 = static_cast<int>(((x1 + 1) * ranges - 1) / total);
+  // the blocks that hold the segment's first and last tile
+  const int turn = p.cut[0];
+  const unsigned per = p.cut[1], more = p.cut[2];
+  const int before = p.cut[kCutRows + b], n = p.cut[kCutRows + b + 1] - before;
+  const unsigned x0 = static_cast<unsigned>(before + turn * b) * p.HH + static_cast<unsigned>(hh) * (n + turn) + turn;
+  auto block_of = [&](unsigned x) {
+    const unsigned long_part = more * (per + 1);
+    return static_cast<int>(x < long_part ? x / (per + 1) : more + (x - long_part) / per);
+  };
+  const int c0 = block_of(x0), c1 = block_of(x0 + n - 1);
   const long long slot = static_cast<long long>(c0) + static_cast<long long>(b) * p.HH + hh;
   int parts = (c1 - c0 + 1) * p.copies;
   if (!TQ_CHECK(slot + (c1 - c0) < p.n_recs, p.err)) parts = 0;
@@ -953,16 +991,37 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   // LANES of them at a time: every lane looks at one maximum and sum, then all
   // take the values with the factors known (no result waits for the last one).
   constexpr int LANES = 32 / S::VH;
+  constexpr int AHEAD = E <= 4 ? 6 : E == 8 ? 4 : 2;
+  const int shift = p.copies - 1;
+  auto load = [&](int s, float (&x)[E]) {
+    const float* src = recs + (s >> shift) * rec_floats + 2 * p.slots +
+                       static_cast<long long>((s & (p.copies - 1)) * p.rows + rl) * S::DV + lane * E - half * S::DV;
+#pragma unroll
+    for (int i = 0; i < E; i += V) {
+      if constexpr (V == 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src + i);
+        x[i] = y.x; x[i + 1] = y.y;
+      } else {
+        const float4 y = *reinterpret_cast<const float4*>(src + i);
+        x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+      }
+    }
+  };
   int most = parts;
   if constexpr (S::VH > 1) most = max(parts, __shfl_xor_sync(kFull, parts, 16));
   for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
     const int mine = s0 + (lane % LANES) * W;
     float m2 = kNegInf, l2 = 0.0f;
     if (mine < parts) {
-      const float* rec = recs + (mine / p.copies) * rec_floats + (mine % p.copies) * p.rows + rl;
+      const float* rec = recs + (mine >> shift) * rec_floats + (mine & (p.copies - 1)) * p.rows + rl;
       m2 = rec[0];
       l2 = rec[p.slots];
     }
+    // the first AHEAD results' values meanwhile
+    float u[AHEAD][E];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (s0 + k * W < parts) load(s0 + k * W, u[k]);
     float mn = m2;
 #pragma unroll
     for (int x = LANES / 2; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, x));
@@ -976,29 +1035,23 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
     const int n_here = min(LANES, (most - s0 + W - 1) / W);
-#pragma unroll 4
-    for (int k = 0; k < n_here; ++k) {
+    // (a part that saw no key is left out, whatever its values are; nor does one
+    // past the end count)
+    auto add_part = [&](int k, const float (&x)[E]) {
       const float f = __shfl_sync(kFull, fb, half * LANES + k);
-      const int s = s0 + k * W;
-      if (f != 0.0f) {  // (a part that saw no key is left out, whatever its values are; nor does one past the end count)
-        const int at = (s % p.copies) * p.rows + rl;
-        const float* src = recs + (s / p.copies) * rec_floats + 2 * p.slots + static_cast<long long>(at) * S::DV + lane * E -
-                           half * S::DV;
+      if (f != 0.0f) {
 #pragma unroll
-        for (int i = 0; i < E; i += V) {
-          if constexpr (V == 2) {
-            const float2 u = *reinterpret_cast<const float2*>(src + i);
-            o[i] = __fmaf_rn(u.x, f, o[i]);
-            o[i + 1] = __fmaf_rn(u.y, f, o[i + 1]);
-          } else {
-            const float4 u = *reinterpret_cast<const float4*>(src + i);
-            o[i] = __fmaf_rn(u.x, f, o[i]);
-            o[i + 1] = __fmaf_rn(u.y, f, o[i + 1]);
-            o[i + 2] = __fmaf_rn(u.z, f, o[i + 2]);
-            o[i + 3] = __fmaf_rn(u.w, f, o[i + 3]);
-          }
-        }
+        for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(x[i], f, o[i]);
       }
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k < n_here) add_part(k, u[k]);
+#pragma unroll 4
+    for (int k = AHEAD; k < n_here; ++k) {
+      float x[E];
+      if (s0 + k * W < parts) load(s0 + k * W, x);
+      add_part(k, x);
     }
   }
   auto merge = [&](float m2, float l2, const float (&x)[E]) {
@@ -1057,14 +1110,14 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
     o[i] = __uint_as_float(__float_as_uint(__fmul_rn(o[i], p.rot_scale)) ^ flip);
   }
   if (p.out_f32) {
-    float* dst = static_cast<float*>(p.out) + row * D + e0;
+    float* dst = static_cast<float*>(p.out) + static_cast<long long>(row) * D + e0;
 #pragma unroll
     for (int i = 0; i < E; i += V) {
       if constexpr (V == 2) *reinterpret_cast<float2*>(dst + i) = make_float2(o[i], o[i + 1]);
       else *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     }
   } else {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + e0);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(row) * D + e0);
 #pragma unroll
     for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16x2(o[i], o[i + 1]);
   }
