@@ -30,21 +30,6 @@ __device__ __forceinline__ void row_range(const int* lens, const int* left_pad, 
   lo = left_pad != nullptr ? min(max(left_pad[b], 0), hi) : 0;
 }
 
-// The nodes that node i of a tree attends to, one bit each: i and its
-// ancestors, or none when i's chain of parents does not end at -1. A parent is
-// a lower number, so the walk ends.
-__device__ __forceinline__ unsigned long long node_ancestors(const volatile int* parents, int i) {
-  if (parents == nullptr) return i == 63 ? ~0ull : (2ull << i) - 1ull;
-  unsigned long long m = 0;
-  for (;;) {
-    m |= 1ull << i;
-    const int up = parents[i];
-    if (up == -1) return m;
-    if (up < 0 || up >= i) return 0ull;
-    i = up;
-  }
-}
-
 // ---- host side
 // Lets a kernel take `bytes` of dynamic shared memory on the current device
 // (asked for once per kernel and device).

@@ -96,8 +96,9 @@ struct TreeShape {
   static constexpr int VR_OFF = KR_OFF + NR * KR_BYTES;
   static constexpr int T_OFF = VR_OFF + NR * VR_BYTES;
   static constexpr int C_OFF = T_OFF + TAB;
-  // a softmax warp's own: the tree's parents, and 32 rows of 20 floats on their way to a record
-  static constexpr int W_OFF = C_OFF + 512 + (SW > 1 ? 2048 : 0), W_BYTES = 256 + 32 * 80;
+  // a softmax warp's own: 32 rows of 64 bytes (80 apart) of the queries or of a
+  // record, and the walk up the tree
+  static constexpr int W_OFF = C_OFF + 512 + (SW > 1 ? 2048 : 0), W_BYTES = 32 * 80;
   static constexpr int SMEM = W_OFF + 4 * SW * W_BYTES;
   // Tensor memory columns: SW outputs | NS score tiles of BUF columns | queries.
   // The weights of 16 tokens take the place of their scores: eight columns of
@@ -506,6 +507,50 @@ __device__ __forceinline__ float sub_bf16_f32(uint32_t x, float c) {
   return r;
 }
 
+// Node i's ancestors (and i) in a chain.
+__device__ __forceinline__ unsigned long long chain_ancestors(int i) { return i == 63 ? ~0ull : (2ull << i) - 1ull; }
+
+// Node `node`'s ancestors (and itself), one bit each, or none when its chain of
+// parents does not end at -1. up: the parents of nodes lane and lane + 32. Every
+// node's set joins the set of the node that it has come to, which has come as
+// far again: six rounds of reads that do not wait for one another, where the walk
+// from node to parent is a read after another (5000 cycles for 32 nodes). `own`:
+// 1056 bytes of shared memory of the warp.
+__device__ __forceinline__ unsigned long long tree_ancestors(uint32_t own, const int (&up)[2], int N, int node, int lane) {
+  constexpr int ROOT = 64, NONE = 65;  // where a chain ends: properly, or not
+  unsigned long long set[2];
+  int at[2];
+  auto store = [&](int i, unsigned long long m, int a) {
+    sts128(own + i * 16, static_cast<uint32_t>(m), static_cast<uint32_t>(m >> 32), static_cast<uint32_t>(a), 0u);
+  };
+  __syncwarp();
+  if (lane < 2) store(ROOT + lane, 0ull, ROOT + lane);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = lane + 32 * k;
+    set[k] = 1ull << i;
+    at[k] = up[k] == -1 ? ROOT : up[k] < 0 || up[k] >= i ? NONE : up[k];
+    if (i < N) store(i, set[k], at[k]);
+  }
+#pragma unroll 1
+  for (int span = 1; span < N; span *= 2) {
+    __syncwarp();
+    uint4 u[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) u[k] = lds128(own + at[k] * 16);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      set[k] |= static_cast<unsigned long long>(u[k].y) << 32 | u[k].x;
+      at[k] = static_cast<int>(u[k].z);
+      if (lane + 32 * k < N) store(lane + 32 * k, set[k], at[k]);
+    }
+  }
+  __syncwarp();
+  const uint4 u = lds128(own + node * 16);
+  return u.z == ROOT ? static_cast<unsigned long long>(u.y) << 32 | u.x : 0ull;
+}
+
 // The softmax warps (group `which` of SW, every SW-th tile): a thread holds one
 // lane of tensor memory, i.e. one query row over its copy's share of the tokens.
 template <int D, bool F32>
@@ -519,8 +564,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
   const uint32_t bars = sm + S::C_OFF;
   const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + kcTmem) + (static_cast<uint32_t>(warp) << 21);
   const uint32_t oc = tm + S::O_COL + which * S::DV;
-  const int own_off = S::W_OFF + (which * 4 + warp) * S::W_BYTES;  // the warp's own shared memory
-  uint8_t* own = smem + own_off;
+  const uint32_t own = sm + S::W_OFF + (which * 4 + warp) * S::W_BYTES;  // the warp's own shared memory
   const int copy = warp / QUADS, rl = (warp % QUADS) * 32 + lane, col0 = copy * W;
   auto s_full = [&](int it) { return warp_wait(bars + kcSFull + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
   auto weighed = [&](int it) { return warp_wait(bars + kcPFree + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
@@ -534,33 +578,63 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     const int r = rb * p.rows + rl;
     const bool row = rl < p.rows && r < p.R;
     const bool work = __any_sync(kFull, row);  // a warp whose lanes have no row only keeps the barriers going
-    // ---- the queries of the segment (every score of the last one is done),
-    // each group its share of the columns, all loads of a round at once
+    const bool climb = w.b != anc_b || rb != anc_rb;
+    int up[2] = {-1, -1};  // parents of nodes lane, lane + 32
+    if (climb && p.parents != nullptr) {
+      const int* from = p.parents + static_cast<long long>(w.b) * p.N;
+      if (lane < p.N) up[0] = __ldg(from + lane);
+      if (lane + 32 < p.N) up[1] = __ldg(from + lane + 32);
+    }
+    // ---- the queries of the segment (every score of the last one is done), each
+    // group its share of the columns. Eight rows of 64 bytes a load, turned in
+    // shared memory (a lane for each row would touch 32 lines a load).
     {
       if (it0 > 0 && !s_full(it0 - 1)) return;
       tmem_fence_after();
       const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N + (row ? r : 0)) * D);
+          p.q + (static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N * D);
+      // row x of the warp's 32, or -1
+      auto row_at = [&](int x) {
+        const int at = (warp % QUADS) * 32 + x;
+        return at < p.rows && rb * p.rows + at < p.R ? rb * p.rows + at : -1;
+      };
+      int from[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) from[i] = row_at(8 * i + (lane >> 2));
       constexpr int SHARE = S::QT / 2 / S::SW, STEP = SHARE < 32 ? SHARE : 32;
 #pragma unroll 1
       for (int c = which * SHARE; c < (which + 1) * SHARE; c += STEP) {
-        uint4 u[STEP / 4];
+        uint4 u[STEP / 16][4];
 #pragma unroll
-        for (int i = 0; i < STEP / 4; ++i) u[i] = row ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < STEP / 16; ++k)
 #pragma unroll
-        for (int i = 0; i < STEP / 16; ++i) {
-          const uint32_t x[16] = {u[4 * i].x,     u[4 * i].y,     u[4 * i].z,     u[4 * i].w,
-                                  u[4 * i + 1].x, u[4 * i + 1].y, u[4 * i + 1].z, u[4 * i + 1].w,
-                                  u[4 * i + 2].x, u[4 * i + 2].y, u[4 * i + 2].z, u[4 * i + 2].w,
-                                  u[4 * i + 3].x, u[4 * i + 3].y, u[4 * i + 3].z, u[4 * i + 3].w};
-          tmem_st16(tm + S::Q_COL + c + 16 * i, x);
+          for (int i = 0; i < 4; ++i)
+            u[k][i] = from[i] >= 0 ? __ldg(src + static_cast<long long>(from[i]) * (D / 8) + c / 4 + 4 * k + (lane & 3))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < STEP / 16; ++k) {
+          uint32_t x[16];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts128(own + (8 * i + (lane >> 2)) * 80 + (lane & 3) * 16, u[k][i].x, u[k][i].y, u[k][i].z, u[k][i].w);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 y = lds128(own + lane * 80 + i * 16);
+            x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+          }
+          tmem_st16(tm + S::Q_COL + c + 16 * k, x);
         }
       }
       if constexpr (S::QT < D) {
+        static_assert(D - S::QT == 256, "a row's rest: 16 bytes a lane");
 #pragma unroll 8
-        for (int c = 0; c < (D - S::QT) / 8; ++c) {
-          const uint4 u = row ? __ldg(src + S::QT / 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-          sts128(sm + S::Q_OFF + (c >> 3) * (128 * 128) + (warp * 32 + lane) * 128 + (((c ^ lane) & 7) << 4), u.x, u.y,
+        for (int x = 0; x < 32; ++x) {
+          const int r2 = row_at(x);
+          const uint4 u = r2 >= 0 ? __ldg(src + static_cast<long long>(r2) * (D / 8) + S::QT / 8 + lane)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+          sts128(sm + S::Q_OFF + (lane >> 3) * (128 * 128) + (warp * 32 + x) * 128 + (((lane ^ x) & 7) << 4), u.x, u.y,
                  u.z, u.w);
         }
         fence_proxy_async();
@@ -570,15 +644,12 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
       warp_arrive(bars + kcQFull, lane);
     }
     // ---- the rows' ancestors (while the first scores are on their way)
-    if (w.b != anc_b || rb != anc_rb) {
-      // (the walk up is one load after another: in shared memory)
-      volatile int* up = reinterpret_cast<volatile int*>(own);
-      if (p.parents != nullptr && w.b != anc_b) {
-        __syncwarp();
-        for (int i = lane; i < p.N; i += 32) up[i] = p.parents[static_cast<long long>(w.b) * p.N + i];
-        __syncwarp();
+    if (climb) {
+      anc = !row ? 0ull : p.parents == nullptr ? chain_ancestors(r % p.N) : 0ull;
+      if (p.parents != nullptr) {
+        const unsigned long long all = tree_ancestors(own, up, p.N, row ? r % p.N : 0, lane);
+        if (row) anc = all;
       }
-      anc = row ? node_ancestors(p.parents == nullptr ? nullptr : up, r % p.N) : 0ull;
       anc_b = w.b;
       anc_rb = rb;
     }
@@ -618,14 +689,14 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
         // hidden tokens (a tile at an end of the sequence, the tree): their
         // scores become -inf in place
         if (tile >= w.n_main - 1 || (tile == 0 && (w.lo & 15) != 0)) {
-          unsigned long long own = attended(tile) >> col0;
+          unsigned long long shown = attended(tile) >> col0;
 #pragma unroll 1
-          for (int c = col0; c < col0 + W; c += 16, own >>= 16) {
+          for (int c = col0; c < col0 + W; c += 16, shown >>= 16) {
             uint32_t s[16];
             tmem_ld16(buf + c, s);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = (static_cast<uint32_t>(own) >> i & 1) ? s[i] : 0xff800000u;
+            for (int i = 0; i < 16; ++i) s[i] = (static_cast<uint32_t>(shown) >> i & 1) ? s[i] : 0xff800000u;
             tmem_st16(buf + c, s);
           }
           tmem_wait_st();
@@ -752,15 +823,17 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
           o[i] = __float_as_uint(x);
         }
         // through shared memory: eight rows of 64 bytes a store, not 32 of 16
+        // (records that keep eight elements of a row, then of the next, need no
+        // turn here, but cost the combine more than
+        // they save)
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sts128(sm + own_off + 256 + lane * 80 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) sts128(own + lane * 80 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int x = 8 * i + (lane >> 2), to = (warp % QUADS) * 32 + x;
-          const uint4 u = lds128(sm + own_off + 256 + x * 80 + (lane & 3) * 16);
+          const uint4 u = lds128(own + x * 80 + (lane & 3) * 16);
           if (to < p.rows && r - rl + to < p.R && store_ok)
             *reinterpret_cast<uint4*>(rec + 2 * p.slots + static_cast<long long>(copy * p.rows + to) * S::DV + c +
                                       (lane & 3) * 4) = u;
@@ -955,7 +1028,7 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
 // (Hadamard butterflies, / sqrt(D), signs) and stores it. W warps share a row.
 // Lane L holds elements [L D/32, (L+1) D/32).
 template <int D, int W>
-__global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) tree_combine_kernel(const __grid_constant__ TreeParams p) {
   using S = TreeShape<D, false>;  // (what is read here is the same for both)
   constexpr int E = D / 32;
   constexpr int V = E < 4 ? E : 4;
@@ -991,11 +1064,11 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   // LANES of them at a time: every lane looks at one maximum and sum, then all
   // take the values with the factors known (no result waits for the last one).
   constexpr int LANES = 32 / S::VH;
-  constexpr int AHEAD = E <= 4 ? 6 : E == 8 ? 4 : 2;
+  constexpr int AHEAD = E <= 4 ? 6 : 2;
   const int shift = p.copies - 1;
   auto load = [&](int s, float (&x)[E]) {
     const float* src = recs + (s >> shift) * rec_floats + 2 * p.slots +
-                       static_cast<long long>((s & (p.copies - 1)) * p.rows + rl) * S::DV + lane * E - half * S::DV;
+                       static_cast<long long>((s & (p.copies - 1)) * p.rows + rl) * S::DV + (lane - half * LANES) * E;
 #pragma unroll
     for (int i = 0; i < E; i += V) {
       if constexpr (V == 2) {
