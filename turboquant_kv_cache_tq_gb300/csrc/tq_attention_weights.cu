@@ -60,9 +60,13 @@ struct WeightsShape {
 // Warps 0-3 and 4-7 sum, 8-15 decode, 16 matrix instructions, 17 loads, 18 and
 // 19 copy what no tile covers.
 constexpr int kWeightsThreads = 640;
+// What a change of (batch row, kv head) costs, in tiles, for the cut: 0 / 2 / 8
+// measured 95 / 90 / 88 us (32 x 8192 tokens) and 192 / 192 / 200 us where the
+// rows are copied narrowly.
+constexpr int kWeightsTurn = 2;
 
 enum : int { wcKFull = 0, wcKEmpty = 16, wcSFull = 32, wcSFree = 48, wcQFull = 64, wcLoaded = 72, wcTaken = 104,
-             wcDrain = 136, wcTmem = 144, wcQuit = 148, wcTile = 152, wcB = 156, wcH = 160, wcCount = 164, wcOdd = 168, wcTurn = 176 };
+             wcDrain = 136, wcTmem = 144, wcQuit = 148, wcOdd = 152, wcStart = 160, wcTurn = 176 };
 
 __device__ __forceinline__ int observers(const WeightsParams& p, int b) {
   return p.n_path != nullptr ? min(max(p.n_path[b], 0), p.P) : p.P;
@@ -91,10 +95,11 @@ struct WeightsWalk {
     rounds = (p.G * obs + NB - 1) / NB;
   }
   __device__ __forceinline__ void init(const WeightsParams& p, const uint8_t* ctl) {
-    tile = *reinterpret_cast<const int*>(ctl + wcTile);
-    b = *reinterpret_cast<const int*>(ctl + wcB);
-    h = *reinterpret_cast<const int*>(ctl + wcH);
-    left = *reinterpret_cast<const int*>(ctl + wcCount);
+    const int4 start = *reinterpret_cast<const int4*>(ctl + wcStart);
+    b = start.x;
+    h = start.y;
+    tile = start.z;
+    left = start.w;
     if (left > 0) {
       row(p);
       tiles = min(left, n - tile);
@@ -251,7 +256,8 @@ __device__ void weights_sum(const WeightsParams& p, uint32_t sm, uint8_t* smem, 
   const uint32_t tm = *reinterpret_cast<const uint32_t*>(ctl + wcTmem) + (static_cast<uint32_t>(warp) << 21) + 256 * which;
   float* s_lse = reinterpret_cast<float*>(smem + S::L_OFF);
   const float kInf = __int_as_float(0x7f800000), by = __fmul_rn(p.scale, 1.44269504088896341f);
-  volatile int* odd = reinterpret_cast<volatile int*>(ctl + wcOdd);  // whether a column of the round is no row of the sum
+  // whether a column of this round is no row of the sum (the next round has the other word)
+  volatile int* odd = reinterpret_cast<volatile int*>(ctl + wcOdd);
   const int tid = warp * 32 + lane;
   WeightsWalk<S::TT, S::NB> w;
   w.init(p, ctl);
@@ -259,47 +265,44 @@ __device__ void weights_sum(const WeightsParams& p, uint32_t sm, uint8_t* smem, 
   for (; w.left > 0; w.next(p)) {
     for (int round = 0; round < w.rounds; ++round) {
       const int cols = min(S::NB, p.G * w.obs - round * S::NB);
-      if (which == 0) {
-        // the round's query rows and -lse log2(e), once the last round's scores
-        // are computed and summed by both groups
-        if (it0 > 0) {
-          if (!warp_wait(bars + wcSFull + 8 * ((it0 - 1) & 1), ((it0 - 1) / 2) & 1, quit, p.err)) return;
-          if (it0 > 1) {
-            const int last = ((it0 - 1) & 1) ? it0 - 1 : it0 - 2;  // the other group's last tile
-            if (!warp_wait(bars + wcSFree + 8, (last / 2) & 1, quit, p.err)) return;
-          }
-          if (tid == 0) *odd = 0;
-          warp_arrive(bars + wcTurn, lane);  // and by every warp of this one
-          if (!warp_wait(bars + wcTurn, turns & 1, quit, p.err)) return;
-          ++turns;
-        }
-        for (int c = tid; c < S::NB; c += 128) {
-          float x = -kInf;  // no such row: nothing is added
+      // the round's query rows and -lse log2(e), once the last round's scores are
+      // computed and summed by both groups. A warp takes every eighth column: lane
+      // x looks up the row of its x-th, then the warp copies row after row.
+      if (turns > 0) {
+        warp_arrive(bars + wcTurn, lane);
+        if (!warp_wait(bars + wcTurn, (turns - 1) & 1, quit, p.err)) return;
+      }
+      if (which == 0 && tid == 0) odd[(turns + 1) & 1] = 0;  // (the last round's, read by nobody now)
+      const uint32_t odd_now = bars + wcOdd + 4 * (turns & 1);
+      ++turns;
+      {
+        constexpr int CW = S::NB / 8, PER = D / 8;  // PER: 16-byte pieces of a row
+        const int c0 = which * 4 + warp, c = c0 + 8 * lane;
+        long long from = -1;  // no such row: zeros
+        if (lane < CW) {
+          float x = -kInf;  // nothing is added
           if (c < cols) {
             const int cc = round * S::NB + c, i = cc / p.G, g = cc - i * p.G;
             const int node = p.path != nullptr ? p.path[static_cast<long long>(w.b) * p.P + i] : i;
             if (node >= 0 && node < p.N) {
-              const float lse = p.lse[(static_cast<long long>(w.b) * p.Hq + w.h * p.G + g) * p.N + node];
+              from = (static_cast<long long>(w.b) * p.Hq + w.h * p.G + g) * p.N + node;
+              const float lse = p.lse[from];
               x = lse == -kInf ? -kInf : __fmul_rn(lse, -1.44269504088896341f);
             }
-            if (x == -kInf) *odd = 1;
+            if (x == -kInf) odd[(turns - 1) & 1] = 1;
           }
           s_lse[c] = x;
         }
-        constexpr int PER = D / 8;  // 16-byte pieces of a row
-        const int rows = (cols + 15) & ~15;
-#pragma unroll 4
-        for (int i = tid; i < rows * PER; i += 128) {
-          const int c = i / PER, k = i - c * PER;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (c < cols) {
-            const int cc = round * S::NB + c, ob = cc / p.G, g = cc - ob * p.G;
-            const int node = p.path != nullptr ? p.path[static_cast<long long>(w.b) * p.P + ob] : ob;
-            if (node >= 0 && node < p.N)
-              v = __ldg(reinterpret_cast<const uint4*>(
-                            p.q + ((static_cast<long long>(w.b) * p.Hq + w.h * p.G + g) * p.N + node) * D) + k);
+        const int pieces = (cols + 15) / 16 * 2 * PER;
+#pragma unroll 8
+        for (int i = 0; i < CW * PER / 32; ++i) {
+          const int at = i * 32 + lane, x = at / PER, k = at - x * PER;
+          const long long r = __shfl_sync(kFull, from, x);
+          if (at < pieces) {
+            const uint4 v = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + r * D) + k) : make_uint4(0u, 0u, 0u, 0u);
+            sts128(sm + S::Q_OFF + (k >> 3) * (S::NB * 128) + (c0 + 8 * x) * 128 + (((k ^ c0) & 7) << 4), v.x, v.y, v.z,
+                   v.w);
           }
-          sts128(sm + S::Q_OFF + (k >> 3) * (S::NB * 128) + c * 128 + (((k ^ c) & 7) << 4), v.x, v.y, v.z, v.w);
         }
         fence_proxy_async();
         warp_arrive(bars + wcQFull, lane);
@@ -322,7 +325,7 @@ __device__ void weights_sum(const WeightsParams& p, uint32_t sm, uint8_t* smem, 
         float2 sum = f2(0.0f);
         if (__any_sync(kFull, mine)) {
           tmem_fence_after();
-          const bool plain = *odd == 0 && !__any_sync(kFull, first > 0);
+          const bool plain = lds32(odd_now) == 0 && !__any_sync(kFull, first > 0);
 #pragma unroll 1
           for (int c = 0; c < cols; c += 16) {
             uint32_t s[16];
@@ -378,11 +381,11 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
       mbar_init(bars + wcLoaded + 8 * i, p.bulk ? 1 : 33);
       mbar_init(bars + wcTaken + 8 * i, S::DWARPS);
     }
-    mbar_init(bars + wcQFull, 4);
+    mbar_init(bars + wcQFull, 8);
     mbar_init(bars + wcDrain, 1);
-    mbar_init(bars + wcTurn, 4);
+    mbar_init(bars + wcTurn, 8);
     *reinterpret_cast<int*>(ctl + wcQuit) = 0;
-    *reinterpret_cast<int*>(ctl + wcOdd) = 0;
+    *reinterpret_cast<int2*>(ctl + wcOdd) = make_int2(0, 0);
     mbar_fence_init();
   }
   __syncthreads();
@@ -400,36 +403,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
-    // the block's range of the line of all tiles: 32 batch rows at a time
-    long long total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      total += __reduce_add_sync(kFull, b < p.B ? weights_row_tiles<S::TT>(p, b) : 0);
-    }
-    total *= p.Hkv;
-    const long long ranges = gridDim.x;
-    const long long first = blockIdx.x * total / ranges, end = (blockIdx.x + 1) * total / ranges;
-    if (lane == 0) *reinterpret_cast<int*>(ctl + wcCount) = static_cast<int>(end - first);
-    long long before = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < p.B && !found && first < end; b0 += 32) {
-      const int n = b0 + lane < p.B ? weights_row_tiles<S::TT>(p, b0 + lane) : 0;
-      long long c = n;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(kFull, c, x);
-        if (lane >= x) c += y;
-      }
-      const long long start = (before + c - n) * p.Hkv, stop = (before + c) * p.Hkv;
-      const bool here = start <= first && first < stop;
-      if (here) {
-        *reinterpret_cast<int*>(ctl + wcB) = b0 + lane;
-        *reinterpret_cast<int*>(ctl + wcH) = static_cast<int>((first - start) / n);
-        *reinterpret_cast<int*>(ctl + wcTile) = static_cast<int>((first - start) % n);
-      }
-      found = __any_sync(kFull, here);
-      before += __shfl_sync(kFull, c, 31);
-    }
+    cut_line<false>([&](int b) { return weights_row_tiles<S::TT>(p, b); }, p.B, p.Hkv, kWeightsTurn, lane,
+                    reinterpret_cast<volatile int*>(ctl + wcStart), nullptr);
   }
   tmem_fence_before();
   __syncthreads();
@@ -508,6 +483,7 @@ extern "C" tq_status tq_attention_weights(const void* q, const float* lse, int64
   if (!ragged_sizes_ok(B, Hkv, t_cap) || !ragged_sizes_ok(B, Hkv, w_cap) || !ragged_sizes_ok(B, Hq, N) ||
       N > lim / 512)
     return TQ_ERR_INVALID_ARG;
+  if (B > 0 && T / 64 + 32 > lim / (B * Hkv)) return TQ_ERR_INVALID_ARG;  // (tiles are counted in 32 bits)
   if (B == 0 || w_cap == 0) return TQ_OK;
   const void* ptrs[] = {q, k_codes, k_scales, k_zeros};
   for (const void* x : ptrs) {

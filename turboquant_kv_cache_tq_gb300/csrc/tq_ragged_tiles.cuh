@@ -16,6 +16,81 @@ __device__ __forceinline__ int sequence_tiles(int lo, int hi) {
   return hi > lo ? (hi - (lo & ~15) + TT - 1) / TT : 0;
 }
 
+// Sum of the lanes' x up to this one.
+__device__ __forceinline__ int warp_prefix(int x, int lane) {
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, i);
+    if (lane >= i) x += y;
+  }
+  return x;
+}
+
+// A block's range of the line of all tiles, found by one warp. Batch row b has
+// `heads` segments of tiles(b) tiles; the line is cut evenly into one range per
+// block, where a segment's first tile counts for up to `turn_cost` tiles more, as
+// a change of segments takes time. No more ranges than tiles: between a segment's
+// first and last block every block has a part of it. `start` gets, from word 0,
+// the range's first batch row, segment and tile and its number of tiles. CUT:
+// block 0 also writes what finds a tile's block again: cut[0] what a turn
+// counts, [1] the length of a range, [2] how many ranges have one more, from
+// kCutRows on [B + 1] the tiles of one segment a row before batch row b.
+constexpr int kCutRows = 4;
+template <bool CUT, typename Tiles>
+__device__ __forceinline__ void cut_line(Tiles tiles, int B, int heads, int turn_cost, int lane, volatile int* start,
+                                         int* cut) {
+  int sum = 0, rows = 0, n0 = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    n0 = b0 + lane < B ? tiles(b0 + lane) : 0;
+    const int c = warp_prefix(n0, lane);
+    if (CUT && blockIdx.x == 0 && b0 + lane < B) cut[kCutRows + b0 + lane + 1] = sum + c;
+    sum += __shfl_sync(kFull, c, 31);
+    rows += __popc(__ballot_sync(kFull, n0 > 0));
+  }
+  const unsigned all = static_cast<unsigned>(sum) * heads, ranges = max(min(all, gridDim.x), 1u);
+  const int turn = min(turn_cost, static_cast<int>(all / ranges));
+  const unsigned line = all + static_cast<unsigned>(turn) * rows * heads, per = line / ranges, more = line - per * ranges;
+  if (CUT && blockIdx.x == 0 && lane == 0) {
+    cut[0] = turn;
+    cut[1] = static_cast<int>(per);
+    cut[2] = static_cast<int>(more);
+    cut[kCutRows] = 0;
+  }
+  const unsigned first = blockIdx.x < ranges ? blockIdx.x * per + min(blockIdx.x, more) : line;
+  const unsigned end = blockIdx.x < ranges ? first + per + (blockIdx.x < more ? 1u : 0u) : line;
+  unsigned from = all, to = all;  // tiles before the two ends
+  int before = 0, ahead = 0;      // tiles and places of a segment a row before b0
+  bool found = first >= line;
+  for (int b0 = 0; b0 < B && !found; b0 += 32) {
+    const int n = B <= 32 ? n0 : b0 + lane < B ? tiles(b0 + lane) : 0;
+    const unsigned length = n > 0 ? n + turn : 0;
+    const int c = before + warp_prefix(n, lane) - n, l = ahead + warp_prefix(static_cast<int>(length), lane);
+    const unsigned at = (l - length) * heads;
+    // where a place of the line lies
+    auto find = [&](unsigned x, int& hh, int& tile) {
+      if (x < at || x - at >= length * heads) return false;
+      hh = static_cast<int>((x - at) / length);
+      tile = max(static_cast<int>(x - at - hh * length) - turn, 0);
+      return true;
+    };
+    int hh = 0, tile = 0;
+    const bool here = find(first, hh, tile);
+    if (here) {
+      start[0] = b0 + lane;
+      start[1] = hh;
+      start[2] = tile;
+    }
+    unsigned who = __ballot_sync(kFull, here);
+    if (who != 0) from = __shfl_sync(kFull, static_cast<unsigned>(c * heads + hh * n + tile), __ffs(who) - 1);
+    who = __ballot_sync(kFull, find(end, hh, tile));
+    if (who != 0) to = __shfl_sync(kFull, static_cast<unsigned>(c * heads + hh * n + tile), __ffs(who) - 1);
+    found = who != 0;
+    before = __shfl_sync(kFull, c + n, 31);
+    ahead = __shfl_sync(kFull, l, 31);
+  }
+  if (lane == 0) start[3] = static_cast<int>(to - from);
+}
+
 // Where the groups of a decoding thread sit. Eight lanes take four groups of
 // two tokens (head_dim 64: two groups of four), and a thread decodes its
 // group's two halves of 16 elements in the order (flip, 1 - flip). So the eight

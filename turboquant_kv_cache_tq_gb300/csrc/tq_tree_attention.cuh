@@ -37,7 +37,7 @@ struct TreeParams {
   const int* parents;
   const int* lens;
   const int* left_pad;
-  int* cut;           // how the line of tiles is cut (written by block 0, see kCutRows)
+  int* cut;           // how the line of tiles is cut (written by block 0, see cut_line)
   float* recs;        // partial records
   void* out;
   float* lse;
@@ -129,24 +129,8 @@ constexpr int kTreeRows = 128;
 
 // Control words in shared memory (byte offsets).
 enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcPFull = 96, kcPFree = 128,
-             kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcTile = 192, kcB = 196, kcHH = 200,
-             kcCount = 204, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
-             kcBad = 352, kcMerge = 480, kcMerged = 488, kcFrom = 496, kcTo = 500, kcMaxSum = 512 };
-
-// Words of TreeParams::cut: the turn's weight in tiles, a range's length, how
-// many ranges have one more; from kCutRows on [B + 1] the tiles of one segment a
-// row before batch row b.
-constexpr int kCutRows = 4;
-
-// Sum of the lanes' x up to this one.
-__device__ __forceinline__ int warp_prefix(int x, int lane) {
-#pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, i);
-    if (lane >= i) x += y;
-  }
-  return x;
-}
+             kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcStart = 192, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
+             kcBad = 352, kcMerge = 480, kcMerged = 488, kcMaxSum = 512 };
 
 // Tiles of a batch row: the sequence's and the tree's.
 template <int TT>
@@ -169,10 +153,11 @@ struct TreeWalk {
     n = n_main + (p.N + TT - 1) / TT;
   }
   __device__ __forceinline__ void init(const TreeParams& p, const uint8_t* ctl) {
-    tile = *reinterpret_cast<const int*>(ctl + kcTile);
-    b = *reinterpret_cast<const int*>(ctl + kcB);
-    hh = *reinterpret_cast<const int*>(ctl + kcHH);
-    left = *reinterpret_cast<const int*>(ctl + kcCount);
+    const int4 start = *reinterpret_cast<const int4*>(ctl + kcStart);
+    b = start.x;
+    hh = start.y;
+    tile = start.z;
+    left = start.w;
     if (left > 0) row(p);
   }
   __device__ __forceinline__ void next_segment(const TreeParams& p) {
@@ -290,7 +275,7 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
   constexpr int KB = KeySpec<KMODE>::B, X = D * KB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
-  const int count = *reinterpret_cast<const int*>(ctl + kcCount);
+  const int count = *reinterpret_cast<const int*>(ctl + kcStart + 12);
   const int which = warp8 / S::KWARPS;
   const TileUnit<S::TT, S::NGS, S::KWARPS> u(warp8 % S::KWARPS, lane);
   // (two parts a tile: a warp's part is always the same one)
@@ -344,7 +329,7 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
   // the lane's copy of the value table
   const uint32_t tab = sm + S::T_OFF + (VT::PAIRS ? 8u * (lane & 15) : 4u * lane);
   const uint32_t vstride = p.vtab_stride;
-  const int count = *reinterpret_cast<const int*>(ctl + kcCount);
+  const int count = *reinterpret_cast<const int*>(ctl + kcStart + 12);
   const int wv = warp8 % S::VWARPS;
   const TileUnit<S::TT, S::NGV, S::VWARPS> u(wv, lane);
   const uint32_t codes = sm + S::VR_OFF + u.token * X + u.group * (4 * VB);
@@ -824,8 +809,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
         }
         // through shared memory: eight rows of 64 bytes a store, not 32 of 16
         // (records that keep eight elements of a row, then of the next, need no
-        // turn here, but cost the combine more than
-        // they save)
+        // turn here, but cost the combine more than they save)
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) sts128(own + lane * 80 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -909,62 +893,8 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
-    // the block's range of the line of all tiles: 32 batch rows at a time
-    int sum = 0, n0 = 0;  // tiles of one segment a row
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      n0 = b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
-      const int c = warp_prefix(n0, lane);
-      if (blockIdx.x == 0 && b0 + lane < p.B) p.cut[kCutRows + b0 + lane + 1] = sum + c;
-      sum += __shfl_sync(kFull, c, 31);
-    }
-    // a segment's first tile counts for `turn` more, what its begin and end cost;
-    // no more ranges than tiles: between a segment's first and last block every
-    // block has a part of it
-    const unsigned all = static_cast<unsigned>(sum) * p.HH, ranges = min(all, gridDim.x);
-    const int turn = min(S::TURN, static_cast<int>(all / ranges));
-    const unsigned line = all + static_cast<unsigned>(turn) * p.B * p.HH, per = line / ranges, more = line - per * ranges;
-    if (blockIdx.x == 0 && lane == 0) {
-      p.cut[0] = turn;
-      p.cut[1] = static_cast<int>(per);
-      p.cut[2] = static_cast<int>(more);
-      p.cut[kCutRows] = 0;
-    }
-    const unsigned first = blockIdx.x < ranges ? blockIdx.x * per + min(blockIdx.x, more) : line;
-    const unsigned end = blockIdx.x < ranges ? first + per + (blockIdx.x < more ? 1u : 0u) : line;
-    volatile int* out = reinterpret_cast<volatile int*>(ctl);
-    if (lane == 0) {  // (tiles before the range's ends, when an end is the line's)
-      out[kcFrom / 4] = static_cast<int>(all);
-      out[kcTo / 4] = static_cast<int>(all);
-    }
-    __syncwarp();
-    int before = 0;
-    bool found = first >= line;
-    for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
-      const int n = p.B <= 32 ? n0 : b0 + lane < p.B ? tree_row_tiles<S::TT>(p, b0 + lane) : 0;
-      const int c = before + warp_prefix(n, lane) - n;  // tiles of a segment before row b0 + lane
-      const unsigned start = (static_cast<unsigned>(c) + turn * (b0 + lane)) * p.HH, length = n + turn;
-      const bool real = b0 + lane < p.B;
-      // where a place of the line lies
-      auto find = [&](unsigned x, int& hh, int& tile) {
-        if (!real || x < start || x - start >= length * p.HH) return false;
-        hh = static_cast<int>((x - start) / length);
-        tile = max(static_cast<int>(x - start - hh * length) - turn, 0);
-        return true;
-      };
-      int hh, tile;
-      if (find(first, hh, tile)) {
-        out[kcB / 4] = b0 + lane;
-        out[kcHH / 4] = hh;
-        out[kcTile / 4] = tile;
-        out[kcFrom / 4] = c * p.HH + hh * n + tile;
-      }
-      const bool last = find(end, hh, tile);
-      if (last) out[kcTo / 4] = c * p.HH + hh * n + tile;
-      found = __any_sync(kFull, last);
-      before = __shfl_sync(kFull, c + n, 31);
-    }
-    __syncwarp();
-    if (lane == 0) out[kcCount / 4] = out[kcTo / 4] - out[kcFrom / 4];
+    cut_line<true>([&](int b) { return tree_row_tiles<S::TT>(p, b); }, p.B, p.HH, S::TURN, lane,
+                   reinterpret_cast<volatile int*>(ctl + kcStart), p.cut);
   }
   tmem_fence_before();
   __syncthreads();
