@@ -264,6 +264,36 @@ def test_tree_many_batch_rows():
         rc.check_tree(got, lse, ref)
 
 
+def _roomy(main, cap):
+    """The same tokens at the start of a cache of `cap` tokens whose other bytes are all ones."""
+    big = {}
+    for k, v in rc.to_gpu(main).items():
+        big[k] = torch.full((*v.shape[:2], cap, v.shape[3]), 255, dtype=torch.uint8, device="cuda") if v.dtype == torch.uint8 \
+            else torch.full((*v.shape[:2], cap, v.shape[3]), -1, dtype=torch.int16, device="cuda").view(torch.float16)
+        big[k][:, :, :v.shape[2]] = v
+    return big
+
+
+@pytest.mark.parametrize("kb,ks", KEY_MODES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,N", [(4, 16), (1, 1), (3, 5), (2, 31), (1, 64)])
+def test_tree_two_lanes_a_row(D, kb, ks, G, N):
+    """The bound T of the lengths, not the lengths, decides how rows are laid out: few
+    rows and a large T give each two lanes."""
+    B, Hkv, T, cap = 3, 2, 201, 26112
+    lens, pad = [201, 64, 0], [0, 5, 0]
+    vb = {(2, False): 2, (4, False): 3, (5, False): 4, (8, False): 5, (8, True): 8}[(kb, ks)]
+    main, tree = (rc.random_cache(B, Hkv, n, D, kb, ks, vb, n + D) for n in (T, N))
+    if kb == 4:
+        main["v_scales"][0, 1, 40, 1] = 0x7C00  # attended to by one row's second head
+        tree["v_scales"][1, :, N - 1, 0] = 0xFE00
+    q, par = _q((B, Hkv * G, N, D), 4), _parents(B, N, N)
+    got, lse = tq.tq_tree_attention(q.cuda(), _roomy(main, cap), cap, rc.to_gpu(tree), kb, ks, vb, parents=_int(par),
+                                    lens=_int(lens), left_pad=_int(pad))
+    torch.cuda.synchronize()
+    rc.check_tree(got, lse, rc.tree_reference(q, main, T, tree, kb, ks, vb, par, lens, pad, dtype=torch.bfloat16))
+
+
 def test_tree_caches_in_pinned_host_memory():
     """Buffers in pinned host memory give the same bits as in device memory."""
     B, Hkv, G, N, T, D = 2, 2, 2, 4, 150, 128
@@ -440,6 +470,19 @@ def test_select_one_long_row():
     g = torch.Generator().manual_seed(2)
     w = (torch.rand((1, 2, 200003), generator=g) ** 8).half().float()
     check_select(w, 200003, 70001, 1000, lens=[200001], left_pad=[3])
+
+
+@pytest.mark.parametrize("T", [8193, 16384, 16385, 40000])
+def test_select_more_rows_than_the_gpu_has_sms(T):
+    g = torch.Generator().manual_seed(T)
+    w = (torch.rand((40, 5, T), generator=g) ** 6).half().float()
+    check_select(w, T, T // 4, 100, lens=[T - 37 * b for b in range(40)], left_pad=[b for b in range(40)])
+
+
+@pytest.mark.parametrize("T", [65536, 140000])
+def test_select_eight_blocks_a_row(T):
+    w = torch.rand((1, 2, T), generator=torch.Generator().manual_seed(T)).half().float()
+    check_select(w, T, T // 3, 77, lens=[T - 5], left_pad=[9])
 
 
 def test_select_many_rows():

@@ -28,7 +28,11 @@ namespace {
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectCopies = 16;    // of the histogram
 constexpr int kSelectKeys = 16384;  // of a slice that shared memory holds; a longer one is read again each pass
-constexpr int kSelectSlice = 8192;  // keys of a block before a row gets more blocks
+// Blocks a row: as many as hold its keys, and while there are fewer blocks than
+// SMs, up to kSelectSlice keys a block (256 rows of 16384 keys: 26 us with one
+// block each, 37 with two; with slices of 4096, 256 rows of 8192 keys take 29
+// us, not 17, and 8 such rows 12.9, not 13.1).
+constexpr int kSelectSlice = 8192;
 
 struct SelectParams {
   const float* w;
@@ -56,17 +60,13 @@ __device__ __forceinline__ void cluster_sync(int cluster) {
     __syncthreads();
   }
 }
-// The word at shared address a of block `rank` of the cluster.
-__device__ __forceinline__ int cluster_read(uint32_t a, int rank, int cluster) {
+// The word at shared address a of block `rank` of the cluster. (Its order is
+// kept by cluster_sync; reads among themselves may move.)
+__device__ __forceinline__ int cluster_read(uint32_t a, int rank) {
   int v;
-  if (cluster > 1) {
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
-                 : "=r"(v)
-                 : "r"(a), "r"(rank)
-                 : "memory");
-  } else {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  }
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
+               : "=r"(v)
+               : "r"(a), "r"(rank));
   return v;
 }
 
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   int* s_hist = select_smem;                       // [256][kSelectCopies]
   uint32_t* s_key = reinterpret_cast<uint32_t*>(select_smem + 256 * kSelectCopies);
   __shared__ int s_bins[2][256];                   // this block's digit counts, by pass parity
+  __shared__ int s_sum[256];                       // the cluster's
   __shared__ int s_digit, s_left;
   __shared__ int s_warp[2][kSelectWarps];          // above and equal keys of each warp's part
   __shared__ int s_total[2];
@@ -137,18 +138,23 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       if ((tid & 1) == 0) s_bins[pass & 1][tid >> 1] = c;
     }
     cluster_sync(p.cluster);
+    const int* counts = s_bins[pass & 1];
+    if (p.cluster > 1) {  // a thread a bin, all blocks' counts on their way at once
+      if (tid < 256) {
+        const uint32_t bin = static_cast<uint32_t>(__cvta_generic_to_shared(counts + tid));
+        int v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = r < p.cluster ? cluster_read(bin, r) : 0;
+        s_sum[tid] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      }
+      __syncthreads();
+      counts = s_sum;
+    }
     if (warp == 0) {
       // lane L takes digits 255 - 8 L .. 248 - 8 L, from the top
-      const uint32_t bins = static_cast<uint32_t>(__cvta_generic_to_shared(&s_bins[pass & 1][0]));
       int c[8], sum = 0;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) c[x] = 0;
-      for (int r = 0; r < p.cluster; ++r) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) c[x] += cluster_read(bins + (255 - 8 * lane - x) * 4, r, p.cluster);
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) sum += c[x];
+      for (int x = 0; x < 8; ++x) sum += c[x] = counts[255 - 8 * lane - x];
       int above = sum;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
@@ -196,10 +202,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   }
   cluster_sync(p.cluster);
   above = equal = 0;
-  const uint32_t totals = static_cast<uint32_t>(__cvta_generic_to_shared(&s_total[0]));
-  for (int r = 0; r < rank; ++r) {
-    above += cluster_read(totals, r, p.cluster);
-    equal += cluster_read(totals + 4, r, p.cluster);
+  if (rank > 0) {
+    const uint32_t totals = static_cast<uint32_t>(__cvta_generic_to_shared(&s_total[0]));
+    int u[7], v[7];
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      u[r] = r < rank ? cluster_read(totals, r) : 0;
+      v[r] = r < rank ? cluster_read(totals + 4, r) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      above += u[r];
+      equal += v[r];
+    }
   }
   for (int x = 0; x < warp; ++x) {
     above += s_warp[0][x];
@@ -356,7 +371,9 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   p.keep = static_cast<int>(keep);
   p.recent = static_cast<int>(recent);
   p.cluster = 1;
-  while (p.cluster < 8 && T > static_cast<int64_t>(p.cluster) * kSelectSlice) p.cluster *= 2;
+  while (p.cluster < 8 && (T > static_cast<int64_t>(p.cluster) * kSelectKeys ||
+                           (T > static_cast<int64_t>(p.cluster) * kSelectSlice && B * H * p.cluster < sm_count())))
+    p.cluster *= 2;
   const int64_t slice = (T + p.cluster - 1) / p.cluster;
   p.held = slice <= kSelectKeys;
   const int smem = (256 * kSelectCopies + (p.held ? static_cast<int>(slice) : 0)) * 4;

@@ -17,7 +17,10 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
   const cudaError_t e = p.out_f32 ? launch_tree_split<D, true>(p, s) : launch_tree_split<D, false>(p, s);
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.N;
-  // many partial results a row (few segments, many blocks): four warps a row
+  // many partial results a row (few segments, many blocks): four warps a row. (All
+  // sides measured, tree of 32 nodes, 4096 tokens, 8 heads: 20 partial results,
+  // one sequence, 18.2 us with four warps, 22.0 with one; 10, two sequences, 22.5
+  // and 21.6, but head_dim 256 39.5 and 41.1; 5, four sequences, 32.7 and 25.9.)
   const long long parts = (p.grid / (static_cast<long long>(p.B) * p.HH) + 1) * p.copies;
   if (parts >= 8) return launch_pdl_block(tree_combine_kernel<D, 4>, static_cast<int>(rows), 128, p, s, 0);
   return launch_pdl_block(tree_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, p, s, 0);
@@ -35,19 +38,26 @@ struct TreePlan {
   int TT, DV;
 };
 
-bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, bool f32, TreePlan* t) {
+// T: at most that many tokens a sequence.
+bool tree_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D, int64_t T, bool f32, TreePlan* t) {
   const long long lim = 0x7fffffffLL;
   t->TT = f32 ? tile_tokens<true>(D) : tile_tokens<false>(D);
   t->DV = static_cast<int>(D == 512 ? TreeShape<512, false>::DV : D);
   t->R = Hq / Hkv * N;
   t->RB = (t->R + kTreeRows - 1) / kTreeRows;
   t->rows = (t->R + t->RB - 1) / t->RB;
-  // (a lane's share is 32 tokens at least; three parts of a weight need the room)
-  t->copies = f32 || t->rows > 64 || t->TT == 32 ? 1 : 2;
-  t->slots = (t->copies * t->rows + 3) / 4 * 4;
   if (t->RB * (D / t->DV) > lim / Hkv) return false;
   t->HH = Hkv * t->RB * (D / t->DV);
   if (B > 0 && t->HH > lim / B) return false;
+  // Two lanes a row where there is room (a lane's share is 32 tokens at least;
+  // three parts of a weight need the columns) and a block has some tiles to gain
+  // it back: a second lane is one more partial result. 16 rows a head, 8 heads, one
+  // sequence of 4096 / 16384 / 32768 / 65536 tokens (3 / 14 / 27 / 54 tiles a
+  // block): 16.3 / 24.7 / 37.2 / 62.4 us with one lane, 17.3 / 25.0 / 35.8 / 57.7
+  // with two.
+  const long long tiles = T / t->TT + 2;
+  t->copies = f32 || t->rows > 64 || t->TT == 32 || B * t->HH < 16LL * sm_count() / tiles ? 1 : 2;
+  t->slots = (t->copies * t->rows + 3) / 4 * 4;
   t->n_recs = sm_count() + B * t->HH;
   t->rec_floats = t->slots * (t->DV + 2);
   t->cut_bytes = ((kCutRows + B + 1) * 4 + 255) / 256 * 256;
@@ -64,8 +74,8 @@ extern "C" int64_t tq_tree_attention_workspace_size(int64_t B, int64_t Hq, int64
   if (B < 0 || Hq < 1 || Hkv < 1 || N < 1 || N > TQ_TREE_MAX_NODES || Hq % Hkv != 0 || !ragged_sizes_ok(B, Hq, 1))
     return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
   if (!ragged_head_dim_ok(D)) return -static_cast<int64_t>(TQ_ERR_HEAD_DIM);
-  TreePlan t;  // (fp32 outputs need less)
-  if (!tree_plan(B, Hq, Hkv, N, D, false, &t)) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
+  TreePlan t;  // (short sequences and fp32 outputs need less)
+  if (!tree_plan(B, Hq, Hkv, N, D, 1LL << 40, false, &t)) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
   return t.bytes;
 }
 
@@ -89,7 +99,7 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   const int64_t need = tq_tree_attention_workspace_size(B, Hq, Hkv, N, D);
   if (need < 0) return static_cast<tq_status>(-need);
   TreePlan t;
-  tree_plan(B, Hq, Hkv, N, D, out_dtype == TQ_F32, &t);
+  tree_plan(B, Hq, Hkv, N, D, T, out_dtype == TQ_F32, &t);
   // tiles in all (and what the turns count for) are counted in 32 bits
   const long long tiles = (T + t.TT - 1) / t.TT + 1 + (N + t.TT - 1) / t.TT;
   if (tiles + 16 > 0x7fffffffLL / (B * t.HH)) return TQ_ERR_INVALID_ARG;

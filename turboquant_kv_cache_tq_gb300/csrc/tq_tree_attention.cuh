@@ -20,7 +20,7 @@
 // result for the combine.
 //
 // Work split: the tiles of all (batch row, kv head, row block, value half) in
-// one line, cut evenly into one range per SM; a range's part of one
+// one line, cut evenly into one range per SM (cut_line); a range's part of one
 // (batch row, ...) is a segment and ends in one partial record (running
 // maximum, weight sum, weighted values). The lengths are read on the device, so
 // the cut is even for ragged batches and one captured launch serves any
@@ -836,6 +836,25 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
   }
 }
 
+// The partial results: one block an SM, which holds all of its tensor memory.
+//
+// What bounds it (32 sequences x 8 heads x 8192 tokens, head_dim 128, 16 nodes,
+// k8 / v8): 168 us in a graph, where the packed bytes take 67 and the products
+// 27; 161 us with 3-bit values. A counter run of 8 such sequences: 0.55
+// instructions a cycle and scheduler, tensor pipe 33%, DRAM 27% busy; warps wait
+// for tensor memory and barriers (4.2 of 12.5 cycles an instruction), for
+// instructions (1.1) and for results (1.4). So it is the decode, five to six
+// instructions an element, at what six roles of 28 warps let the schedulers issue.
+// How it came there: a warp a row, no matrix instructions, 26.2 ms; roles around
+// tcgen05 406 us; packed rows by bulk copies 271; roles bound to schedulers with
+// rolled loops 230; a second softmax group, weights written over their scores 210;
+// one elected lane issuing from uniform control flow 183; turns counted in the cut
+// 168. (Rolled half groups in the decode 218, scores read 32 columns at a time 15%
+// slower.)
+//
+// A small call (8 heads x 4096 tokens, 32 nodes: 18 us with the combine) is one
+// chain: cut 1.3 us, queries into tensor memory 2, first tile 1.5, three more 3,
+// record 2.
 template <int D, bool F32>
 __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kernel(const __grid_constant__ TreeParams p) {
   using S = TreeShape<D, F32>;
@@ -956,7 +975,9 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
 
 // Merges the partial results of each output row, divides, turns the row back
 // (Hadamard butterflies, / sqrt(D), signs) and stores it. W warps share a row.
-// Lane L holds elements [L D/32, (L+1) D/32).
+// Lane L holds elements [L D/32, (L+1) D/32). It reads each record once from L2; a
+// small call spends 3 us here (latency: the cut, the maxima, the values), 11 us when
+// the places were 64-bit divisions. Seven blocks an SM (head_dim 256: 41 -> 39 us).
 template <int D, int W>
 __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) tree_combine_kernel(const __grid_constant__ TreeParams p) {
   using S = TreeShape<D, false>;  // (what is read here is the same for both)
