@@ -307,7 +307,7 @@ __device__ void weights_sum(const WeightsParams& p, uint32_t sm, uint8_t* smem, 
           const int at = i * 32 + lane, x = at / PER, k = at - x * PER;
           const long long r = __shfl_sync(kFull, from, x);
           if (at < pieces) {
-            const uint4 v = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + r * D) + k) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 v = r >= 0 ? reinterpret_cast<const uint4*>(p.q + r * D)[k] : make_uint4(0u, 0u, 0u, 0u);
             sts128(sm + S::Q_OFF + (k >> 3) * (S::NB * 128) + (c0 + 8 * x) * 128 + (((k ^ c0) & 7) << 4), v.x, v.y, v.z,
                    v.w);
           }

@@ -567,9 +567,10 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     int up[2] = {-1, -1};  // parents of nodes lane, lane + 32
     if (climb && p.parents != nullptr) {
       const int* from = p.parents + static_cast<long long>(w.b) * p.N;
-      if (lane < p.N) up[0] = __ldg(from + lane);
-      if (lane + 32 < p.N) up[1] = __ldg(from + lane + 32);
+      if (lane < p.N) up[0] = from[lane];
+      if (lane + 32 < p.N) up[1] = from[lane + 32];
     }
+    // (plain loads: the kernel may have started before its inputs were written)
     // ---- the queries of the segment (every score of the last one is done), each
     // group its share of the columns. Eight rows of 64 bytes a load, turned in
     // shared memory (a lane for each row would touch 32 lines a load).
@@ -594,7 +595,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
         for (int k = 0; k < STEP / 16; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            u[k][i] = from[i] >= 0 ? __ldg(src + static_cast<long long>(from[i]) * (D / 8) + c / 4 + 4 * k + (lane & 3))
+            u[k][i] = from[i] >= 0 ? src[static_cast<long long>(from[i]) * (D / 8) + c / 4 + 4 * k + (lane & 3)]
                                    : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int k = 0; k < STEP / 16; ++k) {
@@ -617,7 +618,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 #pragma unroll 8
         for (int x = 0; x < 32; ++x) {
           const int r2 = row_at(x);
-          const uint4 u = r2 >= 0 ? __ldg(src + static_cast<long long>(r2) * (D / 8) + S::QT / 8 + lane)
+          const uint4 u = r2 >= 0 ? src[static_cast<long long>(r2) * (D / 8) + S::QT / 8 + lane]
                                   : make_uint4(0u, 0u, 0u, 0u);
           sts128(sm + S::Q_OFF + (lane >> 3) * (128 * 128) + (warp * 32 + x) * 128 + (((lane ^ x) & 7) << 4), u.x, u.y,
                  u.z, u.w);
