@@ -214,7 +214,8 @@ __device__ void weights_load(const WeightsParams& p, uint32_t sm, uint8_t* ctl, 
     // the last copies land before the block ends, whatever became of its other warps
     if (!p.bulk) asm volatile("cp.async.wait_all;" ::: "memory");
     else
-      for (int k = max(it - S::NR, 0); k < it; ++k) mbar_wait(bars + wcLoaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
+      for (int k = max(it - S::NR, 0); k < it; ++k)
+        mbar_wait(bars + wcLoaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
   }
   __syncwarp();
 }

@@ -129,7 +129,8 @@ constexpr int kTreeRows = 128;
 
 // Control words in shared memory (byte offsets).
 enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcPFull = 96, kcPFree = 128,
-             kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcStart = 192, kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
+             kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcStart = 192,
+             kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
              kcBad = 352, kcMerge = 480, kcMerged = 488, kcMaxSum = 512 };
 
 // Tiles of a batch row: the sequence's and the tree's.
@@ -262,7 +263,8 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
     // the last copies land before the block ends, whatever became of its other warps
     if (!ALONE) asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ROWWISE)
-      for (int k = max(it - S::NR, 0); k < it; ++k) mbar_wait(bars + loaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
+      for (int k = max(it - S::NR, 0); k < it; ++k)
+        mbar_wait(bars + loaded + 8 * (k % S::NR), (k / S::NR) & 1, kBulkWaitLimit);
   }
   __syncwarp();
 }
@@ -287,7 +289,7 @@ __device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl,
     const int it = part / S::SUBS, st = part % S::KS, rs = it % S::NR;
     if (!warp_wait(bars + kcKLoaded + 8 * rs, (it / S::NR) & 1, quit, p.err)) return;
     if (part >= S::KS && !warp_wait(bars + kcKEmpty + 8 * st, (part / S::KS - 1) & 1, quit, p.err)) return;
-#pragma unroll 1
+#pragma unroll (S::SUBS == 1 ? 2 : 1)
     for (int i = 0; i < S::KP; ++i) {
       const uint32_t at = scales + rs * S::KR_BYTES + i * (u.STEP * S::NGK * 2);
       decode_key_group<KMODE>(u, codes + rs * S::KR_BYTES + i * (u.STEP * X), at, at + S::KR_ZP - S::KR_SC,
@@ -365,7 +367,8 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
           } else if constexpr (VT::PAIRS) {
             cc = table64(field_addr<2 * VB, 7>(w, 2 * j * VB, 0u) + tab);
           } else if constexpr (VB == 8) {
-            cc = make_float2(table32(byte_field_addr(w, 2 * j, vstride, tab)), table32(byte_field_addr(w, 2 * j + 1, vstride, tab)));
+            cc = make_float2(table32(byte_field_addr(w, 2 * j, vstride, tab)),
+                             table32(byte_field_addr(w, 2 * j + 1, vstride, tab)));
           } else {
             cc = make_float2(table32(field_addr<VB, 7>(w, 2 * j * VB, 0u) + tab),
                              table32(field_addr<VB, 7>(w, (2 * j + 1) * VB, 0u) + tab));
@@ -428,7 +431,8 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
           if (sub == 0) mma_ts(tm + S::S_COL + sb * S::BUF, tm + S::Q_COL + 8 * ks, b, kind, ks > 0, issue);
           else
             mma_ss(tm + S::S_COL + sb * S::BUF,
-                   smem_operand(sm + S::Q_OFF, 16, 1024) + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16, b, kind, true, issue);
+                   smem_operand(sm + S::Q_OFF, 16, 1024) + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16, b, kind,
+                   true, issue);
         }
         mma_commit(bars + kcKEmpty + 8 * st, issue);
       }
