@@ -73,10 +73,13 @@ struct TreeShape {
   // halves, each the size of a stage).
   static constexpr int SUBS = D == 512 ? 2 : 1, DS = D / SUBS, NGS = NGK / SUBS;
   static constexpr int K_BYTES = TT * DS * 2, V_BYTES = TT * DV * 2;
-  static constexpr int KS = 2, VS = 2;  // decoded stages
-  // A group of four decoding warps owns a stage and takes every other part (a
-  // barrier's parity tells neighbouring phases apart only, so a warp has to see
-  // every phase of the barriers that it waits on).
+  // Decoded stages. A value stage is taken until its product ends, so two hold
+  // the decoding up: with four, 32 x 8192 tokens take 161 us, not 169 (head_dim 256: 39.6,
+  // not 38.8; 512 has no room).
+  static constexpr int KS = 2, VS = D <= 128 ? 4 : 2;
+  // A group of four decoding warps owns every other stage and takes every other
+  // part (a barrier's parity tells neighbouring phases apart only, so a warp has to
+  // see every phase of the barriers that it waits on).
   static constexpr int KWARPS = 4, VWARPS = 4;
   static constexpr int KP = TT * NGS / (32 * KWARPS), VP = TT * NGV / (32 * VWARPS);  // groups a thread takes of a part
   // Queries: the first QT elements of a row in tensor memory, the rest (head_dim
@@ -96,9 +99,9 @@ struct TreeShape {
   static constexpr int VR_OFF = KR_OFF + NR * KR_BYTES;
   static constexpr int T_OFF = VR_OFF + NR * VR_BYTES;
   static constexpr int C_OFF = T_OFF + TAB;
-  // a softmax warp's own: 32 rows of 64 bytes (80 apart) of the queries or of a
+  // control words; a softmax warp's own: 32 rows of 64 bytes (80 apart) of the queries or of a
   // record, and the walk up the tree
-  static constexpr int W_OFF = C_OFF + 512 + (SW > 1 ? 2048 : 0), W_BYTES = 32 * 80;
+  static constexpr int W_OFF = C_OFF + 656 + (SW > 1 ? 2048 : 0), W_BYTES = 32 * 80;
   static constexpr int SMEM = W_OFF + 4 * SW * W_BYTES;
   // Tensor memory columns: SW outputs | NS score tiles of BUF columns | queries.
   // The weights of 16 tokens take the place of their scores: eight columns of
@@ -115,7 +118,7 @@ struct TreeShape {
   static constexpr int THREADS = 640 + 128 * SW;
   static_assert(Q_COL + QT / 2 <= 512, "tensor memory");
   static_assert(QT == DS, "the first part's queries are the ones in tensor memory");
-  static_assert(SMEM <= 232448, "shared memory");
+  static_assert(SMEM <= 232448 && W_OFF % 16 == 0, "shared memory");
 };
 
 // Warps 0-3 (and 24-27 where SW is 2) softmax (tensor memory ties each to a
@@ -128,10 +131,14 @@ struct TreeShape {
 constexpr int kTreeRows = 128;
 
 // Control words in shared memory (byte offsets).
-enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 48, kcSFull = 64, kcPFull = 96, kcPFree = 128,
-             kcQFull = 160, kcDrain = 168, kcTmem = 184, kcQuit = 188, kcStart = 192,
-             kcKLoaded = 208, kcKTaken = 240, kcVLoaded = 272, kcVTaken = 304, kcAnyBad = 336,
-             kcBad = 352, kcMerge = 480, kcMerged = 488, kcMaxSum = 512 };
+enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 64, kcSFull = 96, kcPFull = 128, kcPFree = 160,
+             kcQFull = 192, kcDrain = 200, kcTmem = 216, kcQuit = 220, kcAnyBad = 224, kcMerge = 232, kcMerged = 240,
+             kcStart = 256, kcKLoaded = 272, kcKTaken = 304, kcVLoaded = 336, kcVTaken = 368, kcBad = 400,
+             kcMaxSum = 656 };
+// Marks of bad values are kept for eight tiles: a tile's are read before the
+// weights of the second tile after it are given out, and the values of the eighth
+// are decoded after the fourth's were multiplied.
+constexpr int kTreeMarks = 8;
 
 // Tiles of a batch row: the sequence's and the tree's.
 template <int TT>
@@ -385,7 +392,7 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
       marks.x = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
       marks.y = __reduce_or_sync(kFull, static_cast<unsigned>(bad >> 32));
     }
-    if (lane == 0) *reinterpret_cast<uint2*>(ctl + kcBad + (it & 3) * 32 + wv * 8) = marks;
+    if (lane == 0) *reinterpret_cast<uint2*>(ctl + kcBad + (it % kTreeMarks) * 32 + wv * 8) = marks;
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
@@ -659,7 +666,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
       unsigned long long bad = 0;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
-        const uint2 u = lds64(bars + kcBad + (it & 3) * 32 + 8 * i);
+        const uint2 u = lds64(bars + kcBad + (it % kTreeMarks) * 32 + 8 * i);
         bad |= static_cast<unsigned long long>(u.y) << 32 | u.x;
       }
       if (bad & attended(tile)) l = __int_as_float(0x7fc00000);
@@ -880,9 +887,11 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + kcKFull + 8 * i, S::KWARPS);
       mbar_init(bars + kcKEmpty + 8 * i, 1);
+      mbar_init(bars + kcDrain + 8 * i, 1);
+    }
+    for (int i = 0; i < S::VS; ++i) {
       mbar_init(bars + kcVFull + 8 * i, S::VWARPS);
       mbar_init(bars + kcVEmpty + 8 * i, 1);
-      mbar_init(bars + kcDrain + 8 * i, 1);
     }
     mbar_init(bars + kcQFull, 4 * S::SW);
     mbar_init(bars + kcMerge, 4 * S::SW);
