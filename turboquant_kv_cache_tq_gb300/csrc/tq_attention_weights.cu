@@ -17,9 +17,11 @@
 // per SM (cut_line); rows beyond a block's columns take further rounds over its
 // range.
 //
-// What bounds it: with few observers the keys' decode (32 x 8 heads x 8192 tokens, 24
-// columns, head_dim 128: 74 us, where the bytes take 37; a warp a token without
-// matrix instructions took 2354); in a small call (8 x 4096 tokens, 256 columns:
+// What bounds it: with few observers (32 x 8 heads x 8192 tokens, 24 columns, head_dim
+// 128: 74 us, where the bytes take 37; a warp a token without matrix instructions
+// took 2354) the hand-overs of a tile from copy to decode, product and sum, 1300
+// cycles each: sixteen decoding warps instead of eight are no faster (80 us), nor
+// are sums fetched a tile ahead (74). In a small call (8 x 4096 tokens, 256 columns:
 // 12.4 us) the chain of cut, queries and two tiles. There the queries were the
 // longest link: 19.4 us when one of the summing groups fetched them, with two
 // divisions a piece.

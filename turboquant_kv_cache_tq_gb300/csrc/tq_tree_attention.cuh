@@ -851,18 +851,20 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 // The partial results: one block an SM, which holds all of its tensor memory.
 //
 // What bounds it (32 sequences x 8 heads x 8192 tokens, head_dim 128, 16 nodes,
-// k8 / v8): 168 us in a graph, where the packed bytes take 67 and the products
-// 27; 161 us with 3-bit values. A counter run of 8 such sequences: 0.55
+// k8 / v8): 161 us in a graph, where the packed bytes take 67 and the products
+// 27; 155 us with 3-bit values. A counter run of 8 such sequences: 0.55
 // instructions a cycle and scheduler, tensor pipe 33%, DRAM 27% busy; warps wait
 // for tensor memory and barriers (4.2 of 12.5 cycles an instruction), for
-// instructions (1.1) and for results (1.4). So it is the decode, five to six
-// instructions an element, at what six roles of 28 warps let the schedulers issue.
+// instructions (1.1) and for results (1.4). A tile takes 1700 cycles; in two tiles'
+// time a value warp decodes for 2500, a key warp for 1100, a softmax warp works for
+// 2000. So it is the values' decode and the hand-overs around it, at what six
+// roles of 28 warps let the schedulers issue.
 // How it came there: a warp a row, no matrix instructions, 26.2 ms; roles around
 // tcgen05 406 us; packed rows by bulk copies 271; roles bound to schedulers with
 // rolled loops 230; a second softmax group, weights written over their scores 210;
 // one elected lane issuing from uniform control flow 183; turns counted in the cut
-// 168. (Rolled half groups in the decode 218, scores read 32 columns at a time 15%
-// slower.)
+// 168; four value stages 161. (Rolled half groups in the decode 218, scores read 32
+// columns at a time 15% slower.)
 //
 // A small call (8 heads x 4096 tokens, 32 nodes: 18 us with the combine) is one
 // chain: cut 1.3 us, queries into tensor memory 2, first tile 1.5, three more 3,
