@@ -254,6 +254,10 @@ __device__ void weights_matrix(const WeightsParams& p, uint32_t sm, uint8_t* ctl
       }
     }
   }
+  // the last tiles' arrivals, which no decoding warp waits for: they land before
+  // the block gives its shared memory back
+  for (int k = max(it - S::KS, 0); k < it; ++k)
+    if (!warp_wait(bars + wcKEmpty + 8 * (k % S::KS), (k / S::KS) & 1, quit, p.err)) return;
 }
 
 // The summing warps (group `which` of two takes every other tile): a thread

@@ -446,6 +446,11 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
       mma_commit(bars + kcSFull + 8 * sb, issue);
     }
   }
+  // the last parts' arrivals, which no decoding warp waits for: they land before
+  // the block gives its shared memory back
+  const int parts = it * S::SUBS;
+  for (int k = max(parts - S::KS, 0); k < parts; ++k)
+    if (!warp_wait(bars + kcKEmpty + 8 * (k % S::KS), (k / S::KS) & 1, quit, p.err)) return;
 }
 
 // The weighted values' warp: O += P V, the weights as a high part, a remainder
@@ -483,6 +488,8 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
       mma_commit(bars + kcVEmpty + 8 * st, issue);
     }
   }
+  for (int k = max(it - S::VS, 0); k < it; ++k)  // (as in tree_scores)
+    if (!warp_wait(bars + kcVEmpty + 8 * (k % S::VS), (k / S::VS) & 1, quit, p.err)) return;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
