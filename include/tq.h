@@ -313,9 +313,11 @@ TQ_API int64_t tq_lloyd_max_fit_workspace_size(int levels);
  * device arrays [B] read while the call runs, so one captured graph serves
  * every step. Values outside [0, T] count as the nearer end of that range;
  * lens == NULL stands for T everywhere, left_pad == NULL for 0. T, known to the
- * host, bounds lens. An array that a call writes shares no memory with another
- * one that it reads or writes, unless its text says so; overlaps that the host
- * can see among the large ones are refused (TQ_ERR_INVALID_ARG).
+ * host, bounds lens; it is at most 2^31 - 2^13, whatever the capacity. Nothing
+ * may change the device arrays while a call that reads them runs. An array that a
+ * call writes shares no memory with another one that it reads or writes, unless
+ * its text says so; overlaps that the host can see among the large ones are
+ * refused (TQ_ERR_INVALID_ARG).
  *
  * One decode step with drafted tokens: encode the draft's keys and values into
  * a small cache of their own (tq_encode_kv, tokens [0, N)); attend with
@@ -423,7 +425,8 @@ TQ_API tq_status tq_attention_weights(const void* q, const float* lse, int64_t B
  *   index    int32 [B, H, keep]: the kept tokens in ascending order, then -1.
  *   count    int32 [B]: min(keep, lens[b] - left_pad[b]), the kept tokens of
  *            every head of row b; not lens or left_pad itself.
- * Limits: 0 <= recent <= keep, B * H < 2^31. keep == 0 writes count alone. */
+ * Limits: 0 <= recent <= keep <= 2^31 - 2^13, 8 B H < 2^31. keep == 0 writes
+ * count alone. */
 TQ_API tq_status tq_evict_select(const float* weights, int64_t B, int64_t H, int64_t T, int64_t w_cap,
                                  const int32_t* lens, const int32_t* left_pad, int64_t keep, int64_t recent,
                                  int32_t* index, int32_t* count, void* stream);

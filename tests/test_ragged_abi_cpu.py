@@ -125,6 +125,17 @@ def test_gather_refusals(tq):
     assert tq.lib().tq_cache_gather(None, None, 1, 2, 128, 8, 3, P, 4, 0, None, None, None, None, None, None) == INVALID
 
 
+def test_token_counts_that_32_bits_do_not_hold_are_refused(tq):
+    """Up to 2^31 - 2^13 tokens a sequence and kept tokens a row: past that the
+    kernels' steps would leave 32 bits."""
+    far = [P + (i << 40) for i in range(8)]
+    for n in ((1 << 31) - (1 << 13) + 1, (1 << 31) - 128, (1 << 31) - 1):
+        assert _select(tq, w=far[0], index=far[1], count=far[2], B=1, H=1, keep=n, recent=n) == INVALID, n
+        assert _select(tq, w=far[0], index=far[1], count=far[2], B=1, H=1, T=n, w_cap=n) == INVALID, n
+        assert _tree(tq, q=far[0], out=far[1], lse=far[2], ws=far[3], Hq=1, Hkv=1, T=n, cache=_cache(tq, n)) == INVALID, n
+        assert _weights(tq, q=far[0], lse=far[1], w_out=far[2], Hq=1, Hkv=1, T=n, cap=n, w_cap=n) == INVALID, n
+
+
 def test_overlaps_are_refused(tq):
     """Arrays that share memory, where the call does not allow it."""
     far = [P + (i << 30) for i in range(16)]

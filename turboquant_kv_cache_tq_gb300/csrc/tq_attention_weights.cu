@@ -489,7 +489,8 @@ extern "C" tq_status tq_attention_weights(const void* q, const float* lse, int64
                                           const int32_t* n_path, int64_t P, float scale, const float* weights_in,
                                           float* weights_out, int64_t w_cap, void* stream) {
   const int64_t lim = 0x7fffffffLL;
-  if (B < 0 || Hq < 1 || Hkv < 1 || N < 1 || T < 0 || P < 0 || w_cap < T || t_cap < T) return TQ_ERR_INVALID_ARG;
+  if (B < 0 || Hq < 1 || Hkv < 1 || N < 1 || T < 0 || T > kRaggedMostTokens || P < 0 || w_cap < T || t_cap < T)
+    return TQ_ERR_INVALID_ARG;
   if (!ragged_head_dim_ok(D)) return TQ_ERR_HEAD_DIM;
   const int kmode = ragged_key_mode(k_bits, k_signed);
   if (kmode < 0) return TQ_ERR_BITS;

@@ -341,7 +341,8 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
                                      const int32_t* lens, const int32_t* left_pad, int64_t keep, int64_t recent,
                                      int32_t* index, int32_t* count, void* stream) {
   const int64_t lim = 0x7fffffffLL;
-  if (B < 0 || H < 0 || T < 0 || w_cap < T || keep < 0 || recent < 0 || recent > keep || keep > lim)
+  if (B < 0 || H < 0 || T < 0 || w_cap < T || keep < 0 || recent < 0 || recent > keep || keep > kRaggedMostTokens ||
+      T > kRaggedMostTokens)
     return TQ_ERR_INVALID_ARG;
   if (!ragged_sizes_ok(B, H, w_cap) || !ragged_sizes_ok(B, H, keep) || !ragged_sizes_ok(B, H, 8) ||
       (B > 0 && H > (lim >> 3) / B))  // (at most 8 blocks a row)

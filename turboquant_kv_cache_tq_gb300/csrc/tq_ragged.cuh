@@ -80,6 +80,10 @@ inline int ragged_key_mode(int bits, int is_signed) {
   if (is_signed) return bits == 8 ? kK8Signed : -1;
   return bits == 2 ? kK2 : bits == 4 ? kK4 : bits == 5 ? kK5 : bits == 8 ? kK8 : -1;
 }
+// The most tokens of a sequence, and kept tokens of a row: the kernels count
+// tokens in 32 bits and step past the last one by up to a tile (128) or the
+// threads of a cluster (4096).
+constexpr int64_t kRaggedMostTokens = (1LL << 31) - (1LL << 13);
 // Whether B * H rows of t_cap tokens can be addressed: byte offsets of any
 // buffer (at most 512 bytes a token) stay far inside 63 bits.
 inline bool ragged_sizes_ok(int64_t B, int64_t H, int64_t t_cap) {

@@ -91,7 +91,7 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
   const int kmode = ragged_key_mode(k_bits, k_signed);
   if (kmode < 0 || !ragged_value_bits_ok(v_bits)) return TQ_ERR_BITS;
   if (out_dtype != TQ_F32 && out_dtype != TQ_BF16) return TQ_ERR_DTYPE;
-  if (Hq % Hkv != 0 || cache->t_cap < T || tree->t_cap < N) return TQ_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0 || T > kRaggedMostTokens || cache->t_cap < T || tree->t_cap < N) return TQ_ERR_INVALID_ARG;
   if (!ragged_sizes_ok(B, Hkv, cache->t_cap) || !ragged_sizes_ok(B, Hkv, tree->t_cap) || !ragged_sizes_ok(B, Hq, N))
     return TQ_ERR_INVALID_ARG;
   if (B * Hq > 0x7ffffff0LL / N) return TQ_ERR_INVALID_ARG;
