@@ -188,6 +188,19 @@ def test_binding_refuses_wrong_tensors(tq):
         tq.tq_cache_gather(cache, cache, torch.zeros((1, 4), dtype=torch.int32))
 
 
+def test_cutting_into_less_room_than_the_budget_is_refused(tq):
+    """A fresh cache too small for the kept tokens would lose the last of them,
+    the recent ones."""
+    cache = tq.alloc_cache(1, 2, 16, 64, 8, 3, device="cpu")
+    w = torch.zeros((1, 2, 16))
+    for keep, T, t_cap in ((8, 16, 7), (8, 16, 0), (12, 10, 9)):
+        with pytest.raises(ValueError, match="t_cap"):
+            tq.evict_rows(cache, w, T, keep, 2, t_cap=t_cap)
+    for keep, T, t_cap in ((8, 16, 8), (12, 10, 10), (8, 16, None)):  # refused for the device alone
+        with pytest.raises(ValueError, match="CUDA device"):
+            tq.evict_rows(cache, w, T, keep, 2, t_cap=t_cap)
+
+
 def test_reference_of_one_token_by_hand():
     """The reference itself: one key alone gives its own value row back, and
     lse is the score."""

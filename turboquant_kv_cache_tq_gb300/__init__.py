@@ -619,10 +619,13 @@ def evict_rows(cache: dict, weights: torch.Tensor, T: int, keep: int, recent: in
                t_cap=None, stream=None):
     """Cuts every (batch row, head) to at most `keep` tokens by their attention
     weights -> (a fresh cache whose rows start at token 0, its weights, its
-    lengths)."""
+    lengths). t_cap: the fresh cache's capacity (keep when None), room for every
+    token that may stay."""
     B, H, cap = cache["k_codes"].shape[:3]
     if weights.shape[-1] != cap:
         raise ValueError("weights must be [B,H,%d], the cache's capacity" % cap)
+    if t_cap is not None and t_cap < min(keep, T):
+        raise ValueError("t_cap must be at least %d, the tokens that may stay" % min(keep, T))
     if _elsewhere(weights.device, stream):
         with _switched(weights.device, stream):
             return evict_rows(cache, weights, T, keep, recent, lens, left_pad, t_cap)
