@@ -188,6 +188,11 @@ def test_binding_refuses_wrong_tensors(tq):
         tq.tq_cache_gather(cache, cache, torch.zeros((1, 4), dtype=torch.int32))
 
 
+def test_a_cache_without_room_has_no_weights(tq):
+    assert _gather(tq, sw=P, dw=None, dst=_cache(tq, 0), n=0, length=None) == OK
+    assert _gather(tq, sw=P, dw=None, dst=_cache(tq, 1), n=0, length=None) == INVALID
+
+
 def test_cutting_into_less_room_than_the_budget_is_refused(tq):
     """A fresh cache too small for the kept tokens would lose the last of them,
     the recent ones."""

@@ -348,7 +348,7 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
       (B > 0 && H > (lim >> 3) / B))  // (at most 8 blocks a row)
     return TQ_ERR_INVALID_ARG;
   if (B == 0 || H == 0) return TQ_OK;
-  if (!weights || !count || (!index && keep > 0)) return TQ_ERR_INVALID_ARG;
+  if ((!weights && w_cap > 0) || !count || (!index && keep > 0)) return TQ_ERR_INVALID_ARG;
   for (const void* x : {static_cast<const void*>(weights), static_cast<const void*>(lens),
                         static_cast<const void*>(left_pad), static_cast<const void*>(index),
                         static_cast<const void*>(count)})
@@ -404,7 +404,8 @@ extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed
   if (ragged_key_mode(k_bits, 0) < 0 || !ragged_value_bits_ok(v_bits)) return TQ_ERR_BITS;
   if (!ragged_sizes_ok(B, H, src->t_cap) || !ragged_sizes_ok(B, H, dst->t_cap) || !ragged_sizes_ok(B, H, n))
     return TQ_ERR_INVALID_ARG;
-  if (src_weights != nullptr && dst_weights == nullptr) return TQ_ERR_INVALID_ARG;
+  // (a cache without room has no weights)
+  if (src_weights != nullptr && dst_weights == nullptr && dst->t_cap > 0) return TQ_ERR_INVALID_ARG;
   if (B == 0 || H == 0) return TQ_OK;
   for (const void* x : {static_cast<const void*>(index), static_cast<const void*>(count),
                         static_cast<const void*>(dst_off), static_cast<const void*>(dst_len),
