@@ -316,8 +316,7 @@ TQ_API int64_t tq_lloyd_max_fit_workspace_size(int levels);
  * host, bounds lens; it is at most 2^31 - 2^13, whatever the capacity. Nothing
  * may change the device arrays while a call that reads them runs. An array that a
  * call writes shares no memory with another one that it reads or writes, unless
- * its text says so; overlaps that the host can see among the large ones are
- * refused (TQ_ERR_INVALID_ARG).
+ * its text says so: such calls are refused (TQ_ERR_INVALID_ARG).
  *
  * One decode step with drafted tokens: encode the draft's keys and values into
  * a small cache of their own (tq_encode_kv, tokens [0, N)); attend with

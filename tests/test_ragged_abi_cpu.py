@@ -157,6 +157,55 @@ def test_overlaps_are_refused(tq):
         assert _gather(tq, **dict(apart, **kw)) == INVALID, kw
 
 
+def test_every_written_array_is_held_apart(tq):
+    """Each array that a call writes against each other one, by one element at
+    either end."""
+    far = [(i + 1) << 30 for i in range(24)]
+    # (argument, bytes) of B = 1, Hq = 4, Hkv = 2, N = 8, T = capacity = 64, D = 128, k8 v3; the tree's capacity is 8
+    names = rc.CACHE_KEYS
+    X = (128, 8, 8, 48, 8)
+    main = {n: far[i] for i, n in enumerate(names)}
+    tree = {n: far[5 + i] for i, n in enumerate(names)}
+    need = tq.lib().tq_tree_attention_workspace_size(1, 4, 2, 8, 128)
+    base = dict(q=far[10], out=far[11], lse=far[12], ws=far[13], parents=far[14], lens=far[15], pad=far[16])
+    size = dict(q=4 * 8 * 128 * 2, out=4 * 8 * 128 * 2, lse=4 * 8 * 4, ws=need, parents=8 * 4, lens=4, pad=4)
+    reads = [(base[n], size[n]) for n in ("q", "parents", "lens", "pad")]
+    reads += [(main[n], 2 * 64 * x) for n, x in zip(names, X)] + [(tree[n], 2 * 8 * x) for n, x in zip(names, X)]
+    step = dict(out=16, lse=4, ws=16)
+
+    def ends(at, length, own, step):
+        """Places for an array of `own` bytes that share its last or first element with [at, at + length)."""
+        return [(at + length - 1) // step * step, -(-(at - own + 1) // step) * step]
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return _tree(tq, cache=_cache(tq, 64, **main), tree=_cache(tq, 8, **tree), **a)
+
+    for name in ("out", "lse", "ws"):
+        for at, length in reads + [(base[n], size[n]) for n in ("out", "lse", "ws") if n != name]:
+            for place in ends(at, length, size[name], step[name]):
+                assert call(**{name: place}) == INVALID, (name, hex(at), hex(place))
+    keys = dict(kc=far[0], ks_=far[1], kz=far[2])
+    base_w = dict(keys, q=far[10], lse=far[12], lens=far[15], pad=far[16], path=far[17], n_path=far[18], w_in=far[19])
+    sums = 2 * 64 * 4
+    for at, length in ((far[0], 2 * 64 * 128), (far[1], 2 * 64 * 8), (far[2], 2 * 64 * 8), (far[10], 4 * 8 * 128 * 2),
+                       (far[12], 4 * 8 * 4), (far[15], 4), (far[16], 4), (far[17], 8 * 4), (far[18], 4), (far[19], sums)):
+        for place in ends(at, length, sums, 4):
+            if place != far[19]:
+                assert _weights(tq, w_out=place, **base_w) == INVALID, (hex(at), hex(place))
+    dst = dict(tree)
+    base_g = dict(index=far[14], length=far[15], sw=far[16], dw=far[17], count=far[18], off=far[19])
+    for name, own in [(n, 2 * 64 * x) for n, x in zip(names, X)] + [("dw", 2 * 64 * 4), ("length", 4)]:
+        others = [(main[n], 2 * 64 * x) for n, x in zip(names, X)]
+        others += [(dst[n], 2 * 64 * x) for n, x in zip(names, X) if n != name]
+        others += [(far[14], 4 * 4), (far[16], 2 * 64 * 4), (far[18], 4), (far[19], 4)]
+        others += [(base_g[n], b) for n, b in (("dw", 2 * 64 * 4), ("length", 4)) if n != name]
+        for at, length in others:
+            for place in ends(at, length, own, 16 if name in dst else 4):
+                d, g = (dict(dst, **{name: place}), base_g) if name in dst else (dst, dict(base_g, **{name: place}))
+                assert _gather(tq, src=_cache(tq, 64, **main), dst=_cache(tq, 64, **d), **g) == INVALID, (name, hex(at))
+
+
 def test_binding_refuses_wrong_tensors(tq):
     """Shapes, types and devices are checked before the library is called."""
     G = 4

@@ -513,8 +513,17 @@ extern "C" tq_status tq_attention_weights(const void* q, const float* lse, int64
                         static_cast<const void*>(weights_out)})
     if (!ragged_aligned4(x)) return TQ_ERR_ALIGNMENT;
   const long long sums = B * Hkv * w_cap * 4;
-  if ((weights_in != weights_out && ragged_overlap(weights_in, sums, weights_out, sums)) ||
-      ragged_overlap(lse, B * Hq * N * 4, weights_out, sums))
+  const long long tokens = B * Hkv * t_cap;
+  if (ragged_shared({{weights_out, sums}}, {{weights_in == weights_out ? nullptr : weights_in, sums},
+                                            {q, B * Hq * N * D * 2},
+                                            {lse, B * Hq * N * 4},
+                                            {k_codes, tokens * (D * k_bits / 8)},
+                                            {k_scales, tokens * (D / 16)},
+                                            {k_zeros, tokens * (D / 16)},
+                                            {lens, B * 4},
+                                            {left_pad, B * 4},
+                                            {path, B * P * 4},
+                                            {n_path, B * 4}}))
     return TQ_ERR_INVALID_ARG;
   WeightsParams p{};
   p.q = static_cast<const uint16_t*>(q);

@@ -353,12 +353,9 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
                         static_cast<const void*>(left_pad), static_cast<const void*>(index),
                         static_cast<const void*>(count)})
     if (!ragged_aligned4(x)) return TQ_ERR_ALIGNMENT;
-  const long long kept = B * H * keep * 4;
-  if (ragged_overlap(index, kept, count, B * 4) || ragged_overlap(index, kept, weights, B * H * w_cap * 4) ||
-      ragged_overlap(count, B * 4, weights, B * H * w_cap * 4))
+  if (ragged_shared({{index, B * H * keep * 4}, {count, B * 4}},
+                    {{weights, B * H * w_cap * 4}, {lens, B * 4}, {left_pad, B * 4}}))
     return TQ_ERR_INVALID_ARG;
-  for (const int32_t* x : {lens, left_pad})
-    if (ragged_overlap(x, B * 4, index, kept) || ragged_overlap(x, B * 4, count, B * 4)) return TQ_ERR_INVALID_ARG;
   SelectParams p{};
   p.w = weights;
   p.lens = lens;
@@ -424,13 +421,24 @@ extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed
     p.dst[k] = static_cast<uint8_t*>(d[k]);
     p.X[k] = X[k];
   }
-  for (int k = 0; k < 5; ++k)
-    for (int j = 0; j < 5; ++j)
-      if (n > 0 && ragged_overlap(s[k], B * H * src->t_cap * X[k], d[j], B * H * dst->t_cap * X[j]))
-        return TQ_ERR_INVALID_ARG;
-  if (ragged_overlap(src_weights, B * H * src->t_cap * 4, dst_weights, B * H * dst->t_cap * 4) ||
-      ragged_overlap(dst_len, B * 4, dst_off, B * 4) || ragged_overlap(dst_len, B * 4, count, B * 4) ||
-      ragged_overlap(dst_len, B * 4, index, B * (index_heads ? H : 1) * n * 4))
+  // (without tokens to copy dst_len alone is written)
+  const long long st_rows = n > 0 ? B * H * src->t_cap : 0, dt_rows = n > 0 ? B * H * dst->t_cap : 0;
+  if (ragged_shared({{d[0], dt_rows * X[0]},
+                     {d[1], dt_rows * X[1]},
+                     {d[2], dt_rows * X[2]},
+                     {d[3], dt_rows * X[3]},
+                     {d[4], dt_rows * X[4]},
+                     {dst_weights, dt_rows * 4},
+                     {dst_len, B * 4}},
+                    {{s[0], st_rows * X[0]},
+                     {s[1], st_rows * X[1]},
+                     {s[2], st_rows * X[2]},
+                     {s[3], st_rows * X[3]},
+                     {s[4], st_rows * X[4]},
+                     {src_weights, st_rows * 4},
+                     {index, B * (index_heads ? H : 1) * n * 4},
+                     {count, B * 4},
+                     {dst_off, B * 4}}))
     return TQ_ERR_INVALID_ARG;
   auto width = [](int bytes) { return bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4; };
   const int wk = width(X[0]), wv = width(X[3]), ws = width(X[1]);  // key and value codes: 16, or 8 at head_dim 64

@@ -72,6 +72,21 @@ inline bool ragged_overlap(const void* a, long long a_bytes, const void* b, long
   return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) &&
          y < x + static_cast<uintptr_t>(a_bytes);
 }
+// Whether an array that a call writes shares memory with another one that it
+// writes or reads.
+struct Span {
+  const void* at;
+  long long bytes;
+};
+inline bool ragged_shared(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* x = w + 1; x != written.end(); ++x)
+      if (ragged_overlap(w->at, w->bytes, x->at, x->bytes)) return true;
+    for (const Span& x : read)
+      if (ragged_overlap(w->at, w->bytes, x.at, x.bytes)) return true;
+  }
+  return false;
+}
 inline bool ragged_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ragged_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool ragged_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }

@@ -114,9 +114,23 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
     if (!ragged_aligned4(x)) return TQ_ERR_ALIGNMENT;
   if (workspace_bytes < need) return TQ_ERR_INVALID_ARG;
   const long long rows = B * Hq * N, out_bytes = rows * D * (out_dtype == TQ_F32 ? 4 : 2);
-  if (ragged_overlap(q, rows * D * 2, out, out_bytes) || ragged_overlap(q, rows * D * 2, lse, rows * 4) ||
-      ragged_overlap(q, rows * D * 2, workspace, need) || ragged_overlap(out, out_bytes, lse, rows * 4) ||
-      ragged_overlap(out, out_bytes, workspace, need) || ragged_overlap(lse, rows * 4, workspace, need))
+  const long long ct = B * Hkv * cache->t_cap, tt = B * Hkv * tree->t_cap;
+  const long long xk = D * k_bits / 8, xv = D * v_bits / 8, xs = D / 16;  // bytes of a token
+  if (ragged_shared({{out, out_bytes}, {lse, rows * 4}, {workspace, need}},
+                    {{q, rows * D * 2},
+                     {cache->k_codes, ct * xk},
+                     {cache->k_scales, ct * xs},
+                     {cache->k_zeros, ct * xs},
+                     {cache->v_codes, ct * xv},
+                     {cache->v_scales, ct * xs},
+                     {tree->k_codes, tt * xk},
+                     {tree->k_scales, tt * xs},
+                     {tree->k_zeros, tt * xs},
+                     {tree->v_codes, tt * xv},
+                     {tree->v_scales, tt * xs},
+                     {parents, B * N * 4},
+                     {lens, B * 4},
+                     {left_pad, B * 4}}))
     return TQ_ERR_INVALID_ARG;
   auto view = [](const tq_packed_cache* c) {
     return PackedView{static_cast<const uint8_t*>(c->k_codes), static_cast<const uint16_t*>(c->k_scales),
