@@ -1,0 +1,25 @@
+"""Properties of the kernels' sources that no run shows."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "turboquant_kv_cache_tq_gb300", "csrc")
+
+
+def _sources():
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh", ".h")):
+            with open(os.path.join(CSRC, name)) as f:
+                yield name, f.read()
+
+
+def test_dynamic_shared_memory_states_its_alignment():
+    """Dynamic shared memory follows a kernel's static arrays: without an
+    alignment of its own it starts wherever they happen to end, and 16-byte
+    accesses to it work by luck."""
+    found = 0
+    for name, text in _sources():
+        for line in re.findall(r"extern __shared__[^;]*;", text):
+            found += 1
+            align = re.search(r"__align__\((\d+)\)", line)
+            assert align and int(align.group(1)) >= 16, (name, line)
+    assert found >= 6

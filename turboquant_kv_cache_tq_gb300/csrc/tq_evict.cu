@@ -71,7 +71,7 @@ __device__ __forceinline__ int cluster_read(uint32_t a, int rank) {
 }
 
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ int select_smem[];
+  extern __shared__ __align__(16) int select_smem[];  // (read in pieces of 16 bytes)
   int* s_hist = select_smem;                       // [256][kSelectCopies]
   uint32_t* s_key = reinterpret_cast<uint32_t*>(select_smem + 256 * kSelectCopies);
   __shared__ int s_bins[2][256];                   // this block's digit counts, by pass parity
