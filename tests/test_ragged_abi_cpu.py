@@ -255,6 +255,16 @@ def test_cutting_into_less_room_than_the_budget_is_refused(tq):
             tq.evict_rows(cache, w, T, keep, 2, t_cap=t_cap)
 
 
+def test_a_stream_of_another_device_is_refused(tq):
+    """(It was passed over, and the current stream of the tensors' device taken.)"""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream"):
+        tq._elsewhere(torch.device("cuda", 0), Stream())
+    assert tq._elsewhere(torch.device("cuda", 1), Stream()) is True
+
+
 def test_reference_of_one_token_by_hand():
     """The reference itself: one key alone gives its own value row back, and
     lse is the score."""

@@ -454,6 +454,8 @@ def _elsewhere(device, stream) -> bool:
     and error word."""
     if device.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device, got %s" % device)
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
     return stream is not None or device.index != torch.cuda.current_device()
 
 
