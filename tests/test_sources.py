@@ -23,3 +23,12 @@ def test_dynamic_shared_memory_states_its_alignment():
             align = re.search(r"__align__\((\d+)\)", line)
             assert align and int(align.group(1)) >= 16, (name, line)
     assert found >= 6
+
+
+def test_device_helpers_of_the_ragged_caches_have_callers():
+    text = dict(_sources())
+    everything = "".join(text.values())
+    for name in ("tq_ragged.cuh", "tq_ragged_tiles.cuh", "tq_tcgen05.cuh", "tq_tree_attention.cuh"):
+        for helper in re.findall(r"__forceinline__ [\w:<> ]*?(\w+)\(", text[name]):
+            if helper not in ("TileUnit", "operator"):  # (a constructor)
+                assert len(re.findall(r"\b%s\b" % helper, everything)) > 1, (name, helper)

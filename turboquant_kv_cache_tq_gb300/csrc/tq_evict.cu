@@ -41,7 +41,7 @@ struct SelectParams {
   int* index;
   int* count;
   long long w_cap;
-  int B, H, T, keep, recent;
+  int H, T, keep, recent;
   int cluster;    // blocks per row
   int held;       // keys of a slice in shared memory: all (slice <= kSelectKeys) or none
 };
@@ -363,7 +363,6 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   p.index = index;
   p.count = count;
   p.w_cap = w_cap;
-  p.B = static_cast<int>(B);
   p.H = static_cast<int>(H);
   p.T = static_cast<int>(T);
   p.keep = static_cast<int>(keep);

@@ -150,13 +150,16 @@ __device__ __forceinline__ void tile_words(uint32_t a, int h, uint32_t (&w)[(B +
   }
 }
 
-// One warp copies n rows (at most 64) of X bytes, src_pitch bytes apart, side by
-// side, asynchronously and in the widest pieces that the rows' alignment allows.
+// One warp copies n rows (at most 128) of X bytes, src_pitch bytes apart, side by
+// side, asynchronously and in the widest pieces that the rows' alignment allows
+// (per of them a row: at most 32, as 512 bytes come in pieces of 16).
 __device__ __forceinline__ void copy_rows_any(uint32_t dst, const uint8_t* src, int src_pitch, int X, int n, int lane) {
   const int odd = X | src_pitch;
   const int shift = (odd & 15) == 0 ? 4 : (odd & 7) == 0 ? 3 : 2;
   const int per = X >> shift;
-  const unsigned inv = (1u << 20) / per + 1;  // i / per for i < 2^13 / per (n per pieces: at most 4096)
+  // i / per = i inv >> 20 while i per < 2^20 and i inv < 2^32: i is below n per <=
+  // 4096, so the products stay below 2^17 and 2^28
+  const unsigned inv = (1u << 20) / per + 1;
 #pragma unroll 2
   for (int i = lane; i < n * per; i += 32) {
     const int t = static_cast<int>(i * inv >> 20), c = (i - t * per) << shift;
