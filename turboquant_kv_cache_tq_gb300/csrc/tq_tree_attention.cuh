@@ -446,11 +446,6 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
       mma_commit(bars + kcSFull + 8 * sb, issue);
     }
   }
-  // the last parts' arrivals, which no decoding warp waits for: they land before
-  // the block gives its shared memory back
-  const int parts = it * S::SUBS;
-  for (int k = max(parts - S::KS, 0); k < parts; ++k)
-    if (!warp_wait(bars + kcKEmpty + 8 * (k % S::KS), (k / S::KS) & 1, quit, p.err)) return;
 }
 
 // The weighted values' warp: O += P V, the weights as a high part, a remainder
@@ -488,8 +483,6 @@ __device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
       mma_commit(bars + kcVEmpty + 8 * st, issue);
     }
   }
-  for (int k = max(it - S::VS, 0); k < it; ++k)  // (as in tree_scores)
-    if (!warp_wait(bars + kcVEmpty + 8 * (k % S::VS), (k / S::VS) & 1, quit, p.err)) return;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -981,6 +974,13 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
     } else {
       if (warp == 20) tree_scores<D, F32>(p, sm, ctl);
       else tree_weigh<D, F32>(p, sm, ctl);
+      // the last parts' and tiles' arrivals, which no decoding warp waits for: they
+      // land before the block gives its shared memory back
+      const int count = *reinterpret_cast<const int*>(ctl + kcStart + 12) * (warp == 20 ? S::SUBS : 1);
+      const int stages = warp == 20 ? S::KS : S::VS, empty = warp == 20 ? kcKEmpty : kcVEmpty;
+#pragma unroll 1
+      for (int k = max(count - stages, 0); k < count; ++k)
+        if (!warp_wait(bars + empty + 8 * (k % stages), (k / stages) & 1, reinterpret_cast<volatile int*>(ctl + kcQuit), p.err)) break;
       if (*reinterpret_cast<volatile int*>(ctl + kcQuit) != 0) {  // gave up: let the matrix work in flight end
         mma_commit(bars + kcDrain + 8 * (warp - 20), elect_lane());
         mbar_wait(bars + kcDrain + 8 * (warp - 20), 0, kBulkWaitLimit);
