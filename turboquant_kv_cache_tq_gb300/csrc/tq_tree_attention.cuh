@@ -978,10 +978,11 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
       // land before the block gives its shared memory back
       const int count = *reinterpret_cast<const int*>(ctl + kcStart + 12) * (warp == 20 ? S::SUBS : 1);
       const int stages = warp == 20 ? S::KS : S::VS, empty = warp == 20 ? kcKEmpty : kcVEmpty;
+      volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
 #pragma unroll 1
       for (int k = max(count - stages, 0); k < count; ++k)
-        if (!warp_wait(bars + empty + 8 * (k % stages), (k / stages) & 1, reinterpret_cast<volatile int*>(ctl + kcQuit), p.err)) break;
-      if (*reinterpret_cast<volatile int*>(ctl + kcQuit) != 0) {  // gave up: let the matrix work in flight end
+        if (!warp_wait(bars + empty + 8 * (k % stages), (k / stages) & 1, quit, p.err)) break;
+      if (*quit != 0) {  // gave up: let the matrix work in flight end
         mma_commit(bars + kcDrain + 8 * (warp - 20), elect_lane());
         mbar_wait(bars + kcDrain + 8 * (warp - 20), 0, kBulkWaitLimit);
       }
