@@ -405,7 +405,9 @@ TQ_API int64_t tq_tree_attention_workspace_size(int64_t B, int64_t Hq, int64_t H
  *   weights_in, weights_out  fp32 [B, Hkv, w_cap], w_cap >= T; weights_in may
  *            be NULL (zeros) or weights_out itself. Every element of
  *            weights_out is written unless the two are the same array: then
- *            only those that an observer attends to.
+ *            only those that an observer attends to. (So sums in arrays much
+ *            longer than the sequences are best kept in place: what is outside
+ *            them is copied otherwise, 8 heads of 131072 words in 325 us.)
  * The sum over a token's observers has a fixed order: equal calls give equal
  * bits. Limits as for tq_tree_attention, but N and P are bounded only by
  * (Hq / Hkv) * P <= 65536. The kernel bounds its waits (tq_device_status). */

@@ -21,7 +21,11 @@
 // 128: 74 us, where the bytes take 37; a warp a token without matrix instructions
 // took 2354) the hand-overs of a tile from copy to decode, product and sum, 1300
 // cycles each: sixteen decoding warps instead of eight are no faster (80 us), nor
-// are sums fetched a tile ahead (74). In a small call (8 x 4096 tokens, 256 columns:
+// are sums fetched a tile ahead (74), nor sums in place (73). Where few (batch row,
+// head) have long stretches outside their sequences, and the sums are not in place,
+// it is the copy of those instead, two warps of one block for each: 8 x 8 x 8192
+// tokens 28 us (in place 22), 2 x 2 x 16384 at head_dim 512 31 (16), 8 heads of 4096
+// tokens in arrays of 131072 327 (6). In a small call (8 x 4096 tokens, 256 columns:
 // 12.4 us) the chain of cut, queries and two tiles. There the queries were the
 // longest link: 19.4 us when one of the summing groups fetched them, with two
 // divisions a piece.

@@ -10,8 +10,12 @@
 // a kv head (tens to hundreds), so a decoded key or value is used by all of
 // them; the packed bytes are read and decoded once per 128 rows and both
 // products run on tcgen05.mma (M = 128 rows) with the accumulators in tensor
-// memory. What then bounds the kernel is the decoding itself (see the figures
-// in tree_split_kernel's comment), as in the decode attention of few rows.
+// memory. (See the figures in tree_split_kernel's comment.) Few rows take the same
+// path and gain nothing from it: one node a sequence, four rows a kv head, takes
+// 148 us where 16 nodes take 162, and tq_decode_attention, which serves equal
+// lengths and at most 16 rows, reads the same format 1.6 times as fast (32 x 8
+// heads, k8 / v8: 8192 tokens a sequence in 124 us, where the 148 are for 6144 on
+// average).
 //
 // The rows are padded to 128 lanes of tensor memory. With at most 64 rows (and
 // tiles of 64 tokens) each row takes two lanes, and lane copy c takes every
@@ -850,21 +854,26 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 
 // The partial results: one block an SM, which holds all of its tensor memory.
 //
-// What bounds it (32 sequences x 8 heads x 8192 tokens, head_dim 128, 16 nodes,
-// k8 / v8): 161 us in a graph, where the packed bytes take 67 and the products
-// 27; 155 us with 3-bit values. A counter run of 8 such sequences: 0.55
-// instructions a cycle and scheduler, tensor pipe 33%, DRAM 27% busy; warps wait
-// for tensor memory and barriers (4.2 of 12.5 cycles an instruction), for
-// instructions (1.1) and for results (1.4). A tile takes 1700 cycles; in two tiles'
-// time a value warp decodes for 2500, a key warp for 1100, a softmax warp works for
-// 2000. So it is the values' decode and the hand-overs around it, at what six
-// roles of 28 warps let the schedulers issue.
+// What bounds it (32 sequences x 8 heads of 4096 to 8192 tokens, head_dim 128, 16
+// nodes, k8 / v8): 162 us in a graph, where the packed bytes take 67 and the
+// products 27. Neither is it: 3-bit values, 28% fewer bytes, take 157 us, 4-bit ones
+// 160. A counter run of 8 such sequences: 0.56 instructions a cycle and scheduler,
+// tensor pipe 35%, DRAM 28% busy; of the 12.5 cycles that a warp takes an
+// instruction it waits 3.4 for tensor memory and barriers' words, 1.5 for its turn,
+// 1.4 for fixed latencies, 1.3 at barriers, 1.2 for instructions. With two value
+// stages an instrumented copy took 1700 cycles a tile: in two tiles' time a value
+// warp decoded for 2500, a key warp for 1100, a softmax warp worked for 2000. The
+// chain of hand-overs among six roles is what remains; which link of it sets the
+// pace with four stages was not measured, and tq_decode_attention's rate on the
+// same format says that the decode alone does not.
 // How it came there: a warp a row, no matrix instructions, 26.2 ms; roles around
-// tcgen05 406 us; packed rows by bulk copies 271; roles bound to schedulers with
-// rolled loops 230; a second softmax group, weights written over their scores 210;
-// one elected lane issuing from uniform control flow 183; turns counted in the cut
-// 168; four value stages 161. (Rolled half groups in the decode 218, scores read 32
-// columns at a time 15% slower.)
+// tcgen05 406 us; packed rows by bulk copies, roles bound to schedulers, rolled
+// loops 271; two softmax groups, weights written over their scores 230; addresses
+// out of the decoding loops 210; one elected lane issuing from uniform control flow
+// 189; the loader's lane 183; turns counted in the cut, places in 32 bits 172;
+// queries and ancestors 168; four value stages 161. (Rolled half groups in the decode
+// 218, scores read 32 columns at a time 15% slower.) The same instructions placed
+// otherwise differ by 5%.
 //
 // A small call (8 heads x 4096 tokens, 32 nodes: 18 us with the combine) is one
 // chain: cut 1.3 us, queries into tensor memory 2, first tile 1.5, three more 3,
