@@ -32,3 +32,13 @@ def test_device_helpers_of_the_ragged_caches_have_callers():
         for helper in re.findall(r"__forceinline__ [\w:<> ]*?(\w+)\(", text[name]):
             if helper not in ("TileUnit", "operator"):  # (a constructor)
                 assert len(re.findall(r"\b%s\b" % helper, everything)) > 1, (name, helper)
+
+
+def test_calls_on_ragged_caches_cannot_throw():
+    """Below a C entry point an exception ends the process: no containers,
+    strings, locks or allocations that throw."""
+    text = dict(_sources())
+    for name in ("tq_ragged.cuh", "tq_ragged_tiles.cuh", "tq_tcgen05.cuh", "tq_tree_attention.cuh", "tq_tree_attention.cu",
+                 "tq_attention_weights.cu", "tq_evict.cu"):
+        code = re.sub(r"//[^\n]*|/\*.*?\*/", "", text[name], flags=re.S)
+        assert not re.search(r"std::(vector|string|map|function|mutex|lock_guard)|\bnew\b|\bthrow\b", code), name

@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) attention_weights_kernel(c
 template <int D>
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t s) {
   using S = WeightsShape<D>;
-  cudaError_t e = allow_smem(attention_weights_kernel<D>, S::SMEM);
+  cudaError_t e = allow_smem<attention_weights_kernel<D>>(S::SMEM);
   if (e != cudaSuccess) return e;
   // one block per SM (each holds all of an SM's tensor memory), but no more
   // than there can be tiles, or rows to copy

@@ -374,7 +374,7 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   const int64_t slice = (T + p.cluster - 1) / p.cluster;
   p.held = slice <= kSelectKeys;
   const int smem = (256 * kSelectCopies + (p.held ? static_cast<int>(slice) : 0)) * 4;
-  if (allow_smem(evict_select_kernel, (256 * kSelectCopies + kSelectKeys) * 4) != cudaSuccess) return TQ_ERR_CUDA;
+  if (allow_smem<evict_select_kernel>((256 * kSelectCopies + kSelectKeys) * 4) != cudaSuccess) return TQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B * H * p.cluster));
   cfg.blockDim = dim3(kSelectThreads);

@@ -3,10 +3,9 @@
 // that only the device knows, draft trees, and the host's checks.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <initializer_list>
-#include <mutex>
-#include <vector>
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -32,23 +31,19 @@ __device__ __forceinline__ void row_range(const int* lens, const int* left_pad, 
 
 // ---- host side
 // Lets a kernel take `bytes` of dynamic shared memory on the current device
-// (asked for once per kernel and device).
-template <typename Params>
-inline cudaError_t allow_smem(void (*kernel)(Params), int bytes) {
-  struct Entry {
-    const void* kernel;
-    int dev;
-  };
-  static std::mutex mutex;
-  static std::vector<Entry> done;
+// (asked for once per kernel and device; two threads may both ask). Nothing here
+// may throw: it runs below C entry points.
+template <auto KERNEL>
+inline cudaError_t allow_smem(int bytes) {
+  constexpr int kDevices = 128;
+  static std::atomic<bool> done[kDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mutex);
-  for (const Entry& x : done)
-    if (x.kernel == reinterpret_cast<const void*>(kernel) && x.dev == dev) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.push_back(Entry{reinterpret_cast<const void*>(kernel), dev});
+  const bool known = dev >= 0 && dev < kDevices;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
   return e;
 }
 

@@ -1185,7 +1185,7 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) tree_combine_kernel(con
 template <int D, bool F32>
 cudaError_t launch_tree_split(const TreeParams& p, cudaStream_t s) {
   using S = TreeShape<D, F32>;
-  cudaError_t e = allow_smem(tree_split_kernel<D, F32>, S::SMEM);
+  cudaError_t e = allow_smem<tree_split_kernel<D, F32>>(S::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl_block(tree_split_kernel<D, F32>, p.grid, S::THREADS, p, s, S::SMEM);
 }
