@@ -1,6 +1,8 @@
 """GPU tests of the calls on ragged packed caches at the ends of what they
 accept: budgets and caches of nothing, full rows, capacities far beyond the
 sequences."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -212,3 +214,40 @@ def test_views_into_larger_storage():
                  lambda x: tq.tq_attention_weights(x, want[1], main, 100, 8, True)):
         with pytest.raises(tq.TQError):
             call(room[1:1 + q.numel()].view(q.shape))
+
+
+def test_a_refused_launch_does_not_fail_the_next_call():
+    """A launch that the host refuses (on the legacy stream, while a stream that
+    waits for it is captured) is that call's error alone."""
+    B, Hkv, G, N, T, D = 1, 2, 2, 4, 100, 64
+    main, tree = (rc.to_gpu(rc.random_cache(B, Hkv, n, D, 8, True, 3, n)) for n in (T, N))
+    q = torch.randn((B, Hkv * G, N, D), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    out, lse = torch.empty_like(q), torch.empty((B, Hkv * G, N), device="cuda")
+    ws = torch.empty(tq.tq_tree_attention_workspace_size(B, Hkv * G, Hkv, N, D), dtype=torch.uint8, device="cuda")
+    w = torch.zeros((B, Hkv, T), device="cuda")
+    index, count = torch.empty((B, Hkv, 9), dtype=torch.int32, device="cuda"), torch.empty((B,), dtype=torch.int32, device="cuda")
+    dst, length = tq.alloc_cache(B, Hkv, 9, D, 8, 3), torch.empty((B,), dtype=torch.int32, device="cuda")
+    path = torch.zeros((B, 2), dtype=torch.int32, device="cuda")
+    calls = [lambda: tq.tq_tree_attention(q, main, T, tree, 8, True, 3, out=out, lse=lse, workspace=ws),
+             lambda: tq.tq_attention_weights(q, lse, main, T, 8, True, weights=w, out=w),
+             lambda: tq.tq_evict_select(w, T, 9, 3, index=index, count=count),
+             lambda: tq.tq_cache_gather(main, dst, path, dst_len=length)]
+    assert torch.cuda.current_stream().cuda_stream == 0
+    for call in calls:  # what a first call sets up
+        call()
+    torch.cuda.synchronize()
+    driver = ctypes.CDLL("libcuda.so.1")
+    for call in calls:
+        stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+        assert driver.cuStreamCreate(ctypes.byref(stream), 0) == 0
+        assert driver.cuStreamBeginCapture_v2(stream, 0) == 0
+        try:
+            with pytest.raises(tq.TQError) as refused:
+                call()
+        finally:
+            driver.cuStreamEndCapture(stream, ctypes.byref(graph))
+            driver.cuStreamDestroy_v2(stream)
+        assert refused.value.status == 6  # TQ_ERR_CUDA
+        call()
+    torch.cuda.synchronize()
+    assert torch.isfinite(lse).all() and count.tolist() == [9] and length.tolist() == [2]

@@ -564,5 +564,5 @@ extern "C" tq_status tq_attention_weights(const void* q, const float* lse, int64
     case 256: e = launch_weights<256>(p, s); break;
     default: e = launch_weights<512>(p, s); break;
   }
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  return launch_status(e);
 }

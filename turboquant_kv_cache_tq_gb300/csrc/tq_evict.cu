@@ -374,7 +374,8 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   const int64_t slice = (T + p.cluster - 1) / p.cluster;
   p.held = slice <= kSelectKeys;
   const int smem = (256 * kSelectCopies + (p.held ? static_cast<int>(slice) : 0)) * 4;
-  if (allow_smem<evict_select_kernel>((256 * kSelectCopies + kSelectKeys) * 4) != cudaSuccess) return TQ_ERR_CUDA;
+  const cudaError_t e = allow_smem<evict_select_kernel>((256 * kSelectCopies + kSelectKeys) * 4);
+  if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B * H * p.cluster));
   cfg.blockDim = dim3(kSelectThreads);
@@ -386,8 +387,7 @@ extern "C" tq_status tq_evict_select(const float* weights, int64_t B, int64_t H,
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, evict_select_kernel, p));
 }
 
 extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed_cache* dst, int64_t B, int64_t H,
@@ -460,13 +460,16 @@ extern "C" tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed
   p.n = static_cast<int>(n);
   p.heads = index_heads != 0;
   p.chunks = static_cast<unsigned>(chunks);
-  const unsigned grid = static_cast<unsigned>(chunks * B * H);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (ws == 16) cache_gather_kernel<uint4, uint4, uint4><<<grid, kGatherThreads, 0, st>>>(p);
-  else if (ws == 8) cache_gather_kernel<uint4, uint4, uint2><<<grid, kGatherThreads, 0, st>>>(p);
-  else if (wk == 16 && wv == 16) cache_gather_kernel<uint4, uint4, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
-  else if (wk == 16) cache_gather_kernel<uint4, uint2, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
-  else if (wv == 16) cache_gather_kernel<uint2, uint4, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
-  else cache_gather_kernel<uint2, uint2, uint32_t><<<grid, kGatherThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(chunks * B * H));
+  cfg.blockDim = dim3(kGatherThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (ws == 16) e = cudaLaunchKernelEx(&cfg, cache_gather_kernel<uint4, uint4, uint4>, p);
+  else if (ws == 8) e = cudaLaunchKernelEx(&cfg, cache_gather_kernel<uint4, uint4, uint2>, p);
+  else if (wk == 16 && wv == 16) e = cudaLaunchKernelEx(&cfg, cache_gather_kernel<uint4, uint4, uint32_t>, p);
+  else if (wk == 16) e = cudaLaunchKernelEx(&cfg, cache_gather_kernel<uint4, uint2, uint32_t>, p);
+  else if (wv == 16) e = cudaLaunchKernelEx(&cfg, cache_gather_kernel<uint2, uint4, uint32_t>, p);
+  else e = cudaLaunchKernelEx(&cfg, cache_gather_kernel<uint2, uint2, uint32_t>, p);
+  return launch_status(e);
 }

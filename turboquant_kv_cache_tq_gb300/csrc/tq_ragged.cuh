@@ -47,6 +47,14 @@ inline cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// The status of a call from what its launches returned. A failed launch's error
+// is taken out of the runtime, where the next call that looks there would find it.
+inline tq_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return TQ_OK;
+  cudaGetLastError();
+  return TQ_ERR_CUDA;
+}
+
 // Whether every buffer (a cache without room has none) is device memory: bulk
 // copies are only used between device and shared memory.
 inline bool ragged_device_memory(std::initializer_list<const void*> ptrs) {

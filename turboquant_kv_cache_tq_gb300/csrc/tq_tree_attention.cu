@@ -191,5 +191,5 @@ extern "C" tq_status tq_tree_attention(const void* q, int64_t B, int64_t Hq, int
     case 256: e = launch_tree<256>(p, s); break;
     default: e = launch_tree<512>(p, s); break;
   }
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  return launch_status(e);
 }
