@@ -34,6 +34,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -147,27 +148,47 @@ def _code_only(text: str) -> str:
     return " ".join("".join(out).split())
 
 
-def kernel_source_hash() -> str:
-    """Hash of the kernel sources (every file of the package's csrc folder,
-    comments and layout left out)."""
+# The translation units of each profiled kernel, by the start of their names.
+KERNEL_UNITS = {"encode_kernel": "tq_encode_", "decode_kernel": "tq_decode_", "decode_bulk_kernel": "tq_decode_",
+                "attn_split_kernel": "tq_attention_d", "attn_combine_kernel": "tq_attention_d"}
+
+
+def kernel_source_hash(kernel: str | None = None) -> str:
+    """Hash of the kernel sources, comments and layout left out: every file of
+    the package's csrc folder, or (kernel given) the kernel's translation units,
+    the C ABI that calls it and the files of the folder that they include, so
+    that another kernel's sources do not count."""
     csrc = os.path.join(ROOT, "turboquant_kv_cache_tq_gb300", "csrc")
-    h = hashlib.sha256()
-    for name in sorted(os.listdir(csrc)):
+    text = {}
+    for name in os.listdir(csrc):
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
-            h.update(name.encode() + _code_only(f.read()).encode())
+            text[name] = f.read()
+    names = set(text)
+    if kernel is not None:
+        units = KERNEL_UNITS.get(kernel)
+        found = [n for n in text if n.endswith(".cu") and (n == "tq_abi.cu" or (units and n.startswith(units)))]
+        names = set()
+        while found:
+            n = found.pop()
+            if n in text and n not in names:
+                names.add(n)
+                found += re.findall(r'^\s*#include "([^"]+)"', text[n], re.M)
+    h = hashlib.sha256()
+    for name in sorted(names):
+        h.update(name.encode() + _code_only(text[name]).encode())
     return h.hexdigest()[:16]
 
 
 def profiled_traffic(key: str):
     """dram bytes per launch ("<kernel>@<workload>") from a committed ncu
-    summary, if it was taken on the current kernel sources; else None."""
+    summary, if it was taken on the kernel's current sources; else None."""
     try:
         with open(PROFILE_TRAFFIC) as f:
             d = json.load(f)
     except (OSError, ValueError):
         return None
     e = d.get(key)
-    if not e or e.get("source_hash") != kernel_source_hash():
+    if not e or e.get("source_hash") != kernel_source_hash(key.split("@")[0]):
         return None
     return e.get("dram_bytes_per_launch")
 
