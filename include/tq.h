@@ -441,8 +441,8 @@ TQ_API tq_status tq_evict_select(const float* weights, int64_t B, int64_t H, int
  *            values count as 0; NULL: 0.
  *   dst_len  NULL, or int32 [B]: receives min(dst_off[b] + count[b],
  *            dst->t_cap); it must not overlap dst_off or count. Where the row
- *            was too short for its path, dst_len - dst_off tokens were copied:
- *            the n_path for tq_attention_weights.
+ *            was too short for its path (dst_off within [0, dst->t_cap]), dst_len
+ *            - dst_off tokens were copied: the n_path for tq_attention_weights.
  *   src_weights, dst_weights  fp32 [B, H, the cache's t_cap] moved beside the
  *            tokens; src_weights NULL with dst_weights given: zeros are
  *            written. Both NULL: no weights.

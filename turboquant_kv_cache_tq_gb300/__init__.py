@@ -615,8 +615,9 @@ def commit_path(cache: dict, lens: torch.Tensor, tree: dict, path: torch.Tensor,
     each sequence of `cache` (weights, when given, start at zero). Returns the
     new lengths. A sequence takes no more tokens than its row has room for: the
     rest of its path is dropped, and the new length is the capacity. So what was
-    appended is new - lens, not n_path: give tq_attention_weights that, or its
-    observers sit at wrong tokens where a row was full."""
+    appended is new - lens (lens within the capacity), not n_path: give
+    tq_attention_weights that, or its observers sit at wrong tokens where a row was
+    full."""
     return tq_cache_gather(tree, cache, path, count=n_path, dst_off=lens, dst_weights=weights, stream=stream)[1]
 
 
