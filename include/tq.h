@@ -455,6 +455,107 @@ TQ_API tq_status tq_cache_gather(const tq_packed_cache* src, const tq_packed_cac
                                  const int32_t* count, const int32_t* dst_off, int32_t* dst_len,
                                  const float* src_weights, float* dst_weights, void* stream);
 
+/* ---- new tokens: append, window, shared prefix --------------------------------
+ * One layer's step on ragged packed caches (no counterpart on the pages: an
+ * addition of this library): the new tokens' keys and values are turned to their
+ * positions, quantised and written at every sequence's end (tq_append_kv), then
+ * their queries attend to the cache (tq_window_attention; tq_prefix_attention
+ * where sequences begin with the same tokens). lens, left_pad and T as above;
+ * count, int32 device array [B], says how many of the N new tokens of the call
+ * batch row b has (values outside [0, N] count as the nearer end; NULL: N
+ * everywhere). */
+
+/* Rows of D contiguous elements, [B, H, N] of them: row (b, h, n) begins
+ * b * stride_b + h * stride_h + n * stride_t elements behind data. Strides are not
+ * negative; those of axes longer than one are multiples of 16 bytes, and data is
+ * 16-byte aligned. Zero strides (broadcast rows) are fine. */
+typedef struct {
+    const void* data;
+    int64_t stride_b, stride_h, stride_t;
+} tq_rows;
+
+/* Appends new tokens to the sequences of a packed cache: new token n < count[b] of
+ * batch row b becomes token lens[b] + n of the row (dropped from the capacity on).
+ *   q        NULL, or the queries [B, Hq, N, D]: turned like the keys into q_out,
+ *            all N of them, whatever count says.
+ *   k, v     the new keys and values [B, Hkv, N, D], of type dtype as q.
+ *   cos, sin fp32 [length, rot_dim / 2]: the angles of every position, scaled for
+ *            long contexts as the model wants them.
+ *   rot_dim  how many of a row's first elements turn: even, at most D; 0: none
+ *            (cos and sin may then be NULL). Pair j of a row at position a is
+ *            (x, y) -> (x cos[a][j] - y sin[a][j], y cos[a][j] + x sin[a][j]), with
+ *            elements 2 j and 2 j + 1 where interleaved is 1, j and j + rot_dim / 2
+ *            where it is 0.
+ *   positions  NULL, or int32 device array [B, N]. NULL: token lens[b] + n has
+ *            position lens[b] - left_pad[b] + n. Positions outside [0, length) count
+ *            as the nearer end.
+ *   lens     int32 device array [B], negative values count as 0; NULL: 0
+ *            everywhere. left_pad: used for positions only, within [0, lens].
+ *   q_out    [B, Hq, N, D] of dtype, contiguous.
+ *   new_lens int32 [B]: receives min(lens[b] + count[b], cache->t_cap).
+ * The rotation rounds every product and sum to fp32; the turned keys are encoded
+ * as tq_encode_kv encodes fp32 keys (they are not rounded to dtype on the way), the
+ * values as it encodes dtype values. Nothing else of the cache is touched. */
+TQ_API tq_status tq_append_kv(const tq_rows* q, const tq_rows* k, const tq_rows* v, tq_dtype dtype,
+                              int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D,
+                              const float* cos, const float* sin, int64_t length, int64_t rot_dim, int interleaved,
+                              const int32_t* positions, const int32_t* lens, const int32_t* left_pad,
+                              const int32_t* count, const tq_packed_cache* cache,
+                              int k_bits, int k_signed, int v_bits, void* q_out, int32_t* new_lens, void* stream);
+
+/* Attention of new tokens that are in the cache already (tq_append_kv) over a
+ * sliding window and each sequence's first tokens: the arithmetic of
+ * tq_tree_attention. Query n < count[b] of batch row b sits at token
+ * p = lens[b] - count[b] + n and attends to the tokens left_pad[b] <= t <= p with
+ * t > p - window or t < left_pad[b] + sinks.
+ *   q        [B, Hq, N, D] bf16, contiguous.
+ *   window   at least 1; T or more: every token up to p. sinks: at least 0.
+ *   out      [B, Hq, N, D] of out_dtype; lse NULL or fp32 [B, Hq, N], as for
+ *            tq_tree_attention. A query that its sequence does not have (n >=
+ *            count[b], or p < left_pad[b]) gives zeros and -inf.
+ *   workspace  device scratch of at least tq_window_attention_workspace_size bytes
+ *            (16-byte aligned), not in use by another call still running; it needs
+ *            no initialisation.
+ * Masked tokens never reach a row, whatever their bytes decode to; NaN as for
+ * tq_tree_attention. Limits: D in {64, 128, 256, 512}; Hq a multiple of Hkv; N >= 1,
+ * (Hq / Hkv) * N <= 2^20, B * Hq * N < 2^31 - 16; any t_cap >= T. B == 0 is a no-op.
+ * Equal calls give equal bits on GPUs of one size. The kernels bound their waits
+ * (tq_device_status). */
+TQ_API tq_status tq_window_attention(const void* q, int64_t B, int64_t Hq, int64_t N,
+                                     const tq_packed_cache* cache, int64_t Hkv, int64_t T, int64_t D,
+                                     int k_bits, int k_signed, int v_bits, const int32_t* lens,
+                                     const int32_t* left_pad, const int32_t* count, int64_t window, int64_t sinks,
+                                     float scale, void* out, tq_dtype out_dtype, float* lse,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of scratch tq_window_attention needs for these sizes on the current
+ * device. Negative: -TQ_ERR_HEAD_DIM or -TQ_ERR_INVALID_ARG. */
+TQ_API int64_t tq_window_attention_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D);
+
+/* Attention of new tokens over a prefix that sequences share and over each
+ * sequence's own tokens, the prefix read and decoded once for all that share it.
+ *   prefix   a packed cache of Bp rows (B a multiple of Bp): sequences
+ *            g * B / Bp to (g + 1) * B / Bp - 1 begin with row g's tokens
+ *            [0, prefix_lens[g]). prefix_lens: int32 device array [Bp], values
+ *            outside [0, P] count as the nearer end; NULL: P everywhere.
+ *   cache    the sequences' own tokens, the new ones included: batch row b holds
+ *            tokens [left_pad[b], lens[b]) that follow its prefix.
+ * Query n < count[b] of batch row b attends to the whole prefix and to its own
+ * tokens left_pad[b] <= t <= p = lens[b] - count[b] + n. Everything else as for
+ * tq_window_attention; the rows that share a prefix are limited to
+ * (B / Bp) * (Hq / Hkv) * N <= 2^20. */
+TQ_API tq_status tq_prefix_attention(const void* q, int64_t B, int64_t Hq, int64_t N,
+                                     const tq_packed_cache* prefix, int64_t Bp, int64_t P,
+                                     const int32_t* prefix_lens, const tq_packed_cache* cache, int64_t Hkv, int64_t T,
+                                     int64_t D, int k_bits, int k_signed, int v_bits, const int32_t* lens,
+                                     const int32_t* left_pad, const int32_t* count, float scale,
+                                     void* out, tq_dtype out_dtype, float* lse,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of scratch tq_prefix_attention needs for these sizes on the current
+ * device. Negative: -TQ_ERR_HEAD_DIM or -TQ_ERR_INVALID_ARG. */
+TQ_API int64_t tq_prefix_attention_workspace_size(int64_t Bp, int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D);
+
 /* Device-side failures of the library's kernels on the current device (no
  * counterpart on the pages: failure detection of this library). Kernels that
  * wait on an asynchronous copy or a matrix product (the decode's bulk-copy path,

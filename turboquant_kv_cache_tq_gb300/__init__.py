@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -23,7 +24,9 @@ __all__ = [
     "tq_unrotate", "tq_lloyd_max_index", "tq_decode_attention", "tq_decode_attention_workspace_size",
     "tq_cache_assemble", "merge_rows", "extend_rows", "extract_row", "filter_rows", "tq_lloyd_max_fit",
     "tq_lloyd_max_fit_status", "tq_tree_attention", "tq_tree_attention_workspace_size", "tq_attention_weights",
-    "tq_evict_select", "tq_cache_gather", "commit_path", "evict_rows",
+    "tq_evict_select", "tq_cache_gather", "commit_path", "evict_rows", "tq_append_kv", "rope_tables",
+    "tq_window_attention", "tq_window_attention_workspace_size", "tq_prefix_attention",
+    "tq_prefix_attention_workspace_size",
     "tq_status_string", "alloc_cache", "HEAD_DIMS", "VALUE_BITS", "KEY_MODES",
 ]
 
@@ -102,6 +105,18 @@ def load_library(path: str) -> ctypes.CDLL:
     L.tq_evict_select.argtypes = [P, I64, I64, I64, I64, P, P, I64, I64, P, P, P]
     L.tq_cache_gather.restype = I
     L.tq_cache_gather.argtypes = [P, P, I64, I64, I64, I, I, P, I64, I, P, P, P, P, P, P]
+    L.tq_append_kv.restype = I
+    L.tq_append_kv.argtypes = [P, P, P, I, I64, I64, I64, I64, I64, P, P, I64, I64, I, P, P, P, P, P, I, I, I, P, P, P]
+    L.tq_window_attention.restype = I
+    L.tq_window_attention.argtypes = [P, I64, I64, I64, P, I64, I64, I64, I, I, I, P, P, P, I64, I64, ctypes.c_float,
+                                      P, I, P, P, I64, P]
+    L.tq_window_attention_workspace_size.restype = I64
+    L.tq_window_attention_workspace_size.argtypes = [I64] * 5
+    L.tq_prefix_attention.restype = I
+    L.tq_prefix_attention.argtypes = [P, I64, I64, I64, P, I64, I64, P, P, I64, I64, I64, I, I, I, P, P, P,
+                                      ctypes.c_float, P, I, P, P, I64, P]
+    L.tq_prefix_attention_workspace_size.restype = I64
+    L.tq_prefix_attention_workspace_size.argtypes = [I64] * 6
     L.tq_lloyd_max_fit.restype = I
     L.tq_lloyd_max_fit.argtypes = [P, I64, I, I, P, P, P, P, I64, P]
     L.tq_lloyd_max_fit_bounded.restype = I
@@ -640,6 +655,208 @@ def evict_rows(cache: dict, weights: torch.Tensor, T: int, keep: int, recent: in
     index, count = tq_evict_select(weights, T, keep, recent, lens=lens, left_pad=left_pad)
     _, length = tq_cache_gather(cache, dst, index, count=count, src_weights=weights, dst_weights=new)
     return dst, new, length
+
+
+# ---- new tokens: append, window, shared prefix --------------------------------------
+class TQRows(ctypes.Structure):
+    """tq_rows of include/tq.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
+
+
+def _rows(t, shape, dtype, what, device):
+    """A [B,H,N,D] tensor with contiguous rows as the library takes it."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or (t.stride(3) != 1 and t.numel()):
+        raise ValueError("%s must be a %s tensor %s on %s with contiguous rows" % (what, dtype, list(shape), device))
+    return TQRows(t.data_ptr(), *t.stride()[:3])
+
+
+def rope_tables(rot_dim: int, length: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
+                original: int = 0, low: float = 1.0, high: float = 4.0, device="cuda"):
+    """(cos, sin), fp32 [length, rot_dim / 2], of the angles position *
+    frequency_j, frequency_j = base ** (-2 j / rot_dim), computed in 64 bits and
+    rounded once. scaling, for contexts `factor` times as long as the trained one:
+    None; "linear" (every frequency / factor); "base" (a larger base, so that the
+    lowest frequency is divided by factor and the highest stays); "bands" (a
+    frequency that turns fewer than `low` times within the `original` trained
+    positions is divided by factor, one that turns more than `high` times stays,
+    with a linear passage between)."""
+    if rot_dim < 2 or rot_dim % 2 or length < 1:
+        raise ValueError("rot_dim must be even and positive, length positive")
+    if factor < 1 or base <= 0:
+        raise ValueError("factor must be at least 1, base positive")
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("a larger base needs two frequencies at least")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if original < 1 or not low < high:
+            raise ValueError("bands need the trained length `original` and low < high")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'bands', got %r" % (scaling,))
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * f
+    return angle.cos().float(), angle.sin().float()
+
+
+def tq_append_kv(k: torch.Tensor, v: torch.Tensor, cache: dict, lens, k_bits: int, k_signed: bool, v_bits: int,
+                 cos=None, sin=None, interleaved: bool = False, q=None, positions=None, left_pad=None, count=None,
+                 q_out=None, new_lens=None, stream=None):
+    """Appends N new tokens k, v [B,Hkv,N,D] (fp32 or bf16; rows contiguous, any
+    other strides of 16-byte multiples, such as views of a fused projection) to
+    the sequences of a packed cache, keys turned by rotary positions: tokens
+    lens[b] + n, n < count[b], of batch row b (lens, left_pad, count: int32 device
+    tensors [B] or None: 0, 0, N). cos, sin: fp32 [length, R / 2] (rope_tables), R
+    the elements of a row that turn, in neighbouring pairs when interleaved, else
+    j with j + R / 2; None: nothing turns. positions: int32 [B,N] or None (lens -
+    left_pad + n). q [B,Hq,N,D]: queries turned alike into q_out. Tokens past the
+    capacity are dropped. Returns (q_out or None, the new lengths)."""
+    dev = k.device
+    if k.dim() != 4 or k.dtype not in _DTYPE:
+        raise ValueError("k must be a [B,Hkv,N,D] float32 or bfloat16 tensor")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_append_kv(k, v, cache, lens, k_bits, k_signed, v_bits, cos, sin, interleaved, q, positions,
+                                left_pad, count, q_out, new_lens)
+    B, Hkv, N, D = k.shape
+    cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
+    kr, vr = _rows(k, k.shape, k.dtype, "k", dev), _rows(v, k.shape, k.dtype, "v", dev)
+    Hq, qr, q_ptr = 0, None, None
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be a [B,Hq,N,D] tensor")
+        Hq = q.shape[1]
+        qr = ctypes.byref(_rows(q, (B, Hq, N, D), k.dtype, "q", dev))
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, D), dtype=k.dtype, device=dev)
+        elif q_out.dtype is not k.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.device != dev:
+            raise ValueError("q_out must be a contiguous [B,Hq,N,D] tensor of q's dtype on q's device")
+        q_ptr = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    length, R = 0, 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2:
+            raise ValueError("cos and sin go together, [length, R / 2] each")
+        length, R = cos.shape[0], 2 * cos.shape[1]
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    st = lib().tq_append_kv(
+        qr, ctypes.byref(kr), ctypes.byref(vr), _DTYPE[k.dtype], B, Hq, Hkv, N, D,
+        _float_ptr(cos, (length, R // 2), "cos", dev), _float_ptr(sin, (length, R // 2), "sin", dev), length, R,
+        int(bool(interleaved)), _int_ptr(positions, (B, N), "positions", dev), _int_ptr(lens, (B,), "lens", dev),
+        _int_ptr(left_pad, (B,), "left_pad", dev), _int_ptr(count, (B,), "count", dev), ctypes.byref(cv), int(k_bits),
+        int(bool(k_signed)), int(v_bits), q_ptr, _int_ptr(new_lens, (B,), "new_lens", dev), _current_stream(dev))
+    _check(st, "tq_append_kv")
+    return q_out, new_lens
+
+
+def tq_window_attention_workspace_size(B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
+    """Bytes of scratch tq_window_attention needs (on the current device)."""
+    r = int(lib().tq_window_attention_workspace_size(int(B), int(Hq), int(Hkv), int(N), int(D)))
+    if r < 0:
+        raise TQError(-r, "tq_window_attention_workspace_size")
+    return r
+
+
+def tq_prefix_attention_workspace_size(Bp: int, B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
+    """Bytes of scratch tq_prefix_attention needs (on the current device)."""
+    r = int(lib().tq_prefix_attention_workspace_size(int(Bp), int(B), int(Hq), int(Hkv), int(N), int(D)))
+    if r < 0:
+        raise TQError(-r, "tq_prefix_attention_workspace_size")
+    return r
+
+
+def _attention_outputs(q, out_dtype, out, lse, workspace, need, dev):
+    """The outputs and the scratch of an attention call, allocated where not given."""
+    B, Hq, N, _ = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous [B,Hq,N,D] tensor of out_dtype on q's device")
+    if lse is None:
+        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(need(), 16), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return out, lse, workspace
+
+
+def tq_window_attention(q: torch.Tensor, cache: dict, T: int, k_bits: int, k_signed: bool, v_bits: int, window: int,
+                        sinks: int = 0, lens=None, left_pad=None, count=None, scale=None, out_dtype=torch.bfloat16,
+                        out=None, lse=None, workspace=None, stream=None):
+    """Attention of N new tokens a sequence, q [B,Hq,N,D] bf16, whose keys and
+    values are in the packed cache already: query n < count[b] sits at token p =
+    lens[b] - count[b] + n and attends to the tokens left_pad[b] <= t <= p with t >
+    p - window or t < left_pad[b] + sinks. lens, left_pad, count: int32 device
+    tensors [B] or None (T, 0, N); lens <= T. Returns (out [B,Hq,N,D] of out_dtype,
+    lse [B,Hq,N] fp32); absent queries give zeros and -inf. workspace: a uint8
+    device tensor of at least tq_window_attention_workspace_size bytes (allocated
+    when None)."""
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
+    if out_dtype not in _DTYPE:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_window_attention(q, cache, T, k_bits, k_signed, v_bits, window, sinks, lens, left_pad, count,
+                                       scale, out_dtype, out, lse, workspace)
+    B, Hq, N, D = q.shape
+    Hkv = cache["k_codes"].shape[1]
+    cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
+    out, lse, workspace = _attention_outputs(q, out_dtype, out, lse, workspace,
+                                             lambda: tq_window_attention_workspace_size(B, Hq, Hkv, N, D), dev)
+    st = lib().tq_window_attention(
+        q.data_ptr(), B, Hq, N, ctypes.byref(cv), Hkv, int(T), D, int(k_bits), int(bool(k_signed)), int(v_bits),
+        _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
+        _int_ptr(count, (B,), "count", dev), int(window), int(sinks), D ** -0.5 if scale is None else float(scale),
+        out.data_ptr(), _DTYPE[out_dtype], _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _current_stream(dev))
+    _check(st, "tq_window_attention")
+    return out, lse
+
+
+def tq_prefix_attention(q: torch.Tensor, prefix: dict, P: int, cache: dict, T: int, k_bits: int, k_signed: bool,
+                        v_bits: int, prefix_lens=None, lens=None, left_pad=None, count=None, scale=None,
+                        out_dtype=torch.bfloat16, out=None, lse=None, workspace=None, stream=None):
+    """Attention of N new tokens a sequence, q [B,Hq,N,D] bf16, over a prefix that
+    sequences share and over each sequence's own tokens. prefix: a packed cache of
+    Bp rows, B a multiple of Bp; sequences g B / Bp to (g + 1) B / Bp - 1 begin with
+    its row g, tokens [0, prefix_lens[g]) (int32 device tensor [Bp] or None: P).
+    cache: the sequences' own tokens [left_pad[b], lens[b]), the new ones included;
+    lens <= T. Query n < count[b] attends to the prefix and to its own tokens up to
+    lens[b] - count[b] + n. Returns (out, lse) as tq_window_attention. workspace: at
+    least tq_prefix_attention_workspace_size bytes (allocated when None)."""
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
+    if out_dtype not in _DTYPE:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return tq_prefix_attention(q, prefix, P, cache, T, k_bits, k_signed, v_bits, prefix_lens, lens, left_pad,
+                                       count, scale, out_dtype, out, lse, workspace)
+    B, Hq, N, D = q.shape
+    Bp, Hkv = prefix["k_codes"].shape[:2]
+    pv = _packed(prefix, Bp, Hkv, D, k_bits, v_bits, dev)
+    cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
+    out, lse, workspace = _attention_outputs(q, out_dtype, out, lse, workspace,
+                                             lambda: tq_prefix_attention_workspace_size(Bp, B, Hq, Hkv, N, D), dev)
+    st = lib().tq_prefix_attention(
+        q.data_ptr(), B, Hq, N, ctypes.byref(pv), Bp, int(P), _int_ptr(prefix_lens, (Bp,), "prefix_lens", dev),
+        ctypes.byref(cv), Hkv, int(T), D, int(k_bits), int(bool(k_signed)), int(v_bits),
+        _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
+        _int_ptr(count, (B,), "count", dev), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        _DTYPE[out_dtype], _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _current_stream(dev))
+    _check(st, "tq_prefix_attention")
+    return out, lse
 
 
 # ---- Lloyd-Max table fit (turboquant-tables.ts) -----------------------------------
