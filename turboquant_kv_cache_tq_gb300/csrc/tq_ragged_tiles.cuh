@@ -34,9 +34,10 @@ __device__ __forceinline__ int warp_prefix(int x, int lane) {
 // the range's first batch row, segment and tile and its number of tiles. CUT:
 // block 0 also writes what finds a tile's block again: cut[0] what a turn
 // counts, [1] the length of a range, [2] how many ranges have one more, from
-// kCutRows on [B + 1] the tiles of one segment a row before batch row b.
+// kCutRows on [B + 1] the tiles of one segment a row before batch row b. FULL: and
+// after them [B + 1] how many rows before batch row b have tiles.
 constexpr int kCutRows = 4;
-template <bool CUT, typename Tiles>
+template <bool CUT, bool FULL = false, typename Tiles>
 __device__ __forceinline__ void cut_line(Tiles tiles, int B, int heads, int turn_cost, int lane, volatile int* start,
                                          int* cut) {
   int sum = 0, rows = 0, n0 = 0;
@@ -45,7 +46,10 @@ __device__ __forceinline__ void cut_line(Tiles tiles, int B, int heads, int turn
     const int c = warp_prefix(n0, lane);
     if (CUT && blockIdx.x == 0 && b0 + lane < B) cut[kCutRows + b0 + lane + 1] = sum + c;
     sum += __shfl_sync(kFull, c, 31);
-    rows += __popc(__ballot_sync(kFull, n0 > 0));
+    const unsigned some = __ballot_sync(kFull, n0 > 0);
+    if (FULL && blockIdx.x == 0 && b0 + lane < B)
+      cut[kCutRows + B + 1 + b0 + lane + 1] = rows + __popc(some & (kFull >> (31 - lane)));
+    rows += __popc(some);
   }
   const unsigned all = static_cast<unsigned>(sum) * heads, ranges = max(min(all, gridDim.x), 1u);
   const int turn = min(turn_cost, static_cast<int>(all / ranges));
@@ -55,6 +59,7 @@ __device__ __forceinline__ void cut_line(Tiles tiles, int B, int heads, int turn
     cut[1] = static_cast<int>(per);
     cut[2] = static_cast<int>(more);
     cut[kCutRows] = 0;
+    if (FULL) cut[kCutRows + B + 1] = 0;
   }
   const unsigned first = blockIdx.x < ranges ? blockIdx.x * per + min(blockIdx.x, more) : line;
   const unsigned end = blockIdx.x < ranges ? first + per + (blockIdx.x < more ? 1u : 0u) : line;

@@ -2,110 +2,233 @@
 #include <cmath>
 
 #include "tq_span_attention.cuh"
+#include "tq_tree_attention.cuh"
 
 namespace tq {
+
+extern template cudaError_t launch_span_few<64, 1>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<64, 2>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<128, 1>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<128, 2>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<256, 1>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<256, 2>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<512, 1>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_few<512, 2>(SpanPass&, long long, cudaStream_t);
+extern template cudaError_t launch_span_rows<64, false>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<128, false>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<256, false>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<512, false>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<64, true>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<128, true>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<256, true>(const SpanPass&, cudaStream_t);
+extern template cudaError_t launch_span_rows<512, true>(const SpanPass&, cudaStream_t);
+
 namespace {
 
-// One block a query row: four warps, a token a step each, a lane D / 32 elements.
-template <int D>
-__global__ void __launch_bounds__(128) span_simple_kernel(const __grid_constant__ SpanParams p) {
-  constexpr int E = D / 32, NG = D / kGroup;
+// Merges the partial results of each output row's passes, divides, turns the row
+// back and stores it (see tree_combine_kernel, whose steps these are). W warps share
+// a row. A query that its sequence does not have gets zeros and -inf here, whatever
+// its rows of the passes hold.
+template <int D, int W>
+__global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(const __grid_constant__ SpanOutput p) {
+  constexpr int E = D / 32, V = E < 4 ? E : 4;
+  // head_dim 512: a pass of many rows keeps the halves of the values in records of
+  // their own, so half a warp looks at the parts of each
+  constexpr int LANES = D == 512 ? 16 : 32;
+  constexpr int AHEAD = E <= 4 ? 6 : 2;
   const float kNegInf = -__int_as_float(0x7f800000);
-  __shared__ float s_o[4][D];
-  __shared__ float s_m[4], s_l[4];
+  __shared__ float s_part[4][E + 2][32];
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x, b = row / (p.Hq * p.N), hq = row / p.N % p.Hq, n = row % p.N, h = hq / p.G;
-  const SpanRow w(p, b);
-  const int at = w.first + n;
-  const bool present = n < w.count && at >= w.lo;
-  const int kb = p.kmode == kK2 ? 2 : p.kmode == kK4 ? 4 : p.kmode == kK5 ? 5 : 8;
-  const int e0 = lane * E, g = e0 / kGroup;
-  float q[E], o[E], m = kNegInf, l = 0.0f;
-  for (int i = 0; i < E; ++i) {
-    q[i] = __uint_as_float(static_cast<uint32_t>(p.q[static_cast<long long>(row) * D + e0 + i]) << 16);
-    o[i] = 0.0f;
-  }
-  auto code = [](const uint8_t* s, int bits, int e) {
-    const int bit = e * bits;
-    uint32_t x = s[bit >> 3];
-    if ((bit & 7) + bits > 8) x |= static_cast<uint32_t>(s[(bit >> 3) + 1]) << 8;
-    return (x >> (bit & 7)) & ((1u << bits) - 1u);
-  };
-  auto half = [](uint16_t x) { return __half2float(__ushort_as_half(x)); };
-  auto tokens = [&](const PackedView& c, int cb, int from, int to) {
-    for (int t = from + warp; t < to; t += 4) {
-      const long long r = (static_cast<long long>(cb) * p.Hkv + h) * c.t_cap + t;
-      const uint8_t* kc = c.k_codes + r * (D * kb / 8);
-      const uint8_t* vc = c.v_codes + r * (D * p.vb / 8);
-      const float ks = half(c.k_scales[r * NG + g]), kz = half(c.k_zeros[r * NG + g]), vs = half(c.v_scales[r * NG + g]);
-      float s = 0.0f;
-      for (int i = 0; i < E; ++i) {
-        const uint32_t u = code(kc, kb, e0 + i);
-        const float x = p.kmode == kK8Signed ? static_cast<float>(static_cast<int8_t>(u)) : static_cast<float>(u);
-        s = __fmaf_rn(q[i], __bfloat162float(__float2bfloat16_rn(__fmul_rn(__fadd_rn(x, kz), ks))), s);
+  const int rows = p.B * p.Hq * p.N, row0 = blockIdx.x * (4 / W) + warp / W, row = min(row0, rows - 1);
+  const int b = row / (p.Hq * p.N), in_b = row - b * (p.Hq * p.N), hq = in_b / p.N, n = in_b - hq * p.N;
+  const int h = hq / p.G, g = hq - h * p.G;
+  int lo, hi;
+  row_range(p.lens, p.left_pad, b, p.T, lo, hi);
+  const int count = p.count != nullptr ? min(max(p.count[b], 0), p.N) : p.N;
+  const bool present = n < count && hi - count + n >= lo;
+  float m = kNegInf, l = 0.0f, o[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[i] = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < p.sources && present; ++k) {
+    const SpanSource& s = p.from[k];
+    const int cb = b / s.share, r = (b - cb * s.share) * s.s_step + g * s.g_step + n * s.n_step;
+    const int rb = r / s.rows, rl = r - rb * s.rows, x = cb * s.RB + rb, lines = s.lines;
+    const int half = s.halves == 1 ? 0 : lane >> 4;
+    const int hh = h * s.halves + half;
+    // the blocks that hold the segment's first and last tile
+    const int turn = s.cut[0];
+    const unsigned per = s.cut[1], more = s.cut[2];
+    const int before = s.cut[kCutRows + x], tiles = s.cut[kCutRows + x + 1] - before;
+    if (tiles == 0) continue;
+    const unsigned place = static_cast<unsigned>(before + turn * s.cut[kCutRows + lines + 1 + x]) * s.HH +
+                           static_cast<unsigned>(hh) * (tiles + turn) + turn;
+    auto block_of = [&](unsigned y) {
+      const unsigned long_part = more * (per + 1);
+      return static_cast<int>(y < long_part ? y / (per + 1) : more + (y - long_part) / per);
+    };
+    const int c0 = block_of(place), c1 = block_of(place + tiles - 1);
+    const long long slot = static_cast<long long>(c0) + static_cast<long long>(x) * s.HH + hh;
+    int parts = (c1 - c0 + 1) * s.copies;
+    if (!TQ_CHECK(slot + (c1 - c0) < s.n_recs, p.err)) parts = 0;
+    const int width = D / s.halves;
+    const long long rec_floats = static_cast<long long>(s.slots) * (width + 2);
+    const float* recs = s.recs + slot * rec_floats;
+    const int shift = s.copies - 1, at = (lane - (s.halves == 1 ? 0 : half * 16)) * E;
+    auto load = [&](int y, float (&u)[E]) {
+      const float* src = recs + (y >> shift) * rec_floats + 2 * s.slots +
+                         static_cast<long long>((y & shift) * s.rows + rl) * width + at;
+#pragma unroll
+      for (int i = 0; i < E; i += V) {
+        if constexpr (V == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + i);
+          u[i] = v.x; u[i + 1] = v.y;
+        } else {
+          const float4 v = *reinterpret_cast<const float4*>(src + i);
+          u[i] = v.x; u[i + 1] = v.y; u[i + 2] = v.z; u[i + 3] = v.w;
+        }
       }
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-      s = __fmul_rn(s, p.scale_log2);
-      const float mn = fmaxf(m, s), ref = mn == kNegInf ? 0.0f : mn;
-      const float f = exp2f(m - ref), e = exp2f(s - ref);
-      const bool bad = __any_sync(kFull, (__float_as_uint(vs) & 0x7f800000u) == 0x7f800000u);
-      l = bad ? __int_as_float(0x7fc00000) : __fmaf_rn(l, f, e);
+    };
+    int most = parts;
+    if constexpr (D == 512) most = max(parts, __shfl_xor_sync(kFull, parts, 16));
+#pragma unroll 1
+    for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
+      const int mine = s0 + (lane % LANES) * W;
+      float m2 = kNegInf, l2 = 0.0f;
+      if (mine < parts) {
+        const float* rec = recs + (mine >> shift) * rec_floats + (mine & shift) * s.rows + rl;
+        m2 = rec[0];
+        l2 = rec[s.slots];
+      }
+      // the first AHEAD results' values meanwhile
+      float u[AHEAD][E];
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y)
+        if (s0 + y * W < parts) load(s0 + y * W, u[y]);
+      float mn = m2;
+#pragma unroll
+      for (int y = LANES / 2; y > 0; y >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, y));
+      mn = fmaxf(mn, m);
+      const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
+      float add = __fmul_rn(l2, fb);
+#pragma unroll
+      for (int y = LANES / 2; y > 0; y >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, y));
+      l = __fmaf_rn(l, fa, add);
       m = mn;
-      for (int i = 0; i < E; ++i) {
-        const uint32_t u = code(vc, p.vb, e0 + i);
-        const float c0 = p.vb == 2 ? kCentroids2[u] : p.vb == 3 ? kCentroids3[u] : p.vb == 4 ? kCentroids4[u]
-                         : p.vb == 5 ? kCentroids5[u] : kCentroids8[u];
-        o[i] = __fmaf_rn(e, __bfloat162float(__float2bfloat16_rn(__fmul_rn(c0, vs))), __fmul_rn(o[i], f));
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
+      const int n_here = min(LANES, (most - s0 + W - 1) / W);
+      // (a part that saw no key is left out, whatever its values are; nor does one
+      // past the end count)
+      auto add_part = [&](int y, const float (&v)[E]) {
+        const float f = __shfl_sync(kFull, fb, (lane & ~(LANES - 1)) + y);
+        if (f != 0.0f) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(v[i], f, o[i]);
+        }
+      };
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y)
+        if (y < n_here) add_part(y, u[y]);
+#pragma unroll 4
+      for (int y = AHEAD; y < n_here; ++y) {
+        float v[E];
+        if (s0 + y * W < parts) load(s0 + y * W, v);
+        add_part(y, v);
       }
     }
-  };
-  if (present) {
-    if (p.share > 0) {
-      const int pb = b / p.share;
-      tokens(p.prefix, pb, 0, p.prefix_lens != nullptr ? min(max(p.prefix_lens[pb], 0), p.P) : p.P);
-    }
-    const int start = max(w.lo, at - p.window + 1);
-    tokens(p.cache, b, w.lo, min(w.sinks, start));
-    tokens(p.cache, b, start, at + 1);
   }
-  if (lane == 0) {
-    s_m[warp] = l != l ? 0.0f : m;
-    s_l[warp] = l;
-  }
-  for (int i = 0; i < E; ++i) s_o[warp][e0 + i] = o[i];
-  __syncthreads();
-  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float sum = 0.0f;
-  for (int x = 0; x < 4; ++x) sum += s_m[x] == kNegInf ? 0.0f : s_l[x] * exp2f(s_m[x] - top);
-  const bool empty = sum == 0.0f;
-  for (int e = threadIdx.x; e < D; e += 128) {
-    float x = 0.0f;
-    for (int y = 0; y < 4; ++y) x += s_m[y] == kNegInf ? 0.0f : s_o[y][e] * exp2f(s_m[y] - top);
-    s_o[0][e] = empty ? 0.0f : x / sum;
-  }
-  __syncthreads();
-  for (int s = 1; s < D; s <<= 1) {
-    for (int i = threadIdx.x; i < D / 2; i += 128) {
-      const int a = (i & ~(s - 1)) * 2 + (i & (s - 1));
-      const float x = s_o[0][a], y = s_o[0][a + s];
-      s_o[0][a] = x + y;
-      s_o[0][a + s] = x - y;
-    }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) s_part[warp][i][lane] = o[i];
+    s_part[warp][E][lane] = l;
+    s_part[warp][E + 1][lane] = m;
     __syncthreads();
+    if (warp % W != 0) return;
+#pragma unroll 1
+    for (int x = 1; x < W; ++x) {
+      const float m2 = s_part[warp + x][E + 1][lane], l2 = s_part[warp + x][E][lane], mn = fmaxf(m, m2);
+      const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
+      l = __fmaf_rn(l2, fb, __fmul_rn(l, fa));
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(s_part[warp + x][i][lane], fb, __fmul_rn(o[i], fa));
+      m = mn;
+    }
   }
-  const uint8_t* neg = D == 64 ? kSignNeg64 : D == 128 ? kSignNeg128 : D == 256 ? kSignNeg256 : kSignNeg512;
-  for (int e = threadIdx.x; e < D; e += 128) {
-    float x = s_o[0][e] * p.rot_scale;
-    if (neg[e >> 3] >> (e & 7) & 1) x = -x;
-    if (p.out_f32) static_cast<float*>(p.out)[static_cast<long long>(row) * D + e] = x;
-    else static_cast<__nv_bfloat16*>(p.out)[static_cast<long long>(row) * D + e] = __float2bfloat16_rn(x);
+  if constexpr (D == 512) {  // a value group may have spoiled one half's sum: the row's lse is NaN then
+    const float other = __shfl_xor_sync(kFull, l, 16);
+    if (other != other) l = other;
   }
-  if (p.lse != nullptr && threadIdx.x == 0) p.lse[row] = empty ? kNegInf : (top + log2f(sum)) * 0.693147180559945309f;
+  finish_row<D>(o, m, l, row, row0 < rows, p.out, p.out_f32, p.lse, p.rot_scale, lane);
 }
 
-cudaError_t launch_plain(void (*kernel)(const SpanParams), int grid, const SpanParams& p, cudaStream_t s) {
-  kernel<<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+// How the query rows of a pass are laid out, and the scratch that follows.
+struct SpanPlan {
+  long long R, RB, rows, copies, slots, HH, lines, n_recs, rec_floats, cut_bytes, bytes;
+  int TT, halves;
+  bool few;
+};
+
+// The most query rows a kv head for which the decode in registers is taken.
+constexpr int kFewRows = kAttnRows;
+
+// B rows of the cache, `rows` query rows a kv head in each, at most T tokens. (Short
+// sequences and fp32 outputs need no more scratch than long ones and bf16.)
+bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool f32, SpanPlan* t) {
+  const long long lim = 0x7fffffffLL;
+  t->few = rows <= kFewRows;
+  t->R = rows;
+  t->halves = !t->few && D == 512 ? 2 : 1;
+  t->HH = Hkv * t->halves;
+  if (t->few) {
+    t->TT = kAttnTile;
+    t->RB = t->copies = 1;
+    t->rows = t->slots = kAttnRows;
+  } else {
+    auto tile = [&](auto f) {
+      constexpr bool F = decltype(f)::value;
+      return D == 64 ? TreeShape<64, F>::TT : D == 128 ? TreeShape<128, F>::TT : D == 256 ? TreeShape<256, F>::TT
+                                                                               : TreeShape<512, F>::TT;
+    };
+    t->TT = f32 ? tile(std::true_type{}) : tile(std::false_type{});
+    t->RB = (rows + kTreeRows - 1) / kTreeRows;
+    t->rows = (rows + t->RB - 1) / t->RB;
+  }
+  if (t->RB > lim / t->HH || (B > 0 && t->RB * t->HH > lim / B)) return false;
+  t->lines = B * t->RB;
+  if (!t->few) {
+    // (two lanes a row as in the tree attention, and where its rule takes them)
+    t->copies = f32 || t->rows > 64 || t->TT == 32 || t->lines * t->HH < 16LL * sm_count() / (T / t->TT + 2) ? 1 : 2;
+    t->slots = (t->copies * t->rows + 3) / 4 * 4;
+  }
+  t->n_recs = (t->few ? kAttnGridPerSm : 1) * sm_count() + t->lines * t->HH;
+  t->rec_floats = t->slots * (D / t->halves + 2);
+  t->cut_bytes = ((kCutRows + 2 * (t->lines + 1)) * 4 + 255) / 256 * 256;
+  t->bytes = t->cut_bytes + t->n_recs * t->rec_floats * 4;
+  return true;
+}
+
+// The passes (the prefix first), then the combine kernel.
+template <int D>
+cudaError_t launch_span(SpanPass* passes, const SpanPlan* plans, int64_t reach, int64_t P, const SpanOutput& o, cudaStream_t s) {
+  long long parts = 0;  // partial results of a row, about
+  for (int k = o.sources - 1; k >= 0; --k) {
+    SpanPass& p = passes[k];
+    const SpanPlan& t = plans[k];
+    cudaError_t e;
+    const long long tiles = t.lines * t.HH * ((k ? P : reach) / t.TT + 2);
+    if (t.few) e = p.R <= 8 ? launch_span_few<D, 1>(p, tiles, s) : launch_span_few<D, 2>(p, tiles, s);
+    else if (o.out_f32) e = launch_span_rows<D, true>(p, s);
+    else e = launch_span_rows<D, false>(p, s);
+    if (e != cudaSuccess) return e;
+    parts = std::max(parts, (p.grid / (t.lines * t.HH) + 1) * t.copies);
+  }
+  // (the rule of the tree attention's combine kernel)
+  const long long rows = static_cast<long long>(o.B) * o.Hq * o.N;
+  if (parts >= 8) return launch_pdl_block(span_combine_kernel<D, 4>, static_cast<int>(rows), 128, o, s, 0);
+  return launch_pdl_block(span_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, o, s, 0);
 }
 
 constexpr int64_t kSpanMostRows = 1 << 20;  // query rows of a kv head
@@ -176,39 +299,126 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
                      {count, B * 4},
                      {prefix_lens, Bp * 4}}))
     return TQ_ERR_INVALID_ARG;
-  SpanParams p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.cache = view(cache);
-  p.prefix = view(pre);
-  p.lens = lens;
-  p.left_pad = left_pad;
-  p.count = count;
-  p.prefix_lens = prefix_lens;
-  p.out = out;
-  p.lse = lse;
-  p.err = device_error_word();
-  p.B = static_cast<int>(B);
-  p.Hq = static_cast<int>(Hq);
-  p.Hkv = static_cast<int>(Hkv);
-  p.G = static_cast<int>(Hq / Hkv);
-  p.N = static_cast<int>(N);
-  p.T = static_cast<int>(T);
-  p.share = Bp > 0 ? static_cast<int>(B / Bp) : 0;
-  p.P = static_cast<int>(P);
-  p.window = static_cast<int>(window < kRaggedMostTokens ? window : kRaggedMostTokens);
-  p.sinks = static_cast<int>(sinks < T ? sinks : T);
-  p.kmode = kmode;
-  p.vb = v_bits;
-  p.out_f32 = out_dtype == TQ_F32;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.rot_scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  // the passes: over the sequences' own tokens, over the prefix
+  const bool f32 = out_dtype == TQ_F32;
+  const int64_t G = Hq / Hkv, share = prefix ? B / Bp : 1;
+  // tokens of a sequence that any new one may see, by which tiles are counted (a
+  // block of rows sees a window and what its tokens add to it)
+  const int64_t reach = window < T ? window + sinks + N + 64 < T ? window + sinks + N + 64 : T : T;
+  SpanPlan plans[2];
+  span_plan(B, Hkv, G * N, D, reach, f32, &plans[0]);
+  if (prefix) span_plan(Bp, Hkv, share * G * N, D, P, f32, &plans[1]);
+  SpanPass passes[2]{};
+  SpanOutput o{};
+  char* scratch = static_cast<char*>(workspace);
+  for (int k = 0; k < (prefix ? 2 : 1); ++k) {
+    const SpanPlan& t = plans[k];
+    SpanPass& p = passes[k];
+    const int64_t rows_of = k ? Bp : B, tokens = k ? P : T;
+    // tiles in all (and what the turns count for) are counted in 32 bits
+    if ((k ? P : reach) / t.TT + 32 > 0x7fffffffLL / (t.lines * t.HH)) return TQ_ERR_INVALID_ARG;
+    p.q = static_cast<const uint16_t*>(q);
+    p.cache = view(k ? prefix : cache);
+    p.lens = k ? prefix_lens : lens;
+    p.left_pad = left_pad;
+    p.count = count;
+    p.cut = reinterpret_cast<int*>(scratch);
+    p.recs = reinterpret_cast<float*>(scratch + t.cut_bytes);
+    scratch += t.bytes;
+    p.err = device_error_word();
+    p.n_recs = t.n_recs;
+    p.B = static_cast<int>(rows_of);
+    p.Hq = static_cast<int>(Hq);
+    p.Hkv = static_cast<int>(Hkv);
+    p.G = static_cast<int>(G);
+    p.N = static_cast<int>(N);
+    p.T = static_cast<int>(tokens);
+    p.share = k ? static_cast<int>(share) : 0;
+    p.window = static_cast<int>(window < kRaggedMostTokens ? window : kRaggedMostTokens);
+    p.sinks = static_cast<int>(sinks < T ? sinks : T);
+    p.R = static_cast<int>(t.R);
+    SpanSource& s = o.from[k];
+    if (k) {  // sequence after sequence, as they lie in memory
+      p.in = static_cast<int>(G * N);
+      p.in_step = 1;
+      p.out_step = static_cast<int>(Hq * N);
+      s.share = p.share;
+      s.s_step = p.in;
+      s.g_step = p.N;
+      s.n_step = 1;
+    } else if (t.few) {  // head after head, as they lie in memory
+      p.in = p.R;
+      p.in_step = 1;
+      s.share = 1;
+      s.g_step = p.N;
+      s.n_step = 1;
+    } else {  // token after token, so that a block of rows sees few tokens
+      p.in = p.G;
+      p.in_step = p.N;
+      p.out_step = 1;
+      s.share = 1;
+      s.g_step = 1;
+      s.n_step = p.G;
+    }
+    p.RB = static_cast<int>(t.RB);
+    p.rows = static_cast<int>(t.rows);
+    p.copies = static_cast<int>(t.copies);
+    p.slots = static_cast<int>(t.slots);
+    p.HH = static_cast<int>(t.HH);
+    p.kmode = kmode;
+    p.vb = v_bits;
+    p.out_f32 = f32;
+    p.x_keys = static_cast<int>(xk);
+    p.x_values = static_cast<int>(xv);
+    p.vtab_stride = 128;
+    const tq_packed_cache* c = k ? prefix : cache;
+    if (t.few) {
+      p.bulk = c->t_cap % kAttnTile == 0;
+      p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    } else {
+      p.bulk = c->t_cap * xs % 16 == 0 && c->t_cap * xk % 16 == 0 && c->t_cap * xv % 16 == 0 &&
+               ragged_device_memory({c->k_codes, c->k_scales, c->k_zeros, c->v_codes, c->v_scales});
+      // The sign goes into the matrix instruction, so that the largest score has
+      // the largest weight. A scale of zero must keep masked scores at -inf.
+      const float by = static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
+      p.scale_log2 = by == 0.0f ? 1e-30f : by;
+      p.negate = scale < 0.0f;
+      // one range of tiles per SM (a block holds all of an SM's tensor memory)
+      const long long tiles = t.lines * t.HH * ((k ? P : reach) / t.TT + 3), sms = sm_count();
+      p.grid = static_cast<int>(tiles < sms ? tiles : sms);
+    }
+    s.cut = p.cut;
+    s.recs = p.recs;
+    s.n_recs = p.n_recs;
+    s.rows = p.rows;
+    s.RB = p.RB;
+    s.lines = static_cast<int>(t.lines);
+    s.HH = p.HH;
+    s.halves = t.halves;
+    s.slots = p.slots;
+    s.copies = p.copies;
+  }
+  o.lens = lens;
+  o.left_pad = left_pad;
+  o.count = count;
+  o.out = out;
+  o.lse = lse;
+  o.err = passes[0].err;
+  o.B = static_cast<int>(B);
+  o.Hq = static_cast<int>(Hq);
+  o.Hkv = static_cast<int>(Hkv);
+  o.G = static_cast<int>(G);
+  o.N = static_cast<int>(N);
+  o.T = static_cast<int>(T);
+  o.sources = prefix ? 2 : 1;
+  o.out_f32 = f32;
+  o.rot_scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = static_cast<int>(rows);
   switch (D) {
-    case 64: return launch_status(launch_plain(span_simple_kernel<64>, grid, p, s));
-    case 128: return launch_status(launch_plain(span_simple_kernel<128>, grid, p, s));
-    case 256: return launch_status(launch_plain(span_simple_kernel<256>, grid, p, s));
-    default: return launch_status(launch_plain(span_simple_kernel<512>, grid, p, s));
+    case 64: return launch_status(launch_span<64>(passes, plans, reach, P, o, s));
+    case 128: return launch_status(launch_span<128>(passes, plans, reach, P, o, s));
+    case 256: return launch_status(launch_span<256>(passes, plans, reach, P, o, s));
+    default: return launch_status(launch_span<512>(passes, plans, reach, P, o, s));
   }
 }
 
@@ -219,13 +429,22 @@ using namespace tq;
 
 extern "C" int64_t tq_window_attention_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
   const tq_status st = span_sizes(B, Hq, Hkv, N, D, 1);
-  return st == TQ_OK ? 16 : -static_cast<int64_t>(st);
+  if (st != TQ_OK) return -static_cast<int64_t>(st);
+  SpanPlan t;
+  if (!span_plan(B, Hkv, Hq / Hkv * N, D, 1LL << 40, false, &t)) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
+  return t.bytes;
 }
 
 extern "C" int64_t tq_prefix_attention_workspace_size(int64_t Bp, int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
   if (Bp < 1 || B < 0 || B % Bp != 0) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
-  const tq_status st = span_sizes(B, Hq, Hkv, N, D, B > 0 ? B / Bp : 1);
-  return st == TQ_OK ? 16 : -static_cast<int64_t>(st);
+  const int64_t share = B > 0 ? B / Bp : 1;
+  const tq_status st = span_sizes(B, Hq, Hkv, N, D, share);
+  if (st != TQ_OK) return -static_cast<int64_t>(st);
+  SpanPlan own, pre;
+  if (!span_plan(B, Hkv, Hq / Hkv * N, D, 1LL << 40, false, &own) ||
+      !span_plan(Bp, Hkv, share * (Hq / Hkv) * N, D, 1LL << 40, false, &pre))
+    return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
+  return own.bytes + pre.bytes;
 }
 
 extern "C" tq_status tq_window_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const tq_packed_cache* cache,

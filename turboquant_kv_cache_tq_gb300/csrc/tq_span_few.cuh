@@ -1,0 +1,536 @@
+// A pass with at most 16 query rows a kv head: a token or two of each sequence.
+//
+// The decode of the packed bytes is the work: a tile of 16 tokens goes from the
+// bytes into the operands of mma.sync (m16n8k16: tokens x query rows) within the
+// lane that decoded it, as in tq_decode_attention, whose layouts, tables and decoding
+// steps these are; tcgen05 would need every decoded element written to shared
+// memory first (see span_rows_kernel, which has many rows a decoded
+// element). What differs: the tiles of a ragged batch, of a window and of its
+// first tokens form one line that every block cuts alike from the lengths on the
+// device (cut_line); which tokens a row sees goes by the row; fp32 outputs take
+// their weights in three bf16 parts; a value group with an infinite or NaN scale is
+// decoded as zeros and spoils the rows that see it, and no other; a capacity that
+// is not a multiple of 16 tokens is read in narrower pieces.
+#pragma once
+
+#include "tq_span_attention.cuh"
+
+namespace tq {
+
+template <int D, int VB, int KMODE, int NT>
+__global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB, NT>::MIN_BLOCKS)
+    span_few_kernel(const __grid_constant__ SpanPass p) {
+  using M = KeySpec<KMODE>;
+  constexpr int KB = M::B;
+  using SM = AttnSmem<D, KB, VB, NT>;
+  using L = typename SM::L;  // the per-warp layout over DH head_dim elements
+  constexpr int SPL = SM::SPL, DH = AttnSplit<D>::DH;
+  constexpr int PDK = D * KB / 8, PDV = D * VB / 8, NG = D / kGroup;
+  using VT = ValueTable<VB>;
+  constexpr int S = SM::S, NW = SM::NW, TEAMS = NW / SPL;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  uint8_t* s_vtab = few_smem;
+  float* s_xchg = reinterpret_cast<float*>(few_smem + SM::XOFF);
+  uint8_t* s_work = few_smem + SM::WORK;
+  volatile int* s_start = reinterpret_cast<volatile int*>(few_smem + SM::SMEM);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int team = warp / SPL;  // warps sharing a tile
+  const int half = warp % SPL;  // the head_dim slice of this warp
+
+  fill_value_table<VB>(s_vtab);
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 0)
+    cut_line<true, true>([&](int b) { return SpanTiles<kAttnTile>(p, b, 0, p.R).count(); }, p.B, p.HH, kFewTurn, lane,
+                         s_start, p.cut);
+  __syncthreads();
+  int b = s_start[0], h = s_start[1], tile_lo = s_start[2], left = s_start[3];
+
+  uint8_t* ring = s_work + warp * S * L::STAGE;
+  const uint32_t ring_sh = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const uint32_t vlane = VT::PAIRS ? 8u * (lane & 15) : 4u * lane;  // the lane's table replica
+  const uint32_t vstride = p.vtab_stride;
+  constexpr float kBias = kMagic + (M::SIGNED ? 128.0f : 0.0f);
+  constexpr float kBias16 = 1024.0f + (M::SIGNED ? 128.0f : 0.0f);
+
+  while (left > 0 && b < p.B) {
+    const SpanTiles<kAttnTile> w(p, b, 0, p.R);
+    const int n_tiles = min(left, w.count() - tile_lo);
+    if (n_tiles <= 0) {  // (a row without tiles)
+      h = 0;
+      ++b;
+      continue;
+    }
+    __syncthreads();  // the previous segment's merge area is free again
+
+    // Query operands of the score MMAs, kept in registers: query row 8 n + g,
+    // head_dim elements c DH/4 + 4 j .. + 3 for k-step j (the contraction's
+    // permuted order, see attn_split_kernel). Padding rows are zero.
+    uint32_t qf[DH / 16][NT][2];
+    {
+      const uint16_t* qsrc = p.queries(b, h, D) + half * DH;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = 8 * n + g;
+        const long long at = p.query(row) * D + c * L::EK;
+#pragma unroll
+        for (int j = 0; j < DH / 16; ++j) {
+          uint2 u = make_uint2(0u, 0u);
+          if (row < p.R) u = *reinterpret_cast<const uint2*>(qsrc + at + 4 * j);
+          qf[j][n][0] = u.x;
+          qf[j][n][1] = u.y;
+        }
+      }
+    }
+    // the token that the lane's query columns 8 n + 2 c + x sit at
+    int at[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) at[n][x] = w.at(p, min(8 * n + 2 * c + x, p.R - 1));
+
+    const long long row0 = (static_cast<long long>(b) * p.Hkv + h) * p.cache.t_cap;
+    const int my_tiles = n_tiles > team ? (n_tiles - team + TEAMS - 1) / TEAMS : 0;
+    // Step k of this warp handles tile team + TEAMS k in stage k mod S (its
+    // slice of each row when SPL > 1); every step commits one copy group
+    // (empty past the end).
+    auto issue = [&](int k) {
+      if (k < my_tiles) {
+        const int t0 = w.token(tile_lo + team + k * TEAMS);
+        const long long t = row0 + t0;
+        const uint32_t dst = ring_sh + (k % S) * L::STAGE;
+        if (p.bulk) {  // (the tile lies inside the capacity, and every row of it on 16 bytes)
+          if (!TQ_CHECK(t0 >= 0 && t0 + kAttnTile <= p.cache.t_cap, p.err)) return;
+          if constexpr (SPL == 1) {
+            copy_region<kAttnTile * PDK>(dst + L::KC, p.cache.k_codes + t * PDK, lane);
+            copy_region<kAttnTile * PDV>(dst + L::VC, p.cache.v_codes + t * PDV, lane);
+          } else {
+            copy_rows<kAttnTile, L::PDK, PDK>(dst + L::KC, p.cache.k_codes + t * PDK + half * L::PDK, lane);
+            copy_rows<kAttnTile, L::PDV, PDV>(dst + L::VC, p.cache.v_codes + t * PDV + half * L::PDV, lane);
+          }
+          copy_region<kAttnTile * NG * 2>(dst + L::KS, p.cache.k_scales + t * NG, lane);
+          copy_region<kAttnTile * NG * 2>(dst + L::KZ, p.cache.k_zeros + t * NG, lane);
+          copy_region<kAttnTile * NG * 2>(dst + L::VS, p.cache.v_scales + t * NG, lane);
+        } else {
+          int n = static_cast<int>(min(static_cast<long long>(kAttnTile), p.cache.t_cap - t0));
+          if (!TQ_CHECK(t0 >= 0 && t0 < p.cache.t_cap, p.err)) n = 0;
+#pragma unroll 1
+          for (int i = 0; i < 5; ++i) {
+            const bool code = i < 2;
+            const uint8_t* from = i == 0   ? p.cache.k_codes
+                                  : i == 1 ? p.cache.v_codes
+                                           : reinterpret_cast<const uint8_t*>(i == 2   ? p.cache.k_scales
+                                                                              : i == 3 ? p.cache.k_zeros
+                                                                                       : p.cache.v_scales);
+            const int pitch = i == 0 ? PDK : i == 1 ? PDV : 2 * NG, x = code ? pitch / SPL : pitch;
+            const int to = i == 0 ? L::KC : i == 1 ? L::VC : i == 2 ? L::KS : i == 3 ? L::KZ : L::VS;
+            copy_rows_any(dst + to, from + t * pitch + (code ? half * x : 0), pitch, x, n, lane);
+          }
+        }
+      }
+    };
+
+    float acc[DH / 16][NT][4];
+#pragma unroll
+    for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
+    float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m_run[n][x] = kNegInf;
+        l_run[n][x] = 0.0f;
+      }
+
+    // (the first turns only fill the ring)
+#pragma unroll 1
+    for (int k = 1 - S; k < my_tiles; ++k) {
+      __syncwarp();
+      issue(k + S - 1);
+      cp_async_commit();
+      if (k < 0) continue;
+      cp_async_wait<S - 1>();
+      __syncwarp();
+      const uint8_t* st = ring + (k % S) * L::STAGE;
+      const int t0 = w.token(tile_lo + team + k * TEAMS);
+      const bool whole = w.whole(p, t0);  // a tile that every row sees needs no mask (warp-uniform)
+
+      // ---- keys: tokens g and g + 8, elements [c EK, (c+1) EK)
+      uint32_t wk[2][L::NWK];
+      float2 ks2[2][L::KGROUPS], kzb2[2][L::KGROUPS];
+      float kzh[2][L::KGROUPS];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int tau = g + 8 * hf;
+        lds_words<L::NWK, L::KALIGN>(st + L::KC + tau * L::PDK, c * (L::EK * KB / 8), wk[hf]);
+        if constexpr (M::SIGNED) {
+#pragma unroll
+          for (int i = 0; i < L::NWK; ++i) wk[hf][i] ^= 0x80808080u;  // code + 128 in each byte
+        }
+#pragma unroll
+        for (int lg = 0; lg < L::KGROUPS; ++lg) {
+          const int grp = (c * L::EK) / kGroup + lg;
+          const uint16_t* sc = reinterpret_cast<const uint16_t*>(st + L::KS);
+          const uint16_t* zr = reinterpret_cast<const uint16_t*>(st + L::KZ);
+          ks2[hf][lg] = f2(__half2float(__ushort_as_half(sc[tau * NG + half * L::NG + grp])));
+          const float zp = __half2float(__ushort_as_half(zr[tau * NG + half * L::NG + grp]));
+          kzb2[hf][lg] = f2(__fsub_rn(zp, kBias));
+          kzh[hf][lg] = __fsub_rn(zp, kBias16);
+        }
+      }
+      // scores S^T = K Q^T: M = the tile's 16 tokens, N = 8 query rows per row
+      // tile n, K = 16 head_dim elements per k-step; two accumulator chains
+      float sacc[NT][2][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sacc[n][ch][e] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DH / 16; ++j) {
+        const int lg = (4 * j) / kGroup;
+        uint32_t af[2][2];  // [token g / g + 8][elements 0-1 / 2-3]
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          // RN(code + zero) in one rounding, RN(. * scale), bf16 (see attn_split_kernel)
+          float2 f01, f23;
+          if constexpr (KB == 8) {
+            const uint32_t u = wk[hf][j];
+            const uint32_t h01 = __byte_perm(u, 0x64646464u, 0x4140);
+            const uint32_t h23 = __byte_perm(u, 0x64646464u, 0x4342);
+            f01 = make_float2(add_f16_f32<false>(h01, kzh[hf][lg]), add_f16_f32<true>(h01, kzh[hf][lg]));
+            f23 = make_float2(add_f16_f32<false>(h23, kzh[hf][lg]), add_f16_f32<true>(h23, kzh[hf][lg]));
+          } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = kMagicBits | code_at<KB>(wk[hf], 4 * j + e);
+            f01 = add2(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), kzb2[hf][lg]);
+            f23 = add2(make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), kzb2[hf][lg]);
+          }
+          const float2 x01 = mul2(f01, ks2[hf][lg]);
+          const float2 x23 = mul2(f23, ks2[hf][lg]);
+          af[hf][0] = pack_bf16x2(x01.x, x01.y);
+          af[hf][1] = pack_bf16x2(x23.x, x23.y);
+        }
+        const uint32_t a[4] = {af[0][0], af[1][0], af[0][1], af[1][1]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_bf16_16816(sacc[n][j & 1], a, qf[j][n][0], qf[j][n][1]);
+      }
+
+      // ---- values: tokens 2c, 2c + 1, 2c + 8, 2c + 9, elements [g EV, (g+1) EV):
+      // packed words and scales loaded ahead of the softmax
+      uint32_t wv[4][L::NWV];
+      uint32_t vs[4];
+      uint32_t most = 0;
+#pragma unroll
+      for (int k4 = 0; k4 < 4; ++k4) {
+        const int tau = 2 * c + (k4 & 1) + 8 * (k4 >> 1);
+        lds_words<L::NWV, L::VALIGN>(st + L::VC + tau * L::PDV, g * (L::EV * VB / 8), wv[k4]);
+        const uint16_t* sv = reinterpret_cast<const uint16_t*>(st + L::VS);
+        vs[k4] = sv[tau * NG + half * L::NG + (g * L::EV) / kGroup];
+        // tokens outside the sequence contribute exactly zero
+        if (!whole && (t0 + tau < w.lo || t0 + tau >= w.hi)) vs[k4] = 0;
+        most = max(most, vs[k4] & 0x7fffu);
+      }
+      // ---- the team's partial scores added (SPL > 1): each warp publishes
+      // its slice's sums in slot k mod 2 and adds all SPL slices in order
+      // (the same terms in the same order in every warp, so the same sums)
+      float sfull[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sfull[n][e] = __fadd_rn(sacc[n][0][e], sacc[n][1][e]);
+      if constexpr (SPL > 1) {
+        float* slot = s_xchg + (k & 1) * (NW * 32 * NT * 4);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) slot[((warp * NT + n) * 4 + e) * 32 + lane] = sfull[n][e];
+        named_barrier(1 + team, 32 * SPL);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float tot = 0.0f;
+#pragma unroll
+            for (int x = 0; x < SPL; ++x) {
+              const float o = x == half ? sfull[n][e] : slot[(((team * SPL + x) * NT + n) * 4 + e) * 32 + lane];
+              tot = x == 0 ? o : __fadd_rn(tot, o);
+            }
+            sfull[n][e] = tot;
+          }
+      }
+
+      // ---- online softmax per query column 8 n + 2 c + x (tokens g, g + 8
+      // in entries x and 2 + x); the column's values sit in the eight lanes
+      // with the same c
+      float pr[NT][4];
+      float al[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float xs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          xs[e] = __fmul_rn(sfull[n][e], p.scale_log2);
+          if (!whole && !w.sees(p, at[n][e & 1], t0 + g + 8 * (e >> 1))) xs[e] = kNegInf;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mt = fmaxf(xs[x], xs[2 + x]);
+          mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
+          mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
+          mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
+          const float mn = fmaxf(m_run[n][x], mt);
+          const float mu = mn == kNegInf ? 0.0f : mn;
+          al[n][x] = fast_exp2(__fsub_rn(m_run[n][x], mu));
+          m_run[n][x] = mn;
+          pr[n][x] = fast_exp2(__fsub_rn(xs[x], mu));
+          pr[n][2 + x] = fast_exp2(__fsub_rn(xs[2 + x], mu));
+          l_run[n][x] = __fadd_rn(__fmul_rn(l_run[n][x], al[n][x]), __fadd_rn(pr[n][x], pr[n][2 + x]));
+        }
+      }
+      // a value group with an infinite or NaN scale: its row is NaN where it is seen
+      if (__any_sync(kFull, most >= 0x7c00u)) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+          if ((vs[k4] & 0x7c00u) == 0x7c00u) {
+            bad |= 1u << (2 * c + (k4 & 1) + 8 * (k4 >> 1));
+            vs[k4] = 0;
+          }
+        bad = __reduce_or_sync(kFull, bad);
+#pragma unroll 1
+        for (int t = 0; t < kAttnTile; ++t)
+          if (bad >> t & 1) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                if (w.sees(p, at[n][x], t0 + t)) l_run[n][x] = __int_as_float(0x7fc00000);
+          }
+      }
+      // rescale O^T: its columns are this lane's query columns 2 c, 2 c + 1
+      {
+        bool change = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) change = change || al[n][0] != 1.0f || al[n][1] != 1.0f;
+        if (__any_sync(kFull, change)) {
+#pragma unroll
+          for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              acc[i][n][0] = __fmul_rn(acc[i][n][0], al[n][0]);
+              acc[i][n][1] = __fmul_rn(acc[i][n][1], al[n][1]);
+              acc[i][n][2] = __fmul_rn(acc[i][n][2], al[n][0]);
+              acc[i][n][3] = __fmul_rn(acc[i][n][3], al[n][1]);
+            }
+        }
+      }
+      // P^T operands (k = token, n = query row): the weights of tokens g and
+      // g + 8 for query columns 2 c, 2 c + 1, split into bf16 parts (two are
+      // exact to 2^-18, the three of an fp32 output to 2^-27), then
+      // transposed 8x8 by 8x8
+      uint32_t b0[NT][2], b1[NT][2], b2[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float x0 = pr[n][2 * hf], x1 = pr[n][2 * hf + 1];
+          const uint32_t hi = pack_bf16x2(x0, x1);
+          const float y0 = __fsub_rn(x0, bf16_lo(hi)), y1 = __fsub_rn(x1, bf16_hi(hi));
+          const uint32_t lo = pack_bf16x2(y0, y1);
+          b0[n][hf] = movmatrix_trans(hi);
+          b1[n][hf] = movmatrix_trans(lo);
+          b2[n][hf] = 0;
+          if (p.out_f32)
+            b2[n][hf] = movmatrix_trans(pack_bf16x2(__fsub_rn(y0, bf16_lo(lo)), __fsub_rn(y1, bf16_hi(lo))));
+        }
+      float2 vs2[4];
+#pragma unroll
+      for (int k4 = 0; k4 < 4; ++k4) vs2[k4] = f2(__half2float(__ushort_as_half(static_cast<unsigned short>(vs[k4]))));
+
+#pragma unroll
+      for (int i = 0; i < DH / 16; ++i) {
+        // elements 2i, 2i + 1 of each token: RN(centroid * scale), to bf16
+        float2 v[4];
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          float2 cc;
+          if constexpr (VB == 4) {
+            cc = *reinterpret_cast<const float2*>(s_vtab + byte_field_addr(wv[k4], i, vstride, vlane));
+          } else if constexpr (VB == 8) {
+            cc = make_float2(*reinterpret_cast<const float*>(s_vtab + byte_field_addr(wv[k4], 2 * i, vstride, vlane)),
+                             *reinterpret_cast<const float*>(s_vtab + byte_field_addr(wv[k4], 2 * i + 1, vstride, vlane)));
+          } else if constexpr (VT::PAIRS) {
+            cc = *reinterpret_cast<const float2*>(s_vtab + field_addr<2 * VB, 7>(wv[k4], 2 * i * VB, vlane));
+          } else {
+            cc = make_float2(*reinterpret_cast<const float*>(s_vtab + field_addr<VB, 7>(wv[k4], 2 * i * VB, vlane)),
+                             *reinterpret_cast<const float*>(s_vtab + field_addr<VB, 7>(wv[k4], (2 * i + 1) * VB, vlane)));
+          }
+          v[k4] = mul2(cc, vs2[k4]);
+        }
+        const uint32_t a[4] = {pack_bf16x2(v[0].x, v[1].x), pack_bf16x2(v[0].y, v[1].y),
+                               pack_bf16x2(v[2].x, v[3].x), pack_bf16x2(v[2].y, v[3].y)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_bf16_16816(acc[i][n], a, b0[n][0], b0[n][1]);
+          mma_bf16_16816(acc[i][n], a, b1[n][0], b1[n][1]);
+          if (p.out_f32) mma_bf16_16816(acc[i][n], a, b2[n][0], b2[n][1]);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    // column sums over the eight lanes of a column
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l_run[n][x] = __fadd_rn(l_run[n][x], __shfl_xor_sync(kFull, l_run[n][x], 4));
+        l_run[n][x] = __fadd_rn(l_run[n][x], __shfl_xor_sync(kFull, l_run[n][x], 8));
+        l_run[n][x] = __fadd_rn(l_run[n][x], __shfl_xor_sync(kFull, l_run[n][x], 16));
+      }
+
+    // ---- merge the teams in shared memory, one record per block (the
+    // warps of a team share m and l and each holds its half of O)
+    __syncthreads();  // every warp is done with its ring
+    float* mine = reinterpret_cast<float*>(s_work) + team * SM::REC;
+    if (g == 0 && half == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mine[8 * n + 2 * c + x] = m_run[n][x];
+          mine[16 + 8 * n + 2 * c + x] = l_run[n][x];
+        }
+    }
+    {
+      float* O = mine + 32 + half * DH;
+#pragma unroll
+      for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int q0 = 8 * n + 2 * c, d0 = g * L::EV + 2 * i;
+          O[q0 * D + d0] = acc[i][n][0];
+          O[(q0 + 1) * D + d0] = acc[i][n][1];
+          O[q0 * D + d0 + 1] = acc[i][n][2];
+          O[(q0 + 1) * D + d0 + 1] = acc[i][n][3];
+        }
+    }
+    if constexpr (SPL > 1) {  // a value group that spoils a row may lie in the other slice
+      __syncthreads();
+      if (g == 0 && half != 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (l_run[n][x] != l_run[n][x]) mine[16 + 8 * n + 2 * c + x] = l_run[n][x];
+      }
+    }
+    __syncthreads();
+    // (a NaN row counts with a finite maximum, so that every merge takes it)
+    const float* all = reinterpret_cast<const float*>(s_work);
+    auto top = [&](int x, int r) {
+      const float m = all[x * SM::REC + r], l = all[x * SM::REC + 16 + r];
+      return l != l && m == kNegInf ? 0.0f : m;
+    };
+    const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(b) * p.HH + h;
+    if (TQ_CHECK(slot < p.n_recs, p.err)) {
+      float* rec = p.recs + slot * SM::REC;
+      for (int i = threadIdx.x; i < p.R * D; i += blockDim.x) {
+        const int r = i / D;
+        float mx = kNegInf;
+#pragma unroll
+        for (int x = 0; x < TEAMS; ++x) mx = fmaxf(mx, top(x, r));
+        float sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < TEAMS; ++x) {
+          const float mw = top(x, r);
+          if (mw != kNegInf) sum = __fadd_rn(sum, __fmul_rn(exp2f(__fsub_rn(mw, mx)), all[x * SM::REC + 32 + i]));
+        }
+        rec[32 + i] = sum;
+      }
+      for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
+        float mx = kNegInf;
+#pragma unroll
+        for (int x = 0; x < TEAMS; ++x) mx = fmaxf(mx, top(x, r));
+        float l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < TEAMS; ++x) {
+          const float mw = top(x, r);
+          if (mw != kNegInf) l = __fadd_rn(l, __fmul_rn(exp2f(__fsub_rn(mw, mx)), all[x * SM::REC + 16 + r]));
+        }
+        rec[r] = mx;
+        rec[16 + r] = l;
+      }
+    }
+    left -= n_tiles;
+    tile_lo = 0;
+    if (++h == p.Hkv) {
+      h = 0;
+      ++b;
+    }
+  }
+}
+
+// The kernel for a format: its blocks an SM, and its launch.
+template <int D, int VB, int KMODE, int NT>
+struct SpanFew {
+  using SM = AttnSmem<D, KeySpec<KMODE>::B, VB, NT>;
+  static constexpr int SMEM = SM::SMEM + 16;
+  static int per_sm() {
+    if (allow_smem<span_few_kernel<D, VB, KMODE, NT>>(SMEM) != cudaSuccess) return 1;
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, span_few_kernel<D, VB, KMODE, NT>, SM::Shape::THREADS, SMEM) !=
+              cudaSuccess || n < 1)
+        n = 1;
+      known.store(n, std::memory_order_relaxed);
+    }
+    return n;
+  }
+  // Sets p.grid to one wave of blocks, fewer where a team of warps would get less
+  // than kAttnMinTeamTiles of `tiles` tiles.
+  static cudaError_t launch(SpanPass& p, long long tiles, cudaStream_t s) {
+    const cudaError_t e = allow_smem<span_few_kernel<D, VB, KMODE, NT>>(SMEM);
+    if (e != cudaSuccess) return e;
+    const int most = per_sm();
+    long long grid = static_cast<long long>(most < kAttnGridPerSm ? most : kAttnGridPerSm) * sm_count();
+    const long long team = SM::NW / AttnSplit<D>::SPL * kAttnMinTeamTiles;
+    grid = std::min(grid, (tiles + team - 1) / team);
+    p.grid = static_cast<int>(std::max(grid, 1LL));
+    return launch_pdl_block(span_few_kernel<D, VB, KMODE, NT>, p.grid, SM::Shape::THREADS, p, s, SMEM);
+  }
+};
+
+template <int D, int VB, int NT>
+cudaError_t launch_span_few_keys(SpanPass& p, long long tiles, cudaStream_t s) {
+  switch (p.kmode) {
+    case kK2: return SpanFew<D, VB, kK2, NT>::launch(p, tiles, s);
+    case kK4: return SpanFew<D, VB, kK4, NT>::launch(p, tiles, s);
+    case kK5: return SpanFew<D, VB, kK5, NT>::launch(p, tiles, s);
+    case kK8: return SpanFew<D, VB, kK8, NT>::launch(p, tiles, s);
+    default: return SpanFew<D, VB, kK8Signed, NT>::launch(p, tiles, s);
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_span_few(SpanPass& p, long long tiles, cudaStream_t s) {
+  switch (p.vb) {
+    case 2: return launch_span_few_keys<D, 2, NT>(p, tiles, s);
+    case 3: return launch_span_few_keys<D, 3, NT>(p, tiles, s);
+    case 4: return launch_span_few_keys<D, 4, NT>(p, tiles, s);
+    case 5: return launch_span_few_keys<D, 5, NT>(p, tiles, s);
+    default: return launch_span_few_keys<D, 8, NT>(p, tiles, s);
+  }
+}
+
+}  // namespace tq

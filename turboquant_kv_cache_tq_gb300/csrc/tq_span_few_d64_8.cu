@@ -1,0 +1,7 @@
+// Window and prefix attention of at most 8 query rows a kv head, head_dim 64 (one
+// translation unit per head_dim and tile of rows, so the library builds in parallel).
+#include "tq_span_few.cuh"
+
+namespace tq {
+template cudaError_t launch_span_few<64, 1>(SpanPass&, long long, cudaStream_t);
+}  // namespace tq

@@ -1,0 +1,72 @@
+// A pass with more than 16 query rows a kv head: a chunk of a prompt, or the new
+// tokens of all the sequences that share a prefix. The tree attention's kernel
+// (tq_tree_attention.cuh) with another walk over tokens: in place of a batch row the
+// line of tiles has (cache row, row block), as each block of 128 rows of a chunk
+// sees a window of its own, and a segment's tiles are the sequence's first tokens and
+// the window.
+#pragma once
+
+#include "tq_span_attention.cuh"
+#include "tq_tree_attention.cuh"
+
+namespace tq {
+
+template <int D, bool F32>
+struct RowsWalk<D, F32, SpanPass> {
+  static constexpr int TT = TreeShape<D, F32>::TT;
+  int x, hh, tile, n, n_main;  // x: b * RB + rb
+  int left;                    // tiles still to come, this one included
+  int b, rb;
+  SpanTiles<TT> s;
+
+  __device__ __forceinline__ static int lines(const SpanPass& p) { return p.B * p.RB; }
+  __device__ __forceinline__ static SpanTiles<TT> span(const SpanPass& p, int b, int rb) {
+    return SpanTiles<TT>(p, b, rb * p.rows, min((rb + 1) * p.rows, p.R));
+  }
+  __device__ __forceinline__ static int row_tiles(const SpanPass& p, int x) {
+    return span(p, x / p.RB, x % p.RB).count();
+  }
+  __device__ __forceinline__ void row(const SpanPass& p) {
+    b = x / p.RB;
+    rb = x - b * p.RB;
+    s = span(p, b, rb);
+    n_main = s.n1;
+    n = s.count();
+  }
+  __device__ __forceinline__ void init(const SpanPass& p, const uint8_t* ctl) {
+    const int4 start = *reinterpret_cast<const int4*>(ctl + kcStart);
+    x = start.x;
+    hh = start.y;
+    tile = start.z;
+    left = start.w;
+    if (left > 0) row(p);
+  }
+  __device__ __forceinline__ void next_segment(const SpanPass& p) {
+    tile = 0;
+    if (++hh == p.HH) {
+      hh = 0;
+      if (left > 0) {
+        do {  // (rows without tiles have no place in the line)
+          if (++x == lines(p)) {  // (cannot be: tiles are left)
+            left = 0;
+            break;
+          }
+          row(p);
+        } while (n == 0);
+      }
+    }
+  }
+  __device__ __forceinline__ int head(const SpanPass&) const { return hh / TreeShape<D, F32>::VH; }
+  __device__ __forceinline__ int half(const SpanPass&) const { return hh % TreeShape<D, F32>::VH; }
+  __device__ __forceinline__ long long record(const SpanPass& p) const { return static_cast<long long>(x) * p.HH + hh; }
+};
+
+template <int D, bool F32>
+cudaError_t launch_span_rows(const SpanPass& p, cudaStream_t s) {
+  using S = TreeShape<D, F32>;
+  const cudaError_t e = allow_smem<tree_split_kernel<D, F32, SpanPass>>(S::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_block(tree_split_kernel<D, F32, SpanPass>, p.grid, S::THREADS, p, s, S::SMEM);
+}
+
+}  // namespace tq

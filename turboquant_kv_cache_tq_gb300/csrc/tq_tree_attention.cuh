@@ -31,6 +31,8 @@
 // lengths.
 #pragma once
 
+#include <type_traits>
+
 #include "tq_ragged_tiles.cuh"
 
 namespace tq {
@@ -59,6 +61,8 @@ struct TreeParams {
   float scale_log2;   // |scale| * log2(e)
   int negate;         // scale < 0
   float rot_scale;
+  // whether one lane of a loading warp loads alone, by bulk copies
+  __device__ __forceinline__ bool alone() const { return bulk && bulk_tree; }
 };
 
 template <int D, bool F32>
@@ -144,21 +148,25 @@ enum : int { kcKFull = 0, kcKEmpty = 16, kcVFull = 32, kcVEmpty = 64, kcSFull = 
 // are decoded after the fourth's were multiplied.
 constexpr int kTreeMarks = 8;
 
-// Tiles of a batch row: the sequence's and the tree's.
-template <int TT>
-__device__ __forceinline__ int tree_row_tiles(const TreeParams& p, int b) {
-  int lo, hi;
-  row_range(p.lens, p.left_pad, b, p.T, lo, hi);
-  return sequence_tiles<TT>(lo, hi) + (p.N + TT - 1) / TT;
-}
+// A walk over the block's tiles, the same in every warp: what differs between the
+// calls whose rows come by the 128 (their parameters P tell them apart).
+template <int D, bool F32, typename P>
+struct RowsWalk;
 
-// A walk over the block's tiles, the same in every warp.
 template <int D, bool F32>
-struct TreeWalk {
+struct RowsWalk<D, F32, TreeParams> {
   static constexpr int TT = TreeShape<D, F32>::TT;
   int b, hh, tile, n, n_main, lo, hi;
   int left;  // tiles still to come, this one included
 
+  // The line of tiles: what it has instead of batch rows (`lines` of them) and the
+  // tiles of each (a batch row's: the sequence's and the tree's).
+  __device__ __forceinline__ static int lines(const TreeParams& p) { return p.B; }
+  __device__ __forceinline__ static int row_tiles(const TreeParams& p, int b) {
+    int lo, hi;
+    row_range(p.lens, p.left_pad, b, p.T, lo, hi);
+    return sequence_tiles<TT>(lo, hi) + (p.N + TT - 1) / TT;
+  }
   __device__ __forceinline__ void row(const TreeParams& p) {
     row_range(p.lens, p.left_pad, b, p.T, lo, hi);
     n_main = sequence_tiles<TT>(lo, hi);
@@ -181,6 +189,12 @@ struct TreeWalk {
     }
   }
   __device__ __forceinline__ bool tail() const { return tile >= n_main; }
+  __device__ __forceinline__ int head(const TreeParams& p) const {
+    return p.HH == p.Hkv ? hh : hh / (p.RB * TreeShape<D, F32>::VH);
+  }
+  __device__ __forceinline__ int half(const TreeParams&) const { return hh % TreeShape<D, F32>::VH; }
+  // the segment's record, counted from the block's first one
+  __device__ __forceinline__ long long record(const TreeParams& p) const { return static_cast<long long>(b) * p.HH + hh; }
   // the tile's first token, and which of its tokens [first, end) are in the
   // sequence or the tree
   __device__ __forceinline__ void span(const TreeParams& p, int& t0, int& first, int& end) const {
@@ -199,8 +213,8 @@ struct TreeWalk {
 // of them belong to the sequence goes to the values' warps with the tile. A
 // warp's steps are in one chain, so pointers move on instead of being computed
 // anew.
-template <int D, bool F32, bool KEYS, bool ALONE>
-__device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int lane) {
+template <int D, bool F32, bool KEYS, bool ALONE, typename P>
+__device__ void tree_load(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int lane) {
   using S = TreeShape<D, F32>;
   constexpr int NG = KEYS ? S::NGK : S::NGV;
   constexpr bool ROWWISE = !KEYS && S::VH > 1;  // half of each row
@@ -261,13 +275,19 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
     }
   };
   if (!ALONE || lane == 0) {
-    TreeWalk<D, F32> w;
+    RowsWalk<D, F32, P> w;
     w.init(p, ctl);
     while (w.left > 0 && going) {
       const int n = min(w.left, w.n - w.tile), main = max(min(n, w.n_main - w.tile), 0);
-      const int h = p.HH == p.Hkv ? w.hh : w.hh / (p.RB * S::VH), half = KEYS || S::VH == 1 ? 0 : w.hh % S::VH;
-      if (main > 0) part(p.cache, p.bulk, w.b, h, half, (w.lo & ~15) + w.tile * S::TT, main, w.lo, w.hi);
-      if (n > main) part(p.tree, p.bulk_tree, w.b, h, half, max(w.tile - w.n_main, 0) * S::TT, n - main, 0, p.N);
+      const int h = w.head(p), half = KEYS || S::VH == 1 ? 0 : w.half(p);
+      if constexpr (std::is_same_v<P, TreeParams>) {
+        if (main > 0) part(p.cache, p.bulk, w.b, h, half, (w.lo & ~15) + w.tile * S::TT, main, w.lo, w.hi);
+        if (n > main) part(p.tree, p.bulk_tree, w.b, h, half, max(w.tile - w.n_main, 0) * S::TT, n - main, 0, p.N);
+      } else {
+        if (main > 0) part(p.cache, p.bulk, w.b, h, half, w.s.s1 + w.tile * S::TT, main, w.s.lo, w.s.hi);
+        if (n > main)
+          part(p.cache, p.bulk, w.b, h, half, w.s.s2 + max(w.tile - w.n_main, 0) * S::TT, n - main, w.s.lo, w.s.hi);
+      }
       w.left -= n;
       w.next_segment(p);
     }
@@ -282,8 +302,8 @@ __device__ void tree_load(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8
 
 // The keys' decoding warps: tile after tile from the packed stages into the
 // key stages.
-template <int D, bool F32, int KMODE>
-__device__ void tree_decode_keys(const TreeParams& p, uint32_t sm, uint8_t* ctl, int warp8, int lane) {
+template <int D, bool F32, int KMODE, typename P>
+__device__ void tree_decode_keys(const P& p, uint32_t sm, uint8_t* ctl, int warp8, int lane) {
   using S = TreeShape<D, F32>;
   constexpr int KB = KeySpec<KMODE>::B, X = D * KB / 8;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
@@ -332,8 +352,8 @@ __device__ __forceinline__ float2 table64(uint32_t a) {
 // softmax warps make NaN every row that attends to it, and the matrix product
 // never meets a non-finite value that a row with weight zero would turn into
 // NaN.
-template <int D, bool F32, int VB>
-__device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int warp8, int lane) {
+template <int D, bool F32, int VB, typename P>
+__device__ void tree_decode_values(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int warp8, int lane) {
   using S = TreeShape<D, F32>;
   using VT = ValueTable<VB>;
   constexpr int X = S::DV * VB / 8;
@@ -408,15 +428,15 @@ __device__ void tree_decode_values(const TreeParams& p, uint32_t sm, uint8_t* sm
 
 // The scores' warp: S = Q K^T, tile after tile. (A block holds all of tensor
 // memory, so its first column is column 0; the kernel checks that.)
-template <int D, bool F32>
-__device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
+template <int D, bool F32, typename P>
+__device__ void tree_scores(const P& p, uint32_t sm, uint8_t* ctl) {
   using S = TreeShape<D, F32>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   constexpr uint32_t tm = 0;
   const bool issue = elect_lane();
   const uint32_t kind = mma_kind(S::TT, false, p.negate != 0);
-  TreeWalk<D, F32> w;
+  RowsWalk<D, F32, P> w;
   w.init(p, ctl);
   int it = 0;
   for (unsigned seg = 0; w.left > 0; ++seg) {
@@ -454,15 +474,15 @@ __device__ void tree_scores(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
 
 // The weighted values' warp: O += P V, the weights as a high part, a remainder
 // to subtract (and what that leaves).
-template <int D, bool F32>
-__device__ void tree_weigh(const TreeParams& p, uint32_t sm, uint8_t* ctl) {
+template <int D, bool F32, typename P>
+__device__ void tree_weigh(const P& p, uint32_t sm, uint8_t* ctl) {
   using S = TreeShape<D, F32>;
   volatile int* quit = reinterpret_cast<volatile int*>(ctl + kcQuit);
   const uint32_t bars = sm + S::C_OFF;
   constexpr uint32_t tm = 0;
   const bool issue = elect_lane();
   constexpr uint32_t kind = mma_kind(S::DV, true, false), kind_rest = mma_kind(S::DV, true, true);
-  TreeWalk<D, F32> w;
+  RowsWalk<D, F32, P> w;
   w.init(p, ctl);
   int it = 0;
   while (w.left > 0) {
@@ -553,8 +573,8 @@ __device__ __forceinline__ unsigned long long tree_ancestors(uint32_t own, const
 
 // The softmax warps (group `which` of SW, every SW-th tile): a thread holds one
 // lane of tensor memory, i.e. one query row over its copy's share of the tokens.
-template <int D, bool F32>
-__device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int which, int warp, int lane) {
+template <int D, bool F32, typename P>
+__device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ctl, int which, int warp, int lane) {
   using S = TreeShape<D, F32>;
   constexpr int TT = S::TT;
   const int W = TT / p.copies;         // tokens of a tile that this lane takes: 32 or 64
@@ -568,22 +588,32 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
   const int copy = warp / QUADS, rl = (warp % QUADS) * 32 + lane, col0 = copy * W;
   auto s_full = [&](int it) { return warp_wait(bars + kcSFull + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
   auto weighed = [&](int it) { return warp_wait(bars + kcPFree + 8 * (it % S::NS), (it / S::NS) & 1, quit, p.err); };
-  TreeWalk<D, F32> w;
+  RowsWalk<D, F32, P> w;
   w.init(p, ctl);
+  constexpr bool TREE = std::is_same_v<P, TreeParams>;
   int it0 = 0, seg = 0, anc_b = -1, anc_rb = -1;
   unsigned long long anc = 0;
   while (w.left > 0) {
     const int n = min(w.left, w.n - w.tile);
-    const int rb = w.hh / S::VH % p.RB, h = w.hh / (S::VH * p.RB);
+    int rb, h;
+    if constexpr (TREE) {
+      rb = w.hh / S::VH % p.RB;
+      h = w.hh / (S::VH * p.RB);
+    } else {
+      rb = w.rb;
+      h = w.head(p);
+    }
     const int r = rb * p.rows + rl;
     const bool row = rl < p.rows && r < p.R;
     const bool work = __any_sync(kFull, row);  // a warp whose lanes have no row only keeps the barriers going
     const bool climb = w.b != anc_b || rb != anc_rb;
     int up[2] = {-1, -1};  // parents of nodes lane, lane + 32
-    if (climb && p.parents != nullptr) {
-      const int* from = p.parents + static_cast<long long>(w.b) * p.N;
-      if (lane < p.N) up[0] = from[lane];
-      if (lane + 32 < p.N) up[1] = from[lane + 32];
+    if constexpr (TREE) {
+      if (climb && p.parents != nullptr) {
+        const int* from = p.parents + static_cast<long long>(w.b) * p.N;
+        if (lane < p.N) up[0] = from[lane];
+        if (lane + 32 < p.N) up[1] = from[lane + 32];
+      }
     }
     // (plain loads: the kernel may have started before its inputs were written)
     // ---- the queries of the segment (every score of the last one is done), each
@@ -592,16 +622,28 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     {
       if (it0 > 0 && !s_full(it0 - 1)) return;
       tmem_fence_after();
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N * D);
+      const uint4* src;
+      if constexpr (TREE)
+        src = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N * D);
+      else
+        src = reinterpret_cast<const uint4*>(p.queries(w.b, h, D));
+      // where row x of the kv head's lies, in rows
+      auto place = [&](int x) -> long long {
+        if constexpr (TREE) return x;
+        else return p.query(x);
+      };
       // row x of the warp's 32, or -1
       auto row_at = [&](int x) {
         const int at = (warp % QUADS) * 32 + x;
         return at < p.rows && rb * p.rows + at < p.R ? rb * p.rows + at : -1;
       };
-      int from[4];
+      std::conditional_t<TREE, int, long long> from[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) from[i] = row_at(8 * i + (lane >> 2));
+      for (int i = 0; i < 4; ++i) {
+        from[i] = row_at(8 * i + (lane >> 2));
+        if (from[i] >= 0) from[i] = place(static_cast<int>(from[i]));
+      }
       constexpr int SHARE = S::QT / 2 / S::SW, STEP = SHARE < 32 ? SHARE : 32;
 #pragma unroll 1
       for (int c = which * SHARE; c < (which + 1) * SHARE; c += STEP) {
@@ -633,7 +675,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 #pragma unroll 8
         for (int x = 0; x < 32; ++x) {
           const int r2 = row_at(x);
-          const uint4 u = r2 >= 0 ? src[static_cast<long long>(r2) * (D / 8) + S::QT / 8 + lane]
+          const uint4 u = r2 >= 0 ? src[place(r2) * (D / 8) + S::QT / 8 + lane]
                                   : make_uint4(0u, 0u, 0u, 0u);
           sts128(sm + S::Q_OFF + (lane >> 3) * (128 * 128) + (warp * 32 + x) * 128 + (((lane ^ x) & 7) << 4), u.x, u.y,
                  u.z, u.w);
@@ -645,25 +687,35 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
       warp_arrive(bars + kcQFull, lane);
     }
     // ---- the rows' ancestors (while the first scores are on their way)
-    if (climb) {
-      anc = !row ? 0ull : p.parents == nullptr ? chain_ancestors(r % p.N) : 0ull;
-      if (p.parents != nullptr) {
-        const unsigned long long all = tree_ancestors(own, up, p.N, row ? r % p.N : 0, lane);
-        if (row) anc = all;
+    if constexpr (TREE) {
+      if (climb) {
+        anc = !row ? 0ull : p.parents == nullptr ? chain_ancestors(r % p.N) : 0ull;
+        if (p.parents != nullptr) {
+          const unsigned long long all = tree_ancestors(own, up, p.N, row ? r % p.N : 0, lane);
+          if (row) anc = all;
+        }
+        anc_b = w.b;
+        anc_rb = rb;
       }
-      anc_b = w.b;
-      anc_rb = rb;
+    } else {
+      anc = row;
     }
+    int at = 0;  // (spans) the token that the row sits at
+    if constexpr (!TREE) at = w.s.at(p, row ? r : 0);
     float m = kNegInf, l = 0.0f;
     // which of a tile's tokens the row attends to
     auto attended = [&](int tile) -> unsigned long long {
-      TreeWalk<D, F32> x = w;
-      x.tile = tile;
-      int t0, first, end;
-      x.span(p, t0, first, end);
-      unsigned long long a = anc == 0 ? 0ull : x.tail() ? anc >> t0 : ~0ull << first;
-      if (end < 64) a &= (1ull << end) - 1ull;
-      return a;
+      if constexpr (TREE) {
+        RowsWalk<D, F32, P> x = w;
+        x.tile = tile;
+        int t0, first, end;
+        x.span(p, t0, first, end);
+        unsigned long long a = anc == 0 ? 0ull : x.tail() ? anc >> t0 : ~0ull << first;
+        if (end < 64) a &= (1ull << end) - 1ull;
+        return a;
+      } else {
+        return anc == 0 ? 0ull : w.s.seen(p, at, w.s.token(tile));
+      }
     };
     // a marked token (a value group with a non-finite scale) that it attends to makes the row NaN
     auto spoil = [&](int it, int tile) {
@@ -689,7 +741,10 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
         tmem_fence_after();
         // hidden tokens (a tile at an end of the sequence, the tree): their
         // scores become -inf in place
-        if (tile >= w.n_main - 1 || (tile == 0 && (w.lo & 15) != 0)) {
+        bool some;
+        if constexpr (TREE) some = tile >= w.n_main - 1 || (tile == 0 && (w.lo & 15) != 0);
+        else some = !w.s.whole(p, w.s.token(tile));
+        if (some) {
           unsigned long long shown = attended(tile) >> col0;
 #pragma unroll 1
           for (int c = col0; c < col0 + W; c += 16, shown >>= 16) {
@@ -801,7 +856,7 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
     }
     if (work) {
       tmem_fence_after();
-      const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(w.b) * p.HH + w.hh;
+      const long long slot = static_cast<long long>(blockIdx.x) + w.record(p);
       float* rec = p.recs + slot * p.slots * (S::DV + 2);
       const bool store_ok = TQ_CHECK(slot < p.n_recs, p.err);
       const int at = copy * p.rows + rl;
@@ -878,8 +933,8 @@ __device__ void tree_softmax(const TreeParams& p, uint32_t sm, uint8_t* smem, ui
 // A small call (8 heads x 4096 tokens, 32 nodes: 18 us with the combine) is one
 // chain: cut 1.3 us, queries into tensor memory 2, first tile 1.5, three more 3,
 // record 2.
-template <int D, bool F32>
-__global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kernel(const __grid_constant__ TreeParams p) {
+template <int D, bool F32, typename P>
+__global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kernel(const __grid_constant__ P p) {
   using S = TreeShape<D, F32>;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* smem = tree_smem;
@@ -913,9 +968,9 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
       mbar_init(bars + kcPFree + 8 * i, 1);
     }
     for (int i = 0; i < S::NR; ++i) {
-      mbar_init(bars + kcKLoaded + 8 * i, p.bulk && p.bulk_tree ? 1 : 33);
+      mbar_init(bars + kcKLoaded + 8 * i, p.alone() ? 1 : 33);
       mbar_init(bars + kcKTaken + 8 * i, S::KWARPS * S::SUBS);
-      mbar_init(bars + kcVLoaded + 8 * i, S::VH == 1 && p.bulk && p.bulk_tree ? 1 : 33);
+      mbar_init(bars + kcVLoaded + 8 * i, S::VH == 1 && p.alone() ? 1 : 33);
       mbar_init(bars + kcVTaken + 8 * i, S::VWARPS);
     }
     *reinterpret_cast<int*>(ctl + kcQuit) = 0;
@@ -937,8 +992,9 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
-    cut_line<true>([&](int b) { return tree_row_tiles<S::TT>(p, b); }, p.B, p.HH, S::TURN, lane,
-                   reinterpret_cast<volatile int*>(ctl + kcStart), p.cut);
+    cut_line<true, !std::is_same_v<P, TreeParams>>([&](int b) { return RowsWalk<D, F32, P>::row_tiles(p, b); },
+                                                   RowsWalk<D, F32, P>::lines(p), p.HH, S::TURN, lane,
+                                                   reinterpret_cast<volatile int*>(ctl + kcStart), p.cut);
   }
   tmem_fence_before();
   __syncthreads();
@@ -973,7 +1029,7 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
     }
   } else {
     if constexpr (S::SW == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const bool alone = p.bulk && p.bulk_tree;
+    const bool alone = p.alone();
     if (warp == 22) {
       if (alone) tree_load<D, F32, true, true>(p, sm, smem, ctl, lane);
       else tree_load<D, F32, true, false>(p, sm, smem, ctl, lane);
@@ -1004,6 +1060,58 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
     tmem_fence_after();
     tmem_free(*reinterpret_cast<const uint32_t*>(ctl + kcTmem), 512);
   }
+}
+
+// An output row from its merged result: the division, the Hadamard butterflies, /
+// sqrt(D) and signs, the store, the log-sum-exp. Lane L holds elements [L D/32, (L+1)
+// D/32); whole warps call.
+template <int D>
+__device__ __forceinline__ void finish_row(float (&o)[D / 32], float m, float l, int row, bool store, void* out, int out_f32,
+                                           float* lse, float rot_scale, int lane) {
+  constexpr int E = D / 32, V = E < 4 ? E : 4;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  const bool empty = l == 0.0f;
+  const float inv = empty ? 0.0f : __fdiv_rn(1.0f, l);
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[i] = empty ? 0.0f : __fmul_rn(o[i], inv);
+#pragma unroll
+  for (int h2 = 1; h2 < E; h2 <<= 1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if ((i & h2) == 0) {
+        const float a = o[i], c = o[i + h2];
+        o[i] = __fadd_rn(a, c);
+        o[i + h2] = __fsub_rn(a, c);
+      }
+  }
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const float sgn = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(o[i], sgn, __shfl_xor_sync(kFull, o[i], x));
+  }
+  if (!store) return;
+  const uint8_t* neg = D == 64 ? kSignNeg64 : D == 128 ? kSignNeg128 : D == 256 ? kSignNeg256 : kSignNeg512;
+  const int e0 = lane * E;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const uint32_t flip = (neg[(e0 + i) >> 3] >> ((e0 + i) & 7) & 1u) << 31;
+    o[i] = __uint_as_float(__float_as_uint(__fmul_rn(o[i], rot_scale)) ^ flip);
+  }
+  if (out_f32) {
+    float* dst = static_cast<float*>(out) + static_cast<long long>(row) * D + e0;
+#pragma unroll
+    for (int i = 0; i < E; i += V) {
+      if constexpr (V == 2) *reinterpret_cast<float2*>(dst + i) = make_float2(o[i], o[i + 1]);
+      else *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    }
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + static_cast<long long>(row) * D + e0);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16x2(o[i], o[i + 1]);
+  }
+  if (lse != nullptr && lane == 0)
+    lse[row] = empty ? kNegInf : __fmul_rn(__fadd_rn(m, log2f(l)), 0.693147180559945309f);
 }
 
 // Merges the partial results of each output row, divides, turns the row back
@@ -1138,56 +1246,15 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) tree_combine_kernel(con
     const float other = __shfl_xor_sync(kFull, l, 16);
     if (other != other) l = other;
   }
-  const bool empty = l == 0.0f;
-  const float inv = empty ? 0.0f : __fdiv_rn(1.0f, l);
-#pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = empty ? 0.0f : __fmul_rn(o[i], inv);
-#pragma unroll
-  for (int h2 = 1; h2 < E; h2 <<= 1) {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if ((i & h2) == 0) {
-        const float a = o[i], c = o[i + h2];
-        o[i] = __fadd_rn(a, c);
-        o[i + h2] = __fsub_rn(a, c);
-      }
-  }
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const float sgn = (lane & x) ? -1.0f : 1.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(o[i], sgn, __shfl_xor_sync(kFull, o[i], x));
-  }
-  if (row0 >= rows) return;
-  const uint8_t* neg = D == 64 ? kSignNeg64 : D == 128 ? kSignNeg128 : D == 256 ? kSignNeg256 : kSignNeg512;
-  const int e0 = lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const uint32_t flip = (neg[(e0 + i) >> 3] >> ((e0 + i) & 7) & 1u) << 31;
-    o[i] = __uint_as_float(__float_as_uint(__fmul_rn(o[i], p.rot_scale)) ^ flip);
-  }
-  if (p.out_f32) {
-    float* dst = static_cast<float*>(p.out) + static_cast<long long>(row) * D + e0;
-#pragma unroll
-    for (int i = 0; i < E; i += V) {
-      if constexpr (V == 2) *reinterpret_cast<float2*>(dst + i) = make_float2(o[i], o[i + 1]);
-      else *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-    }
-  } else {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(row) * D + e0);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16x2(o[i], o[i + 1]);
-  }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[row] = empty ? kNegInf : __fmul_rn(__fadd_rn(m, log2f(l)), 0.693147180559945309f);
+  finish_row<D>(o, m, l, row, row0 < rows, p.out, p.out_f32, p.lse, p.rot_scale, lane);
 }
 
 template <int D, bool F32>
 cudaError_t launch_tree_split(const TreeParams& p, cudaStream_t s) {
   using S = TreeShape<D, F32>;
-  cudaError_t e = allow_smem<tree_split_kernel<D, F32>>(S::SMEM);
+  cudaError_t e = allow_smem<tree_split_kernel<D, F32, TreeParams>>(S::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl_block(tree_split_kernel<D, F32>, p.grid, S::THREADS, p, s, S::SMEM);
+  return launch_pdl_block(tree_split_kernel<D, F32, TreeParams>, p.grid, S::THREADS, p, s, S::SMEM);
 }
 
 }  // namespace tq
