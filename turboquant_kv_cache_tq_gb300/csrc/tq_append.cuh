@@ -8,10 +8,14 @@
 // and its bytes are those that the codec gives for it. Values are encoded as they
 // are.
 //
-// A lane holds one group of 32 elements of a row, a warp the rows that fill it
-// (the codec's layout), and an item is that many rows of the values, the keys or
-// the queries. A partner outside the lane's group is read from memory a second
-// time (it is in L1), not passed between lanes.
+// Keys and values: a lane holds one group of 32 elements of a row, a warp the rows
+// that fill it (the codec's layout). A partner outside the lane's group is read from
+// memory a second time (it is in L1), not passed between lanes. A warp's keys are
+// heads of one token where there are enough, so that its lanes read the same angles.
+// Queries are not encoded, so they come in 16-byte pieces: a lane turns a
+// pair of pieces, keeps that pair's angles, and goes through heads of the token with
+// them (each row reading its angles anew, 512 bytes for 256 of a bf16 row, bound the
+// kernel by L1: prompts of 4 x 2048 tokens 80 us).
 #pragma once
 
 #include <type_traits>
@@ -44,11 +48,14 @@ struct AppendParams {
   int* new_lens;
   long long t_cap;
   int B, Hq, Hkv, N, R, length, interleaved;
-  int wide;            // a pair's elements and angles come in whole groups: vector loads
+  int wide;            // keys: a pair's elements and angles come in whole groups: vector loads
+  int pieces;          // queries: in pairs of pieces (else in groups, like the keys)
+  int steps;           // and how many heads of a token a lane goes through
   int kmode, vb;
   int kv_rows, q_rows; // B Hkv N, B Hq N (0: no queries)
+  int q_items;         // warps' worth of queries
   float rot_scale, neg_zero;
-  FastDiv by_n, by_hkv, by_hq;
+  FastDiv by_n, by_hkv, by_hq, by_heads;  // by_heads: items of a token's queries
   long long cache_rows;  // B Hkv t_cap (debug checks)
   unsigned* err;
 };
@@ -141,8 +148,102 @@ __device__ __forceinline__ void append_turn(const AppendParams& p, const void* r
   }
 }
 
+// Queries in pairs of 16-byte pieces: D / (2 C) lanes a row of pieces of C elements,
+// pair u < R / (2 C) made of pieces that turn together (C angles), the others copied.
+// Item: some heads of one token.
 template <int D, bool F32>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+struct AppendPieces {
+  static constexpr int C = F32 ? 4 : 8, PAIRS = D / (2 * C);
+  static constexpr int LANES = PAIRS < 32 ? PAIRS : 32, TURNS = PAIRS / LANES;  // lanes a row; pairs of a lane
+  static constexpr int HEADS = 32 / LANES;                                      // heads side by side
+};
+
+template <int D, bool F32, typename Position>
+__device__ __forceinline__ void append_queries(const AppendParams& p, int item, int lane, Position position) {
+  using S = AppendPieces<D, F32>;
+  constexpr int C = S::C;
+  const int bn = fast_div(item, p.by_heads), part = item - bn * ((p.Hq + S::HEADS * p.steps - 1) / (S::HEADS * p.steps));
+  const int b = fast_div(bn, p.by_n), n = bn - b * p.N;
+  const int h0 = part * S::HEADS * p.steps + lane / S::LANES;
+  const int h1 = min(p.Hq, (part + 1) * S::HEADS * p.steps);
+  const float* angles = nullptr;
+  long long at = 0;
+  if (p.R > 0) {
+    at = static_cast<long long>(position(b, n)) * (p.R >> 1);
+    angles = p.cos + at;
+  }
+#pragma unroll 1
+  for (int turn = 0; turn < S::TURNS; ++turn) {
+    const int u = turn * S::LANES + lane % S::LANES;
+    const bool turns = 2 * u * C < p.R;
+    const int e0 = !turns || p.interleaved ? 2 * u * C : u * C, e1 = !turns || p.interleaved ? e0 + C : e0 + (p.R >> 1);
+    float c[C], s[C];
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+      float4 x = make_float4(1.0f, 1.0f, 1.0f, 1.0f), y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (turns) {
+        x = *reinterpret_cast<const float4*>(angles + u * C + i);
+        y = *reinterpret_cast<const float4*>(p.sin + at + u * C + i);
+      }
+      c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
+      s[i] = y.x; s[i + 1] = y.y; s[i + 2] = y.z; s[i + 3] = y.w;
+    }
+    constexpr int SIZE = F32 ? 4 : 2;
+    const char* src = static_cast<const char*>(p.q.data) + (b * p.q.sb + n * p.q.st) * SIZE;
+    char* dst = static_cast<char*>(p.q_out) + (static_cast<long long>(b) * p.Hq * p.N + n) * D * SIZE;
+#pragma unroll 4
+    for (int h = h0; h < h1; h += S::HEADS) {
+      const char* from = src + h * p.q.sh * SIZE;
+      const uint4 w0 = *reinterpret_cast<const uint4*>(from + e0 * SIZE), w1 = *reinterpret_cast<const uint4*>(from + e1 * SIZE);
+      uint4 o0 = w0, o1 = w1;
+      if (turns) {
+        float x[2 * C];
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (F32) {
+            x[i] = __uint_as_float(w[i]);
+          } else {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          // pair i: neighbours, or element i of either piece
+          const float a = p.interleaved ? x[2 * i] : x[i], z = p.interleaved ? x[2 * i + 1] : x[C + i];
+          const float y0 = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(z, s[i]));
+          const float y1 = __fadd_rn(__fmul_rn(z, c[i]), __fmul_rn(a, s[i]));
+          if (p.interleaved) {
+            x[2 * i] = y0;
+            x[2 * i + 1] = y1;
+          } else {
+            x[i] = y0;
+            x[C + i] = y1;
+          }
+        }
+        uint32_t y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (F32) {
+            y[i] = __float_as_uint(x[i]);
+          } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            y[i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+        }
+        o0 = make_uint4(y[0], y[1], y[2], y[3]);
+        o1 = make_uint4(y[4], y[5], y[6], y[7]);
+      }
+      char* to = dst + static_cast<long long>(h) * p.N * D * SIZE;
+      *reinterpret_cast<uint4*>(to + e0 * SIZE) = o0;
+      *reinterpret_cast<uint4*>(to + e1 * SIZE) = o1;
+    }
+  }
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
   using G = Geo<D>;
   constexpr int NG = D / kGroup;
   __shared__ CellEntry s_cells[CellGrid<8>::NC];
@@ -166,7 +267,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
   const int lane = threadIdx.x & 31, sub = lane / G::LPR, l = lane % G::LPR;
   const int n_warps = gridDim.x * (kAppendThreads / 32);
-  const int kv_items = (p.kv_rows + G::RPW - 1) / G::RPW, q_items = (p.q_rows + G::RPW - 1) / G::RPW;
+  const int kv_items = (p.kv_rows + G::RPW - 1) / G::RPW;
   auto start = [&](int b) { return p.lens != nullptr ? max(p.lens[b], 0) : 0; };
   auto counted = [&](int b) { return p.count != nullptr ? min(max(p.count[b], 0), p.N) : p.N; };
   if (blockIdx.x == 0) {
@@ -182,12 +283,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   auto no_prefetch = [] {};
   // the values' items first (the longest), then the keys', then the queries'
 #pragma unroll 1
-  for (int it = warp_index(); it < 2 * kv_items + q_items; it += n_warps) {
+  for (int it = warp_index(); it < 2 * kv_items + p.q_items; it += n_warps) {
     const int kind = it < kv_items ? 0 : it < 2 * kv_items ? 1 : 2;
+    if (kind == 2 && p.pieces) {
+      append_queries<D, F32>(p, it - 2 * kv_items, lane, position);
+      continue;
+    }
     const int rows = kind < 2 ? p.kv_rows : p.q_rows, H = kind < 2 ? p.Hkv : p.Hq;
     const int r0 = (it - kind * kv_items) * G::RPW + sub, r = min(r0, rows - 1);
-    const int bh = fast_div(r, p.by_n), n = r - bh * p.N;
-    const int b = fast_div(bh, kind < 2 ? p.by_hkv : p.by_hq), h = bh - b * H;
+    int b, h, n;
+    if (kind == 1) {  // head after head of a token
+      const int bn = fast_div(r, p.by_hkv);
+      h = r - bn * H;
+      b = fast_div(bn, p.by_n);
+      n = bn - b * p.N;
+    } else {  // token after token of a head
+      const int bh = fast_div(r, p.by_n);
+      n = r - bh * p.N;
+      b = fast_div(bh, kind == 0 ? p.by_hkv : p.by_hq);
+      h = bh - b * H;
+    }
+    const int bh = b * H + h;
     const RowsView& x = kind == 0 ? p.v : kind == 1 ? p.k : p.q;
     const long long at = b * x.sb + h * x.sh + n * x.st;
     const void* row = F32 ? static_cast<const void*>(static_cast<const float*>(x.data) + at)
@@ -249,10 +365,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 }
 
 template <int D, bool F32>
-cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
-  const long long items = 2LL * ((p.kv_rows + Geo<D>::RPW - 1) / Geo<D>::RPW) + (p.q_rows + Geo<D>::RPW - 1) / Geo<D>::RPW;
-  const long long blocks = (items + kAppendThreads / 32 - 1) / (kAppendThreads / 32), most = 2LL * sm_count();
-  return launch_pdl(append_kernel<D, F32>, static_cast<int>(std::max(std::min(blocks, most), 1LL)), p, s, 0, kAppendThreads);
+cudaError_t launch_append(const AppendParams& params, cudaStream_t s) {
+  using S = AppendPieces<D, F32>;
+  AppendParams p = params;
+  const long long kv_items = 2LL * ((p.kv_rows + Geo<D>::RPW - 1) / Geo<D>::RPW), warps = 2LL * sm_count() * (kAppendThreads / 32);
+  p.pieces = p.R % (2 * S::C) == 0;
+  p.steps = 1;
+  long long q_items = (p.q_rows + Geo<D>::RPW - 1) / Geo<D>::RPW;
+  if (p.pieces && p.q_rows > 0) {
+    // as many heads a lane as leave every warp an item or two
+    const long long tokens = static_cast<long long>(p.B) * p.N;
+    auto items = [&](int steps) { return tokens * ((p.Hq + S::HEADS * steps - 1) / (S::HEADS * steps)); };
+    while (p.steps < 8 && S::HEADS * p.steps < p.Hq && items(2 * p.steps) >= 2 * warps) p.steps *= 2;
+    p.by_heads = make_fast_div((p.Hq + S::HEADS * p.steps - 1) / (S::HEADS * p.steps));
+    q_items = items(p.steps);
+  }
+  p.q_items = static_cast<int>(q_items);
+  const long long blocks = (kv_items + q_items + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const int grid = static_cast<int>(std::max(std::min(blocks, 2LL * sm_count()), 1LL));
+  return launch_pdl(append_kernel<D, F32>, grid, p, s, 0, kAppendThreads);
 }
 
 }  // namespace tq

@@ -271,32 +271,50 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
 
       // ---- online softmax per query column 8 n + 2 c + x (tokens g, g + 8
       // in entries x and 2 + x); the column's values sit in the eight lanes
-      // with the same c
+      // with the same c. The reference maximum moves only when a weight would
+      // pass 2^8, so most tiles need neither the maximum over the lanes nor a rescaling.
       float pr[NT][4];
-      float al[NT][2];
+      bool raise = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float xs[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          xs[e] = __fmul_rn(sfull[n][e], p.scale_log2);
-          if (!whole && !w.sees(p, at[n][e & 1], t0 + g + 8 * (e >> 1))) xs[e] = kNegInf;
+          pr[n][e] = __fmul_rn(sfull[n][e], p.scale_log2);
+          if (!whole && !w.sees(p, at[n][e & 1], t0 + g + 8 * (e >> 1))) pr[n][e] = kNegInf;
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float mt = fmaxf(xs[x], xs[2 + x]);
-          mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
-          mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
-          mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
-          const float mn = fmaxf(m_run[n][x], mt);
-          const float mu = mn == kNegInf ? 0.0f : mn;
-          al[n][x] = fast_exp2(__fsub_rn(m_run[n][x], mu));
-          m_run[n][x] = mn;
-          pr[n][x] = fast_exp2(__fsub_rn(xs[x], mu));
-          pr[n][2 + x] = fast_exp2(__fsub_rn(xs[2 + x], mu));
-          l_run[n][x] = __fadd_rn(__fmul_rn(l_run[n][x], al[n][x]), __fadd_rn(pr[n][x], pr[n][2 + x]));
-        }
+        for (int x = 0; x < 2; ++x) raise = raise || fmaxf(pr[n][x], pr[n][2 + x]) > __fadd_rn(m_run[n][x], 8.0f);
       }
+      if (__any_sync(kFull, raise)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mt = fmaxf(pr[n][x], pr[n][2 + x]);
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
+            const float mn = fmaxf(m_run[n][x], mt);
+            const float al = mn == kNegInf ? 1.0f : fast_exp2(__fsub_rn(m_run[n][x], mn));
+            m_run[n][x] = mn;
+            l_run[n][x] = __fmul_rn(l_run[n][x], al);
+            // O^T's columns are this lane's query columns 2 c, 2 c + 1
+#pragma unroll
+            for (int i = 0; i < DH / 16; ++i) {
+              acc[i][n][x] = __fmul_rn(acc[i][n][x], al);
+              acc[i][n][2 + x] = __fmul_rn(acc[i][n][2 + x], al);
+            }
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float mu = m_run[n][x] == kNegInf ? 0.0f : m_run[n][x];
+          pr[n][x] = fast_exp2(__fsub_rn(pr[n][x], mu));
+          pr[n][2 + x] = fast_exp2(__fsub_rn(pr[n][2 + x], mu));
+          l_run[n][x] = __fadd_rn(l_run[n][x], __fadd_rn(pr[n][x], pr[n][2 + x]));
+        }
       // a value group with an infinite or NaN scale: its row is NaN where it is seen
       if (__any_sync(kFull, most >= 0x7c00u)) {
         uint32_t bad = 0;
@@ -316,23 +334,6 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
               for (int x = 0; x < 2; ++x)
                 if (w.sees(p, at[n][x], t0 + t)) l_run[n][x] = __int_as_float(0x7fc00000);
           }
-      }
-      // rescale O^T: its columns are this lane's query columns 2 c, 2 c + 1
-      {
-        bool change = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) change = change || al[n][0] != 1.0f || al[n][1] != 1.0f;
-        if (__any_sync(kFull, change)) {
-#pragma unroll
-          for (int i = 0; i < DH / 16; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[i][n][0] = __fmul_rn(acc[i][n][0], al[n][0]);
-              acc[i][n][1] = __fmul_rn(acc[i][n][1], al[n][1]);
-              acc[i][n][2] = __fmul_rn(acc[i][n][2], al[n][0]);
-              acc[i][n][3] = __fmul_rn(acc[i][n][3], al[n][1]);
-            }
-        }
       }
       // P^T operands (k = token, n = query row): the weights of tokens g and
       // g + 8 for query columns 2 c, 2 c + 1, split into bf16 parts (two are
