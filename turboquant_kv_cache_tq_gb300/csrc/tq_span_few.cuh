@@ -17,6 +17,68 @@
 
 namespace tq {
 
+// A block's range of the line of all tiles, found by every warp for itself: the
+// line of cut_line, where a segment's tiles are preceded by up to kFewTurn places for
+// what its beginning and end cost. Block 0 writes what the combine kernel finds a
+// segment's blocks by. (A straight line of code that runs once is paid in
+// instruction fetches, some 100 cycles for eight of them: cut_line with its two
+// searches took 5.8 us here.)
+struct FewRange {
+  int b, h;
+  unsigned at, left, turn;  // the place in the segment, the places still to come
+};
+
+__device__ __forceinline__ FewRange few_range(const SpanPass& p, int lane) {
+  FewRange o;
+  const bool writes = blockIdx.x == 0 && threadIdx.x < 32;
+  int sum = 0, rows = 0, n = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const bool here = b0 + lane < p.B;
+    n = here ? SpanTiles<kAttnTile>(p, b0 + lane, 0, p.R).count() : 0;
+    const unsigned some = __ballot_sync(kFull, n > 0);
+    if (writes) {
+      const int c = warp_prefix(n, lane);
+      if (here) {
+        p.cut[kCutRows + b0 + lane + 1] = sum + c;
+        p.cut[kCutRows + p.B + 1 + b0 + lane + 1] = rows + __popc(some & (kFull >> (31 - lane)));
+      }
+    }
+    sum += __reduce_add_sync(kFull, n);
+    rows += __popc(some);
+  }
+  const unsigned all = static_cast<unsigned>(sum) * p.HH, ranges = max(min(all, gridDim.x), 1u);
+  o.turn = min(static_cast<unsigned>(kFewTurn), all / ranges);
+  const unsigned line = all + o.turn * rows * p.HH, per = line / ranges, more = line - per * ranges;
+  if (writes && lane == 0) {
+    p.cut[0] = static_cast<int>(o.turn);
+    p.cut[1] = static_cast<int>(per);
+    p.cut[2] = static_cast<int>(more);
+    p.cut[kCutRows] = p.cut[kCutRows + p.B + 1] = 0;
+  }
+  unsigned place = blockIdx.x * per + min(blockIdx.x, more);
+  o.left = blockIdx.x < ranges ? per + (blockIdx.x < more ? 1u : 0u) : 0u;
+  o.b = o.h = 0;
+  o.at = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B && o.left > 0; b0 += 32) {
+    if (p.B > 32) n = b0 + lane < p.B ? SpanTiles<kAttnTile>(p, b0 + lane, 0, p.R).count() : 0;
+    const unsigned one = n > 0 ? n + o.turn : 0, end = static_cast<unsigned>(warp_prefix(static_cast<int>(one), lane)) * p.HH;
+    const unsigned who = __ballot_sync(kFull, place < end);
+    if (who != 0) {
+      const int from = __ffs(who) - 1;
+      const unsigned length = __shfl_sync(kFull, one, from);
+      place -= __shfl_sync(kFull, end, from) - length * p.HH;
+      o.b = b0 + from;
+      o.h = static_cast<int>(place / length);
+      o.at = place - o.h * length;
+      break;
+    }
+    place -= __shfl_sync(kFull, end, 31);
+  }
+  return o;
+}
+
 template <int D, int VB, int KMODE, int NT>
 __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB, NT>::MIN_BLOCKS)
     span_few_kernel(const __grid_constant__ SpanPass p) {
@@ -33,21 +95,22 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
   uint8_t* s_vtab = few_smem;
   float* s_xchg = reinterpret_cast<float*>(few_smem + SM::XOFF);
   uint8_t* s_work = few_smem + SM::WORK;
-  volatile int* s_start = reinterpret_cast<volatile int*>(few_smem + SM::SMEM);
+  // a team's partial result (16 maxima, 16 sums, rows of RS floats), and the teams' factors
+  constexpr int RS = D + 4, PART = 32 + 16 * RS;
+  float* s_part = reinterpret_cast<float*>(s_work);
+  float* s_factor = s_part + TEAMS * PART;
+  static_assert(TEAMS * 16 <= AttnShape<D, VB, NT>::THREADS, "a thread a row and team");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int team = warp / SPL;  // warps sharing a tile
   const int half = warp % SPL;  // the head_dim slice of this warp
 
-  fill_value_table<VB>(s_vtab);
+  fill_value_rows<VB>(s_vtab);
   pdl_launch_dependents();
   pdl_wait();
-  if (warp == 0)
-    cut_line<true, true>([&](int b) { return SpanTiles<kAttnTile>(p, b, 0, p.R).count(); }, p.B, p.HH, kFewTurn, lane,
-                         s_start, p.cut);
+  FewRange at0 = few_range(p, lane);
   __syncthreads();
-  int b = s_start[0], h = s_start[1], tile_lo = s_start[2], left = s_start[3];
 
   uint8_t* ring = s_work + warp * S * L::STAGE;
   const uint32_t ring_sh = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
@@ -56,41 +119,23 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
   constexpr float kBias = kMagic + (M::SIGNED ? 128.0f : 0.0f);
   constexpr float kBias16 = 1024.0f + (M::SIGNED ? 128.0f : 0.0f);
 
-  while (left > 0 && b < p.B) {
+  while (at0.left > 0 && at0.b < p.B) {
+    const int b = at0.b, h = at0.h;
     const SpanTiles<kAttnTile> w(p, b, 0, p.R);
-    const int n_tiles = min(left, w.count() - tile_lo);
-    if (n_tiles <= 0) {  // (a row without tiles)
-      h = 0;
-      ++b;
+    if (w.count() == 0) {  // (a row without tiles has no place in the line)
+      at0.h = 0;
+      ++at0.b;
       continue;
     }
-    __syncthreads();  // the previous segment's merge area is free again
-
-    // Query operands of the score MMAs, kept in registers: query row 8 n + g,
-    // head_dim elements c DH/4 + 4 j .. + 3 for k-step j (the contraction's
-    // permuted order, see attn_split_kernel). Padding rows are zero.
-    uint32_t qf[DH / 16][NT][2];
-    {
-      const uint16_t* qsrc = p.queries(b, h, D) + half * DH;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int row = 8 * n + g;
-        const long long at = p.query(row) * D + c * L::EK;
-#pragma unroll
-        for (int j = 0; j < DH / 16; ++j) {
-          uint2 u = make_uint2(0u, 0u);
-          if (row < p.R) u = *reinterpret_cast<const uint2*>(qsrc + at + 4 * j);
-          qf[j][n][0] = u.x;
-          qf[j][n][1] = u.y;
-        }
-      }
+    const unsigned take = min(at0.left, w.count() + at0.turn - at0.at), end = at0.at + take;
+    const int tile_lo = at0.at > at0.turn ? at0.at - at0.turn : 0, n_tiles = (end > at0.turn ? end - at0.turn : 0) - tile_lo;
+    at0.left -= take;
+    at0.at = 0;
+    if (++at0.h == p.Hkv) {
+      at0.h = 0;
+      ++at0.b;
     }
-    // the token that the lane's query columns 8 n + 2 c + x sit at
-    int at[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) at[n][x] = w.at(p, min(8 * n + 2 * c + x, p.R - 1));
+    if (n_tiles == 0) break;  // (the range ends before the segment's first tile)
 
     const long long row0 = (static_cast<long long>(b) * p.Hkv + h) * p.cache.t_cap;
     const int my_tiles = n_tiles > team ? (n_tiles - team + TEAMS - 1) / TEAMS : 0;
@@ -133,6 +178,39 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
       }
     };
 
+    // the first tiles are on their way while the queries are read
+#pragma unroll 1
+    for (int k = 0; k < S - 1; ++k) {
+      issue(k);
+      cp_async_commit();
+    }
+
+    // Query operands of the score MMAs, kept in registers: query row 8 n + g,
+    // head_dim elements c DH/4 + 4 j .. + 3 for k-step j (the contraction's
+    // permuted order, see attn_split_kernel). Padding rows are zero.
+    uint32_t qf[DH / 16][NT][2];
+    {
+      const uint16_t* qsrc = p.queries(b, h, D) + half * DH;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = 8 * n + g;
+        const long long at = p.query(row) * D + c * L::EK;
+#pragma unroll
+        for (int j = 0; j < DH / 16; ++j) {
+          uint2 u = make_uint2(0u, 0u);
+          if (row < p.R) u = *reinterpret_cast<const uint2*>(qsrc + at + 4 * j);
+          qf[j][n][0] = u.x;
+          qf[j][n][1] = u.y;
+        }
+      }
+    }
+    // the token that the lane's query columns 8 n + 2 c + x sit at
+    int at[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) at[n][x] = w.at(p, min(8 * n + 2 * c + x, p.R - 1));
+
     float acc[DH / 16][NT][4];
 #pragma unroll
     for (int i = 0; i < DH / 16; ++i)
@@ -149,13 +227,11 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
         l_run[n][x] = 0.0f;
       }
 
-    // (the first turns only fill the ring)
 #pragma unroll 1
-    for (int k = 1 - S; k < my_tiles; ++k) {
+    for (int k = 0; k < my_tiles; ++k) {
       __syncwarp();
       issue(k + S - 1);
       cp_async_commit();
-      if (k < 0) continue;
       cp_async_wait<S - 1>();
       __syncwarp();
       const uint8_t* st = ring + (k % S) * L::STAGE;
@@ -400,31 +476,32 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
       }
 
     // ---- merge the teams in shared memory, one record per block (the
-    // warps of a team share m and l and each holds its half of O)
+    // warps of a team share m and l and each holds its half of O). A row's
+    // elements lie as the lanes hold them: 16 i + 2 g + e in place of g EV + 2 i + e,
+    // so that a store's lanes meet different banks.
     __syncthreads();  // every warp is done with its ring
-    float* mine = reinterpret_cast<float*>(s_work) + team * SM::REC;
+    float* mine = s_part + team * PART;
     if (g == 0 && half == 0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          mine[8 * n + 2 * c + x] = m_run[n][x];
-          mine[16 + 8 * n + 2 * c + x] = l_run[n][x];
+          const float m = m_run[n][x], l = l_run[n][x];
+          // (a NaN row counts with a finite maximum, so that every merge takes it)
+          mine[8 * n + 2 * c + x] = l != l && m == kNegInf ? 0.0f : m;
+          mine[16 + 8 * n + 2 * c + x] = l;
         }
     }
-    {
-      float* O = mine + 32 + half * DH;
 #pragma unroll
-      for (int i = 0; i < DH / 16; ++i)
+    for (int n = 0; n < NT; ++n)
+      if (8 * n + 2 * c < p.R) {
+        float* O = mine + 32 + (8 * n + 2 * c) * RS + half * DH + 2 * g;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int q0 = 8 * n + 2 * c, d0 = g * L::EV + 2 * i;
-          O[q0 * D + d0] = acc[i][n][0];
-          O[(q0 + 1) * D + d0] = acc[i][n][1];
-          O[q0 * D + d0 + 1] = acc[i][n][2];
-          O[(q0 + 1) * D + d0 + 1] = acc[i][n][3];
+        for (int i = 0; i < DH / 16; ++i) {
+          *reinterpret_cast<float2*>(O + 16 * i) = make_float2(acc[i][n][0], acc[i][n][2]);
+          *reinterpret_cast<float2*>(O + RS + 16 * i) = make_float2(acc[i][n][1], acc[i][n][3]);
         }
-    }
+      }
     if constexpr (SPL > 1) {  // a value group that spoils a row may lie in the other slice
       __syncthreads();
       if (g == 0 && half != 0) {
@@ -432,52 +509,52 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (l_run[n][x] != l_run[n][x]) mine[16 + 8 * n + 2 * c + x] = l_run[n][x];
+            if (l_run[n][x] != l_run[n][x]) {
+              mine[16 + 8 * n + 2 * c + x] = l_run[n][x];
+              if (m_run[n][x] == kNegInf) mine[8 * n + 2 * c + x] = 0.0f;
+            }
       }
     }
     __syncthreads();
-    // (a NaN row counts with a finite maximum, so that every merge takes it)
-    const float* all = reinterpret_cast<const float*>(s_work);
-    auto top = [&](int x, int r) {
-      const float m = all[x * SM::REC + r], l = all[x * SM::REC + 16 + r];
-      return l != l && m == kNegInf ? 0.0f : m;
-    };
     const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(b) * p.HH + h;
-    if (TQ_CHECK(slot < p.n_recs, p.err)) {
-      float* rec = p.recs + slot * SM::REC;
-      for (int i = threadIdx.x; i < p.R * D; i += blockDim.x) {
-        const int r = i / D;
-        float mx = kNegInf;
+    const bool store = TQ_CHECK(slot < p.n_recs, p.err);
+    float* rec = p.recs + slot * SM::REC;
+    if (threadIdx.x < TEAMS * 16) {
+      const int r = threadIdx.x & 15, x = threadIdx.x >> 4;
+      float mx = kNegInf, sum = 0.0f;
 #pragma unroll
-        for (int x = 0; x < TEAMS; ++x) mx = fmaxf(mx, top(x, r));
-        float sum = 0.0f;
-#pragma unroll
-        for (int x = 0; x < TEAMS; ++x) {
-          const float mw = top(x, r);
-          if (mw != kNegInf) sum = __fadd_rn(sum, __fmul_rn(exp2f(__fsub_rn(mw, mx)), all[x * SM::REC + 32 + i]));
-        }
-        rec[32 + i] = sum;
-      }
-      for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
-        float mx = kNegInf;
-#pragma unroll
-        for (int x = 0; x < TEAMS; ++x) mx = fmaxf(mx, top(x, r));
-        float l = 0.0f;
-#pragma unroll
-        for (int x = 0; x < TEAMS; ++x) {
-          const float mw = top(x, r);
-          if (mw != kNegInf) l = __fadd_rn(l, __fmul_rn(exp2f(__fsub_rn(mw, mx)), all[x * SM::REC + 16 + r]));
-        }
+      for (int y = 0; y < TEAMS; ++y) mx = fmaxf(mx, s_part[y * PART + r]);
+      const float ref = mx == kNegInf ? 0.0f : mx;
+      s_factor[threadIdx.x] = fast_exp2(__fsub_rn(s_part[x * PART + r], ref));
+      if (x == 0 && store) {
+#pragma unroll 1
+        for (int y = 0; y < TEAMS; ++y)
+          sum = __fmaf_rn(s_part[y * PART + 16 + r], fast_exp2(__fsub_rn(s_part[y * PART + r], ref)), sum);
         rec[r] = mx;
-        rec[16 + r] = l;
+        rec[16 + r] = sum;
       }
     }
-    left -= n_tiles;
-    tile_lo = 0;
-    if (++h == p.Hkv) {
-      h = 0;
-      ++b;
+    __syncthreads();
+    if (store) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < p.R * (D / 4); i += blockDim.x) {
+        const int r = i / (D / 4), e = i % (D / 4) * 4;  // elements e .. e + 3 of row r
+        const int in = e % DH, at = r * RS + (e - in) + 16 * (in % L::EV / 2) + 2 * (in / L::EV);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int x = 0; x < TEAMS; ++x) {
+          const float f = s_factor[x * 16 + r];
+          const float2 u = *reinterpret_cast<const float2*>(s_part + x * PART + 32 + at);
+          const float2 v = *reinterpret_cast<const float2*>(s_part + x * PART + 32 + at + 16);
+          o.x = __fmaf_rn(u.x, f, o.x);
+          o.y = __fmaf_rn(u.y, f, o.y);
+          o.z = __fmaf_rn(v.x, f, o.z);
+          o.w = __fmaf_rn(v.y, f, o.w);
+        }
+        *reinterpret_cast<float4*>(rec + 32 + r * D + e) = o;
+      }
     }
+    __syncthreads();  // the merge area is free again
   }
 }
 
@@ -485,7 +562,9 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
 template <int D, int VB, int KMODE, int NT>
 struct SpanFew {
   using SM = AttnSmem<D, KeySpec<KMODE>::B, VB, NT>;
-  static constexpr int SMEM = SM::SMEM + 16;
+  static constexpr int TEAMS = SM::NW / AttnSplit<D>::SPL;
+  static constexpr int MERGE = TEAMS * (32 + 16 * (D + 4) + 16) * 4;
+  static constexpr int SMEM = SM::WORK + (SM::RING > MERGE ? SM::RING : MERGE);
   static int per_sm() {
     if (allow_smem<span_few_kernel<D, VB, KMODE, NT>>(SMEM) != cudaSuccess) return 1;
     static std::atomic<int> known{0};

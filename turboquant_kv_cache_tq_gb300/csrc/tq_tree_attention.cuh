@@ -943,11 +943,11 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
   const uint32_t bars = sm + S::C_OFF;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   switch (p.vb) {
-    case 2: fill_value_table<2>(smem + S::T_OFF); break;
-    case 3: fill_value_table<3>(smem + S::T_OFF); break;
-    case 4: fill_value_table<4>(smem + S::T_OFF); break;
-    case 5: fill_value_table<5>(smem + S::T_OFF); break;
-    default: fill_value_table<8>(smem + S::T_OFF); break;
+    case 2: fill_value_rows<2>(smem + S::T_OFF); break;
+    case 3: fill_value_rows<3>(smem + S::T_OFF); break;
+    case 4: fill_value_rows<4>(smem + S::T_OFF); break;
+    case 5: fill_value_rows<5>(smem + S::T_OFF); break;
+    default: fill_value_rows<8>(smem + S::T_OFF); break;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
