@@ -398,6 +398,11 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
     s.slots = p.slots;
     s.copies = p.copies;
   }
+  // two passes run side by side, unless one reads narrow pieces (through L1)
+  if (prefix && passes[0].bulk && passes[1].bulk) {
+    passes[1].order = 1;
+    passes[0].order = 2;
+  }
   o.lens = lens;
   o.left_pad = left_pad;
   o.count = count;

@@ -49,8 +49,22 @@ struct SpanPass {
   int bulk;           // every tile of the cache starts on 16 bytes in every buffer (few rows: and ends inside it)
   float scale_log2;   // scale * log2(e); rows by the 128: its magnitude
   int negate;         // rows by the 128: scale < 0
+  int order;          // 1, 2: the first, second of two passes that run side by side (0: alone)
 
   __device__ __forceinline__ bool alone() const { return bulk; }
+  // A kernel's place in the stream. Of two passes that run side by side the first
+  // lets the second start only when all that came before this call is done, and the
+  // second starts without a wait: its inputs are written (they are read from L2, as
+  // nothing says that this SM's L1 knows of them) and its scratch is free. It waits for the
+  // first before it ends, so whatever waits for it has waited for both.
+  __device__ __forceinline__ void begin() const {
+    if (order != 1) pdl_launch_dependents();
+    if (order != 2) pdl_wait();
+    if (order == 1) pdl_launch_dependents();
+  }
+  __device__ __forceinline__ void end() const {
+    if (order == 2) pdl_wait();
+  }
   __device__ __forceinline__ long long query(int r) const {
     const int o = r / in;
     return static_cast<long long>(r - o * in) * in_step + static_cast<long long>(o) * out_step;
@@ -77,7 +91,9 @@ struct SpanTiles {
   __device__ __forceinline__ static int tiles(int from, int to) { return to > from ? (to - from + TT - 1) / TT : 0; }
   __device__ __forceinline__ SpanTiles() {}
   __device__ __forceinline__ SpanTiles(const SpanPass& p, int b, int r0, int r1) {
-    row_range(p.lens, p.share > 0 ? nullptr : p.left_pad, b, p.T, lo, hi);
+    // (read from L2: see begin)
+    hi = p.lens != nullptr ? min(max(__ldcg(p.lens + b), 0), p.T) : p.T;
+    lo = p.share == 0 && p.left_pad != nullptr ? min(max(__ldcg(p.left_pad + b), 0), hi) : 0;
     s2 = n2 = 0;
     if (p.share > 0) {  // all rows see all of it
       first = p0 = p1 = hi - 1;
@@ -86,7 +102,7 @@ struct SpanTiles {
       n1 = tiles(0, hi);
       return;
     }
-    const int count = p.count != nullptr ? min(max(p.count[b], 0), p.N) : p.N;
+    const int count = p.count != nullptr ? min(max(__ldcg(p.count + b), 0), p.N) : p.N;
     first = hi - count;
     sinks = lo + min(p.sinks, hi - lo);
     const int n0 = p.by_token() ? r0 / p.G : 0, n_last = p.by_token() ? (r1 - 1) / p.G : p.N - 1;
@@ -160,8 +176,10 @@ struct SpanOutput {
   float rot_scale;
 };
 
-// What a change of segments costs, in tiles (see cut_line).
-constexpr int kFewTurn = 16;
+// What a change of segments costs a pass of few rows, in tiles of 16 tokens (see
+// few_range; 8 / 16 / 24: 8 sequences x 8 heads x 8192 tokens, 3-bit values 32 / 35 /
+// 36 us, 32 x 8 x 4160 tokens 74 / 74 / 74).
+constexpr int kFewTurn = 8;
 
 // Launches, translation units of their own. launch_span_few: at most 8 NT rows a kv
 // head (NT: 1 or 2) and `tiles` tiles of 16 tokens in all; sets p.grid.

@@ -63,6 +63,12 @@ struct TreeParams {
   float rot_scale;
   // whether one lane of a loading warp loads alone, by bulk copies
   __device__ __forceinline__ bool alone() const { return bulk && bulk_tree; }
+  // the kernel's place in the stream
+  __device__ __forceinline__ void begin() const {
+    pdl_launch_dependents();
+    pdl_wait();
+  }
+  __device__ __forceinline__ void end() const {}
 };
 
 template <int D, bool F32>
@@ -633,6 +639,10 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
         if constexpr (TREE) return x;
         else return p.query(x);
       };
+      auto load = [&](long long i) {
+        if constexpr (TREE) return src[i];
+        else return __ldcg(src + i);
+      };
       // row x of the warp's 32, or -1
       auto row_at = [&](int x) {
         const int at = (warp % QUADS) * 32 + x;
@@ -652,7 +662,7 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
         for (int k = 0; k < STEP / 16; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            u[k][i] = from[i] >= 0 ? src[static_cast<long long>(from[i]) * (D / 8) + c / 4 + 4 * k + (lane & 3)]
+            u[k][i] = from[i] >= 0 ? load(static_cast<long long>(from[i]) * (D / 8) + c / 4 + 4 * k + (lane & 3))
                                    : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int k = 0; k < STEP / 16; ++k) {
@@ -675,7 +685,7 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
 #pragma unroll 8
         for (int x = 0; x < 32; ++x) {
           const int r2 = row_at(x);
-          const uint4 u = r2 >= 0 ? src[place(r2) * (D / 8) + S::QT / 8 + lane]
+          const uint4 u = r2 >= 0 ? load(place(r2) * (D / 8) + S::QT / 8 + lane)
                                   : make_uint4(0u, 0u, 0u, 0u);
           sts128(sm + S::Q_OFF + (lane >> 3) * (128 * 128) + (warp * 32 + x) * 128 + (((lane ^ x) & 7) << 4), u.x, u.y,
                  u.z, u.w);
@@ -989,8 +999,7 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
   // theirs that took it first, and then waited for this kernel to end, would
   // wait for ever.
   __syncthreads();
-  pdl_launch_dependents();
-  pdl_wait();
+  p.begin();
   if (warp == 0) {
     cut_line<true, !std::is_same_v<P, TreeParams>>([&](int b) { return RowsWalk<D, F32, P>::row_tiles(p, b); },
                                                    RowsWalk<D, F32, P>::lines(p), p.HH, S::TURN, lane,
@@ -1060,6 +1069,7 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
     tmem_fence_after();
     tmem_free(*reinterpret_cast<const uint32_t*>(ctl + kcTmem), 512);
   }
+  p.end();
 }
 
 // An output row from its merged result: the division, the Hadamard butterflies, /
