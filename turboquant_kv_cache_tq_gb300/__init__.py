@@ -57,6 +57,9 @@ class TQError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libtq.so (raises if it has not been built)."""
     global _lib
+    loaded = _lib
+    if loaded is not None:
+        return loaded
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -397,6 +400,7 @@ class TQPackedCache(ctypes.Structure):
 
 
 _BUFFERS = ("k_codes", "k_scales", "k_zeros", "v_codes", "v_scales")
+_INT32, _FLOAT32, _BFLOAT16 = torch.int32, torch.float32, torch.bfloat16
 
 
 def _refuse_cache(cache, B, H, D, k_bits, v_bits, device, names):
@@ -443,17 +447,17 @@ def _int_ptr(t, shape, what, device):
     """Device pointer of an optional int32 tensor of a given shape."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s must be a contiguous int32 tensor %s on %s" % (what, list(shape), device))
-    return t.data_ptr()
+    if t.dtype is _INT32 and t.shape == shape and t.is_contiguous() and t.get_device() == device.index:
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous int32 tensor %s on %s" % (what, list(shape), device))
 
 
 def _float_ptr(t, shape, what, device):
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s must be a contiguous float32 tensor %s on %s" % (what, list(shape), device))
-    return t.data_ptr()
+    if t.dtype is _FLOAT32 and t.shape == shape and t.is_contiguous() and t.get_device() == device.index:
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous float32 tensor %s on %s" % (what, list(shape), device))
 
 
 @contextlib.contextmanager
@@ -666,9 +670,11 @@ class TQRows(ctypes.Structure):
 
 def _rows(t, shape, dtype, what, device):
     """A [B,H,N,D] tensor with contiguous rows as the library takes it."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or (t.stride(3) != 1 and t.numel()):
-        raise ValueError("%s must be a %s tensor %s on %s with contiguous rows" % (what, dtype, list(shape), device))
-    return TQRows(t.data_ptr(), *t.stride()[:3])
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index:
+        b, h, n, d = t.stride()
+        if d == 1 or not t.numel():
+            return TQRows(t.data_ptr(), b, h, n)
+    raise ValueError("%s must be a %s tensor %s on %s with contiguous rows" % (what, dtype, list(shape), device))
 
 
 def rope_tables(rot_dim: int, length: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
@@ -716,24 +722,28 @@ def tq_append_kv(k: torch.Tensor, v: torch.Tensor, cache: dict, lens, k_bits: in
     left_pad + n). q [B,Hq,N,D]: queries turned alike into q_out. Tokens past the
     capacity are dropped. Returns (q_out or None, the new lengths)."""
     dev = k.device
-    if k.dim() != 4 or k.dtype not in _DTYPE:
+    kind = _DTYPE.get(k.dtype)
+    if k.dim() != 4 or kind is None:
         raise ValueError("k must be a [B,Hkv,N,D] float32 or bfloat16 tensor")
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
             return tq_append_kv(k, v, cache, lens, k_bits, k_signed, v_bits, cos, sin, interleaved, q, positions,
                                 left_pad, count, q_out, new_lens)
-    B, Hkv, N, D = k.shape
+    shape, dtype = k.shape, k.dtype
+    B, Hkv, N, D = shape
     cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
-    kr, vr = _rows(k, k.shape, k.dtype, "k", dev), _rows(v, k.shape, k.dtype, "v", dev)
+    kr, vr = _rows(k, shape, dtype, "k", dev), _rows(v, shape, dtype, "v", dev)
     Hq, qr, q_ptr = 0, None, None
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be a [B,Hq,N,D] tensor")
         Hq = q.shape[1]
-        qr = ctypes.byref(_rows(q, (B, Hq, N, D), k.dtype, "q", dev))
+        shape = (B, Hq, N, D)
+        qr = ctypes.byref(_rows(q, shape, dtype, "q", dev))
         if q_out is None:
-            q_out = torch.empty((B, Hq, N, D), dtype=k.dtype, device=dev)
-        elif q_out.dtype is not k.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.device != dev:
+            q_out = torch.empty(shape, dtype=dtype, device=dev)
+        elif (q_out.dtype is not dtype or q_out.shape != shape or not q_out.is_contiguous()
+              or q_out.get_device() != dev.index):
             raise ValueError("q_out must be a contiguous [B,Hq,N,D] tensor of q's dtype on q's device")
         q_ptr = q_out.data_ptr()
     elif q_out is not None:
@@ -743,21 +753,26 @@ def tq_append_kv(k: torch.Tensor, v: torch.Tensor, cache: dict, lens, k_bits: in
         if cos is None or sin is None or cos.dim() != 2:
             raise ValueError("cos and sin go together, [length, R / 2] each")
         length, R = cos.shape[0], 2 * cos.shape[1]
+    one = (B,)
+    new_ptr = None
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_lens = torch.empty(one, dtype=_INT32, device=dev)
+        new_ptr = new_lens.data_ptr()
     st = lib().tq_append_kv(
-        qr, ctypes.byref(kr), ctypes.byref(vr), _DTYPE[k.dtype], B, Hq, Hkv, N, D,
+        qr, ctypes.byref(kr), ctypes.byref(vr), kind, B, Hq, Hkv, N, D,
         _float_ptr(cos, (length, R // 2), "cos", dev), _float_ptr(sin, (length, R // 2), "sin", dev), length, R,
-        int(bool(interleaved)), _int_ptr(positions, (B, N), "positions", dev), _int_ptr(lens, (B,), "lens", dev),
-        _int_ptr(left_pad, (B,), "left_pad", dev), _int_ptr(count, (B,), "count", dev), ctypes.byref(cv), int(k_bits),
-        int(bool(k_signed)), int(v_bits), q_ptr, _int_ptr(new_lens, (B,), "new_lens", dev), _current_stream(dev))
-    _check(st, "tq_append_kv")
+        1 if interleaved else 0, _int_ptr(positions, (B, N), "positions", dev), _int_ptr(lens, one, "lens", dev),
+        _int_ptr(left_pad, one, "left_pad", dev), _int_ptr(count, one, "count", dev), ctypes.byref(cv), int(k_bits),
+        1 if k_signed else 0, int(v_bits), q_ptr, new_ptr or _int_ptr(new_lens, one, "new_lens", dev),
+        _current_stream(dev))
+    if st:
+        _check(st, "tq_append_kv")
     return q_out, new_lens
 
 
 def tq_window_attention_workspace_size(B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
     """Bytes of scratch tq_window_attention needs (on the current device)."""
-    r = int(lib().tq_window_attention_workspace_size(int(B), int(Hq), int(Hkv), int(N), int(D)))
+    r = lib().tq_window_attention_workspace_size(B, Hq, Hkv, N, D)
     if r < 0:
         raise TQError(-r, "tq_window_attention_workspace_size")
     return r
@@ -765,26 +780,32 @@ def tq_window_attention_workspace_size(B: int, Hq: int, Hkv: int, N: int, D: int
 
 def tq_prefix_attention_workspace_size(Bp: int, B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
     """Bytes of scratch tq_prefix_attention needs (on the current device)."""
-    r = int(lib().tq_prefix_attention_workspace_size(int(Bp), int(B), int(Hq), int(Hkv), int(N), int(D)))
+    r = lib().tq_prefix_attention_workspace_size(Bp, B, Hq, Hkv, N, D)
     if r < 0:
         raise TQError(-r, "tq_prefix_attention_workspace_size")
     return r
 
 
-def _attention_outputs(q, out_dtype, out, lse, workspace, need, dev):
-    """The outputs and the scratch of an attention call, allocated where not given."""
-    B, Hq, N, _ = q.shape
+def _attention_outputs(q, out_dtype, out, lse, workspace, size, sizes, dev):
+    """The outputs and the scratch of an attention call, allocated where not
+    given, and their pointers and the scratch's bytes. size(*sizes): what it needs."""
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        out = torch.empty_like(q, dtype=out_dtype)
     elif out.dtype != out_dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous [B,Hq,N,D] tensor of out_dtype on q's device")
     if lse is None:
-        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=dev)
+        lse = torch.empty(q.shape[:3], dtype=_FLOAT32, device=dev)
+        lse_ptr = lse.data_ptr()
+    else:
+        lse_ptr = _float_ptr(lse, q.shape[:3], "lse", dev)
     if workspace is None:
-        workspace = torch.empty(max(need(), 16), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        need = max(size(*sizes), 16)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device == dev and workspace.is_contiguous():
+        need = workspace.numel() * workspace.element_size()
+    else:
         raise ValueError("workspace must be a contiguous tensor on q's device")
-    return out, lse, workspace
+    return out, lse, workspace, out.data_ptr(), lse_ptr, workspace.data_ptr(), need
 
 
 def tq_window_attention(q: torch.Tensor, cache: dict, T: int, k_bits: int, k_signed: bool, v_bits: int, window: int,
@@ -798,7 +819,7 @@ def tq_window_attention(q: torch.Tensor, cache: dict, T: int, k_bits: int, k_sig
     lse [B,Hq,N] fp32); absent queries give zeros and -inf. workspace: a uint8
     device tensor of at least tq_window_attention_workspace_size bytes (allocated
     when None)."""
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or not q.is_contiguous():
+    if q.dtype is not _BFLOAT16 or q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B,Hq,N,D] bfloat16 tensor")
     if out_dtype not in _DTYPE:
         raise ValueError("out_dtype must be float32 or bfloat16")
@@ -810,15 +831,16 @@ def tq_window_attention(q: torch.Tensor, cache: dict, T: int, k_bits: int, k_sig
     B, Hq, N, D = q.shape
     Hkv = cache["k_codes"].shape[1]
     cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
-    out, lse, workspace = _attention_outputs(q, out_dtype, out, lse, workspace,
-                                             lambda: tq_window_attention_workspace_size(B, Hq, Hkv, N, D), dev)
+    out, lse, workspace, out_ptr, lse_ptr, ws_ptr, ws_bytes = _attention_outputs(
+        q, out_dtype, out, lse, workspace, tq_window_attention_workspace_size, (B, Hq, Hkv, N, D), dev)
+    one = (B,)
     st = lib().tq_window_attention(
-        q.data_ptr(), B, Hq, N, ctypes.byref(cv), Hkv, int(T), D, int(k_bits), int(bool(k_signed)), int(v_bits),
-        _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
-        _int_ptr(count, (B,), "count", dev), int(window), int(sinks), D ** -0.5 if scale is None else float(scale),
-        out.data_ptr(), _DTYPE[out_dtype], _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _current_stream(dev))
-    _check(st, "tq_window_attention")
+        q.data_ptr(), B, Hq, N, ctypes.byref(cv), Hkv, int(T), D, int(k_bits), 1 if k_signed else 0, int(v_bits),
+        _int_ptr(lens, one, "lens", dev), _int_ptr(left_pad, one, "left_pad", dev), _int_ptr(count, one, "count", dev),
+        int(window), int(sinks), D ** -0.5 if scale is None else float(scale), out_ptr, _DTYPE[out_dtype], lse_ptr,
+        ws_ptr, ws_bytes, _current_stream(dev))
+    if st:
+        _check(st, "tq_window_attention")
     return out, lse
 
 
@@ -846,16 +868,17 @@ def tq_prefix_attention(q: torch.Tensor, prefix: dict, P: int, cache: dict, T: i
     Bp, Hkv = prefix["k_codes"].shape[:2]
     pv = _packed(prefix, Bp, Hkv, D, k_bits, v_bits, dev)
     cv = _packed(cache, B, Hkv, D, k_bits, v_bits, dev)
-    out, lse, workspace = _attention_outputs(q, out_dtype, out, lse, workspace,
-                                             lambda: tq_prefix_attention_workspace_size(Bp, B, Hq, Hkv, N, D), dev)
+    out, lse, workspace, out_ptr, lse_ptr, ws_ptr, ws_bytes = _attention_outputs(
+        q, out_dtype, out, lse, workspace, tq_prefix_attention_workspace_size, (Bp, B, Hq, Hkv, N, D), dev)
+    one = (B,)
     st = lib().tq_prefix_attention(
         q.data_ptr(), B, Hq, N, ctypes.byref(pv), Bp, int(P), _int_ptr(prefix_lens, (Bp,), "prefix_lens", dev),
-        ctypes.byref(cv), Hkv, int(T), D, int(k_bits), int(bool(k_signed)), int(v_bits),
-        _int_ptr(lens, (B,), "lens", dev), _int_ptr(left_pad, (B,), "left_pad", dev),
-        _int_ptr(count, (B,), "count", dev), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-        _DTYPE[out_dtype], _float_ptr(lse, (B, Hq, N), "lse", dev), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _current_stream(dev))
-    _check(st, "tq_prefix_attention")
+        ctypes.byref(cv), Hkv, int(T), D, int(k_bits), 1 if k_signed else 0, int(v_bits), _int_ptr(lens, one, "lens", dev),
+        _int_ptr(left_pad, one, "left_pad", dev), _int_ptr(count, one, "count", dev),
+        D ** -0.5 if scale is None else float(scale), out_ptr, _DTYPE[out_dtype], lse_ptr, ws_ptr, ws_bytes,
+        _current_stream(dev))
+    if st:
+        _check(st, "tq_prefix_attention")
     return out, lse
 
 

@@ -44,26 +44,25 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
   const int rows = p.B * p.Hq * p.N, row0 = blockIdx.x * (4 / W) + warp / W, row = min(row0, rows - 1);
   const int b = row / (p.Hq * p.N), in_b = row - b * (p.Hq * p.N), hq = in_b / p.N, n = in_b - hq * p.N;
   const int h = hq / p.G, g = hq - h * p.G;
-  int lo, hi;
-  row_range(p.lens, p.left_pad, b, p.T, lo, hi);
-  const int count = p.count != nullptr ? min(max(p.count[b], 0), p.N) : p.N;
-  const bool present = n < count && hi - count + n >= lo;
-  float m = kNegInf, l = 0.0f, o[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = 0.0f;
-#pragma unroll 1
-  for (int k = 0; k < p.sources && present; ++k) {
-    const SpanSource& s = p.from[k];
+  // Where the row's records are: even lanes find those of the first pass, odd lanes
+  // the second's (one code for both, as instructions that run once are paid in
+  // fetches, and one wait). From here on the parts of both passes are one list.
+  const SpanSource& s = p.from[lane & (p.sources - 1)];
+  const int half = lane >> 4, hh = h * s.halves + (s.halves == 1 ? 0 : half);
+  const float* recs;
+  int rec_floats, rl, mine;  // mine: the pass's parts
+  {
     const int cb = b / s.share, r = (b - cb * s.share) * s.s_step + g * s.g_step + n * s.n_step;
-    const int rb = r / s.rows, rl = r - rb * s.rows, x = cb * s.RB + rb, lines = s.lines;
-    const int half = s.halves == 1 ? 0 : lane >> 4;
-    const int hh = h * s.halves + half;
-    // the blocks that hold the segment's first and last tile
-    const int turn = s.cut[0];
-    const unsigned per = s.cut[1], more = s.cut[2];
+    const int rb = r / s.rows, x = cb * s.RB + rb;
+    rl = r - rb * s.rows;
+    const unsigned turn = s.cut[0], per = max(s.cut[1], 1), more = s.cut[2];
     const int before = s.cut[kCutRows + x], tiles = s.cut[kCutRows + x + 1] - before;
-    if (tiles == 0) continue;
-    const unsigned place = static_cast<unsigned>(before + turn * s.cut[kCutRows + lines + 1 + x]) * s.HH +
+    int lo, hi;
+    row_range(p.lens, p.left_pad, b, p.T, lo, hi);
+    const int count = p.count != nullptr ? min(max(p.count[b], 0), p.N) : p.N;
+    const bool present = n < count && hi - count + n >= lo;
+    // the blocks that hold the segment's first and last tile
+    const unsigned place = (before + turn * s.cut[kCutRows + s.lines + 1 + x]) * s.HH +
                            static_cast<unsigned>(hh) * (tiles + turn) + turn;
     auto block_of = [&](unsigned y) {
       const unsigned long_part = more * (per + 1);
@@ -71,73 +70,87 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
     };
     const int c0 = block_of(place), c1 = block_of(place + tiles - 1);
     const long long slot = static_cast<long long>(c0) + static_cast<long long>(x) * s.HH + hh;
-    int parts = (c1 - c0 + 1) * s.copies;
-    if (!TQ_CHECK(slot + (c1 - c0) < s.n_recs, p.err)) parts = 0;
-    const int width = D / s.halves;
-    const long long rec_floats = static_cast<long long>(s.slots) * (width + 2);
-    const float* recs = s.recs + slot * rec_floats;
-    const int shift = s.copies - 1, at = (lane - (s.halves == 1 ? 0 : half * 16)) * E;
-    auto load = [&](int y, float (&u)[E]) {
-      const float* src = recs + (y >> shift) * rec_floats + 2 * s.slots +
-                         static_cast<long long>((y & shift) * s.rows + rl) * width + at;
+    mine = present && tiles > 0 ? (c1 - c0 + 1) * s.copies : 0;
+    if (!TQ_CHECK(mine == 0 || slot + (c1 - c0) < s.n_recs, p.err)) mine = 0;
+    rec_floats = s.slots * (D / s.halves + 2);
+    recs = s.recs + slot * rec_floats;
+  }
+  const int group = D == 512 ? lane & 16 : 0;  // the lanes that look at the parts of this lane's half
+  const int parts0 = __shfl_sync(kFull, mine, group);
+  const int parts = parts0 + (p.sources > 1 ? __shfl_sync(kFull, mine, group + 1) : 0);
+  int most = parts;
+  if constexpr (D == 512) most = max(most, __shfl_xor_sync(kFull, most, 16));
+  float m = kNegInf, l = 0.0f, o[E];
 #pragma unroll
-      for (int i = 0; i < E; i += V) {
-        if constexpr (V == 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + i);
-          u[i] = v.x; u[i + 1] = v.y;
-        } else {
-          const float4 v = *reinterpret_cast<const float4*>(src + i);
-          u[i] = v.x; u[i + 1] = v.y; u[i + 2] = v.z; u[i + 3] = v.w;
+  for (int i = 0; i < E; ++i) o[i] = 0.0f;
+  // LANES parts at a time: every lane looks at one maximum and sum, then all take
+  // the values with the factors known (no result waits for the last one).
+#pragma unroll 1
+  for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
+    const int part = s0 + (lane % LANES) * W, k = part >= parts0 ? 1 : 0, y = part - (k ? parts0 : 0);
+    const SpanSource& f = p.from[k];
+    const int shift = f.copies - 1, from = group + k;
+    const int at = __shfl_sync(kFull, rl, from) + (y & shift) * f.rows;
+    const float* rec = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(recs), from)) +
+                       static_cast<long long>(y >> shift) * __shfl_sync(kFull, rec_floats, from);
+    const float* values = rec + 2 * f.slots + static_cast<long long>(at) * (D / f.halves);
+    float m2 = kNegInf, l2 = 0.0f;
+    if (part < parts) {
+      m2 = rec[at];
+      l2 = rec[f.slots + at];
+    }
+    auto load = [&](int z, float (&u)[E]) {
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(values), group + z));
+      // (a record of half the values has them from its own first on)
+      const int first = D == 512 && p.from[s0 + z * W >= parts0 ? 1 : 0].halves == 2 ? (lane & 15) * E : lane * E;
+      if (s0 + z * W < parts) {
+#pragma unroll
+        for (int i = 0; i < E; i += V) {
+          if constexpr (V == 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + first + i);
+            u[i] = v.x; u[i + 1] = v.y;
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(src + first + i);
+            u[i] = v.x; u[i + 1] = v.y; u[i + 2] = v.z; u[i + 3] = v.w;
+          }
         }
       }
     };
-    int most = parts;
-    if constexpr (D == 512) most = max(parts, __shfl_xor_sync(kFull, parts, 16));
+    // the first AHEAD results' values meanwhile
+    float u[AHEAD][E];
+#pragma unroll
+    for (int z = 0; z < AHEAD; ++z) load(z, u[z]);
+    float mn = m2;
+#pragma unroll
+    for (int z = LANES / 2; z > 0; z >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, z));
+    mn = fmaxf(mn, m);
+    const float fa = m == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m2, mn));
+    float add = __fmul_rn(l2, fb);
+#pragma unroll
+    for (int z = LANES / 2; z > 0; z >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, z));
+    l = __fmaf_rn(l, fa, add);
+    m = mn;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
+    const int n_here = min(LANES, (most - s0 + W - 1) / W);
+    // (a part that saw no key is left out, whatever its values are; nor does one
+    // past the end count)
+    auto add_part = [&](int z, const float (&v)[E]) {
+      const float x = __shfl_sync(kFull, fb, group + z);
+      if (x != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(v[i], x, o[i]);
+      }
+    };
+#pragma unroll
+    for (int z = 0; z < AHEAD; ++z) add_part(z, u[z]);
 #pragma unroll 1
-    for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
-      const int mine = s0 + (lane % LANES) * W;
-      float m2 = kNegInf, l2 = 0.0f;
-      if (mine < parts) {
-        const float* rec = recs + (mine >> shift) * rec_floats + (mine & shift) * s.rows + rl;
-        m2 = rec[0];
-        l2 = rec[s.slots];
-      }
-      // the first AHEAD results' values meanwhile
-      float u[AHEAD][E];
+    for (int z = AHEAD; z < n_here; z += AHEAD) {
 #pragma unroll
-      for (int y = 0; y < AHEAD; ++y)
-        if (s0 + y * W < parts) load(s0 + y * W, u[y]);
-      float mn = m2;
+      for (int a = 0; a < AHEAD; ++a) load(min(z + a, LANES - 1), u[a]);
 #pragma unroll
-      for (int y = LANES / 2; y > 0; y >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, y));
-      mn = fmaxf(mn, m);
-      const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
-      float add = __fmul_rn(l2, fb);
-#pragma unroll
-      for (int y = LANES / 2; y > 0; y >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, y));
-      l = __fmaf_rn(l, fa, add);
-      m = mn;
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
-      const int n_here = min(LANES, (most - s0 + W - 1) / W);
-      // (a part that saw no key is left out, whatever its values are; nor does one
-      // past the end count)
-      auto add_part = [&](int y, const float (&v)[E]) {
-        const float f = __shfl_sync(kFull, fb, (lane & ~(LANES - 1)) + y);
-        if (f != 0.0f) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(v[i], f, o[i]);
-        }
-      };
-#pragma unroll
-      for (int y = 0; y < AHEAD; ++y)
-        if (y < n_here) add_part(y, u[y]);
-#pragma unroll 4
-      for (int y = AHEAD; y < n_here; ++y) {
-        float v[E];
-        if (s0 + y * W < parts) load(s0 + y * W, v);
-        add_part(y, v);
-      }
+      for (int a = 0; a < AHEAD; ++a)
+        if (z + a < n_here) add_part(z + a, u[a]);
     }
   }
   if constexpr (W > 1) {
@@ -171,21 +184,33 @@ struct SpanPlan {
   bool few;
 };
 
-// The most query rows a kv head for which the decode in registers is taken.
-constexpr int kFewRows = kAttnRows;
+// Whether a pass of `rows` query rows a kv head over `tiles` tiles of 16 tokens (of
+// one row block, all heads and cache rows) decodes in registers, 16 rows at a time:
+// the kernel of 128 rows starts and ends more slowly, but decodes a tile once. Both
+// sides at 8 heads (registers / 128 rows): 32 rows, head_dim 128, 2048 tokens 14.7 /
+// 16.9 us, 8192 24 / 21; 64 rows, 512 tokens 14.3 / 15.4, 2048 18.5 / 17.5; 32 rows, 64,
+// 8192 17.6 / 19.3, 32768 50 / 33; 256, 2048 19.5 / 20.5, 8192 38 / 31. At head_dim 512,
+// where 128 rows decode the keys once for each half of the values: 32 rows, 32768 tokens
+// 203 / 294; 64 rows, 2048 50 / 52, 8192 116 / 102. Above 128 rows never (which the
+// scratch is sized by).
+constexpr int kFewRows = kAttnRows, kFewMost = 128;
+bool span_few(int64_t rows, int64_t tiles, int64_t D) {
+  if (rows <= kFewRows || (D == 512 && rows <= 2 * kFewRows)) return true;
+  return rows <= kFewMost && tiles * ((rows + kFewRows - 1) / kFewRows) < (D == 512 ? 5000 : 450000 / D);
+}
 
-// B rows of the cache, `rows` query rows a kv head in each, at most T tokens. (Short
-// sequences and fp32 outputs need no more scratch than long ones and bf16.)
-bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool f32, SpanPlan* t) {
+// B rows of the cache, `rows` query rows a kv head in each. (Long sequences and bf16
+// outputs need the most scratch.)
+bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool f32, bool few, SpanPlan* t) {
   const long long lim = 0x7fffffffLL;
-  t->few = rows <= kFewRows;
+  t->few = few;
   t->R = rows;
   t->halves = !t->few && D == 512 ? 2 : 1;
   t->HH = Hkv * t->halves;
   if (t->few) {
     t->TT = kAttnTile;
-    t->RB = t->copies = 1;
-    t->rows = t->slots = kAttnRows;
+    t->copies = 1;
+    t->slots = kAttnRows;
   } else {
     auto tile = [&](auto f) {
       constexpr bool F = decltype(f)::value;
@@ -193,9 +218,10 @@ bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool 
                                                                                : TreeShape<512, F>::TT;
     };
     t->TT = f32 ? tile(std::true_type{}) : tile(std::false_type{});
-    t->RB = (rows + kTreeRows - 1) / kTreeRows;
-    t->rows = (rows + t->RB - 1) / t->RB;
   }
+  const int block = few ? kAttnRows : kTreeRows;
+  t->RB = (rows + block - 1) / block;
+  t->rows = (rows + t->RB - 1) / t->RB;
   if (t->RB > lim / t->HH || (B > 0 && t->RB * t->HH > lim / B)) return false;
   t->lines = B * t->RB;
   if (!t->few) {
@@ -210,6 +236,15 @@ bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool 
   return true;
 }
 
+// The scratch of a pass, whatever its length and output type.
+bool span_bytes(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t* bytes) {
+  SpanPlan few{}, many{};
+  if (rows <= kFewMost && !span_plan(B, Hkv, rows, D, 1LL << 40, false, true, &few)) return false;
+  if (rows > kFewRows && !span_plan(B, Hkv, rows, D, 1LL << 40, false, false, &many)) return false;
+  *bytes = std::max(few.bytes, many.bytes);
+  return true;
+}
+
 // The passes (the prefix first), then the combine kernel.
 template <int D>
 cudaError_t launch_span(SpanPass* passes, const SpanPlan* plans, int64_t reach, int64_t P, const SpanOutput& o, cudaStream_t s) {
@@ -219,7 +254,7 @@ cudaError_t launch_span(SpanPass* passes, const SpanPlan* plans, int64_t reach, 
     const SpanPlan& t = plans[k];
     cudaError_t e;
     const long long tiles = t.lines * t.HH * ((k ? P : reach) / t.TT + 2);
-    if (t.few) e = p.R <= 8 ? launch_span_few<D, 1>(p, tiles, s) : launch_span_few<D, 2>(p, tiles, s);
+    if (t.few) e = p.rows <= 8 ? launch_span_few<D, 1>(p, tiles, s) : launch_span_few<D, 2>(p, tiles, s);
     else if (o.out_f32) e = launch_span_rows<D, true>(p, s);
     else e = launch_span_rows<D, false>(p, s);
     if (e != cudaSuccess) return e;
@@ -306,8 +341,11 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
   // block of rows sees a window and what its tokens add to it)
   const int64_t reach = window < T ? window + sinks + N + 64 < T ? window + sinks + N + 64 : T : T;
   SpanPlan plans[2];
-  span_plan(B, Hkv, G * N, D, reach, f32, &plans[0]);
-  if (prefix) span_plan(Bp, Hkv, share * G * N, D, P, f32, &plans[1]);
+  auto plan = [&](int64_t rows_of, int64_t rows, int64_t tokens, SpanPlan* t) {
+    span_plan(rows_of, Hkv, rows, D, tokens, f32, span_few(rows, rows_of * Hkv * (tokens / kAttnTile + 1), D), t);
+  };
+  plan(B, G * N, reach, &plans[0]);
+  if (prefix) plan(Bp, share * G * N, P, &plans[1]);
   SpanPass passes[2]{};
   SpanOutput o{};
   char* scratch = static_cast<char*>(workspace);
@@ -346,7 +384,7 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
       s.s_step = p.in;
       s.g_step = p.N;
       s.n_step = 1;
-    } else if (t.few) {  // head after head, as they lie in memory
+    } else if (t.few && t.RB == 1) {  // head after head, as they lie in memory
       p.in = p.R;
       p.in_step = 1;
       s.share = 1;
@@ -435,9 +473,8 @@ using namespace tq;
 extern "C" int64_t tq_window_attention_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
   const tq_status st = span_sizes(B, Hq, Hkv, N, D, 1);
   if (st != TQ_OK) return -static_cast<int64_t>(st);
-  SpanPlan t;
-  if (!span_plan(B, Hkv, Hq / Hkv * N, D, 1LL << 40, false, &t)) return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
-  return t.bytes;
+  int64_t bytes = 0;
+  return span_bytes(B, Hkv, Hq / Hkv * N, D, &bytes) ? bytes : -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
 }
 
 extern "C" int64_t tq_prefix_attention_workspace_size(int64_t Bp, int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
@@ -445,11 +482,10 @@ extern "C" int64_t tq_prefix_attention_workspace_size(int64_t Bp, int64_t B, int
   const int64_t share = B > 0 ? B / Bp : 1;
   const tq_status st = span_sizes(B, Hq, Hkv, N, D, share);
   if (st != TQ_OK) return -static_cast<int64_t>(st);
-  SpanPlan own, pre;
-  if (!span_plan(B, Hkv, Hq / Hkv * N, D, 1LL << 40, false, &own) ||
-      !span_plan(Bp, Hkv, share * (Hq / Hkv) * N, D, 1LL << 40, false, &pre))
+  int64_t own = 0, pre = 0;
+  if (!span_bytes(B, Hkv, Hq / Hkv * N, D, &own) || !span_bytes(Bp, Hkv, share * (Hq / Hkv) * N, D, &pre))
     return -static_cast<int64_t>(TQ_ERR_INVALID_ARG);
-  return own.bytes + pre.bytes;
+  return own + pre;
 }
 
 extern "C" tq_status tq_window_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const tq_packed_cache* cache,

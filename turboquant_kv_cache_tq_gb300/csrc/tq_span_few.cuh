@@ -1,4 +1,5 @@
-// A pass with at most 16 query rows a kv head: a token or two of each sequence.
+// A pass with few query rows a kv head: at most 16, a token or two of each sequence, or
+// some blocks of 16 over a cache too short for the tensor core's longer start.
 //
 // The decode of the packed bytes is the work: a tile of 16 tokens goes from the
 // bytes into the operands of mma.sync (m16n8k16: tokens x query rows) within the
@@ -24,24 +25,30 @@ namespace tq {
 // instruction fetches, some 100 cycles for eight of them: cut_line with its two
 // searches took 5.8 us here.)
 struct FewRange {
-  int b, h;
+  int x, h;                 // x: b * RB + rb (cache row, row block)
   unsigned at, left, turn;  // the place in the segment, the places still to come
 };
+
+__device__ __forceinline__ SpanTiles<kAttnTile> few_tiles(const SpanPass& p, int x) {
+  const int b = p.RB == 1 ? x : x / p.RB, r0 = (x - b * p.RB) * p.rows;
+  return SpanTiles<kAttnTile>(p, b, r0, min(r0 + p.rows, p.R));
+}
 
 __device__ __forceinline__ FewRange few_range(const SpanPass& p, int lane) {
   FewRange o;
   const bool writes = blockIdx.x == 0 && threadIdx.x < 32;
+  const int lines = p.B * p.RB;
   int sum = 0, rows = 0, n = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const bool here = b0 + lane < p.B;
-    n = here ? SpanTiles<kAttnTile>(p, b0 + lane, 0, p.R).count() : 0;
+  for (int x0 = 0; x0 < lines; x0 += 32) {
+    const bool here = x0 + lane < lines;
+    n = here ? few_tiles(p, x0 + lane).count() : 0;
     const unsigned some = __ballot_sync(kFull, n > 0);
     if (writes) {
       const int c = warp_prefix(n, lane);
       if (here) {
-        p.cut[kCutRows + b0 + lane + 1] = sum + c;
-        p.cut[kCutRows + p.B + 1 + b0 + lane + 1] = rows + __popc(some & (kFull >> (31 - lane)));
+        p.cut[kCutRows + x0 + lane + 1] = sum + c;
+        p.cut[kCutRows + lines + 1 + x0 + lane + 1] = rows + __popc(some & (kFull >> (31 - lane)));
       }
     }
     sum += __reduce_add_sync(kFull, n);
@@ -54,22 +61,22 @@ __device__ __forceinline__ FewRange few_range(const SpanPass& p, int lane) {
     p.cut[0] = static_cast<int>(o.turn);
     p.cut[1] = static_cast<int>(per);
     p.cut[2] = static_cast<int>(more);
-    p.cut[kCutRows] = p.cut[kCutRows + p.B + 1] = 0;
+    p.cut[kCutRows] = p.cut[kCutRows + lines + 1] = 0;
   }
   unsigned place = blockIdx.x * per + min(blockIdx.x, more);
   o.left = blockIdx.x < ranges ? per + (blockIdx.x < more ? 1u : 0u) : 0u;
-  o.b = o.h = 0;
+  o.x = o.h = 0;
   o.at = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < p.B && o.left > 0; b0 += 32) {
-    if (p.B > 32) n = b0 + lane < p.B ? SpanTiles<kAttnTile>(p, b0 + lane, 0, p.R).count() : 0;
+  for (int x0 = 0; x0 < lines && o.left > 0; x0 += 32) {
+    if (lines > 32) n = x0 + lane < lines ? few_tiles(p, x0 + lane).count() : 0;
     const unsigned one = n > 0 ? n + o.turn : 0, end = static_cast<unsigned>(warp_prefix(static_cast<int>(one), lane)) * p.HH;
     const unsigned who = __ballot_sync(kFull, place < end);
     if (who != 0) {
       const int from = __ffs(who) - 1;
       const unsigned length = __shfl_sync(kFull, one, from);
       place -= __shfl_sync(kFull, end, from) - length * p.HH;
-      o.b = b0 + from;
+      o.x = x0 + from;
       o.h = static_cast<int>(place / length);
       o.at = place - o.h * length;
       break;
@@ -118,12 +125,13 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
   constexpr float kBias = kMagic + (M::SIGNED ? 128.0f : 0.0f);
   constexpr float kBias16 = 1024.0f + (M::SIGNED ? 128.0f : 0.0f);
 
-  while (at0.left > 0 && at0.b < p.B) {
-    const int b = at0.b, h = at0.h;
-    const SpanTiles<kAttnTile> w(p, b, 0, p.R);
+  while (at0.left > 0 && at0.x < p.B * p.RB) {
+    const int x = at0.x, h = at0.h, b = p.RB == 1 ? x : x / p.RB;
+    const int r0 = (x - b * p.RB) * p.rows, R = min(p.rows, p.R - r0);  // the block's rows
+    const SpanTiles<kAttnTile> w(p, b, r0, r0 + R);
     if (w.count() == 0) {  // (a row without tiles has no place in the line)
       at0.h = 0;
-      ++at0.b;
+      ++at0.x;
       continue;
     }
     const unsigned take = min(at0.left, w.count() + at0.turn - at0.at), end = at0.at + take;
@@ -132,7 +140,7 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
     at0.at = 0;
     if (++at0.h == p.Hkv) {
       at0.h = 0;
-      ++at0.b;
+      ++at0.x;
     }
     if (n_tiles == 0) break;  // (the range ends before the segment's first tile)
 
@@ -193,11 +201,11 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = 8 * n + g;
-        const long long at = p.query(row) * D + c * L::EK;
+        const long long at = p.query(r0 + row) * D + c * L::EK;
 #pragma unroll
         for (int j = 0; j < DH / 16; ++j) {
           uint2 u = make_uint2(0u, 0u);
-          if (row < p.R) u = __ldcg(reinterpret_cast<const uint2*>(qsrc + at + 4 * j));
+          if (row < R) u = __ldcg(reinterpret_cast<const uint2*>(qsrc + at + 4 * j));
           qf[j][n][0] = u.x;
           qf[j][n][1] = u.y;
         }
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) at[n][x] = w.at(p, min(8 * n + 2 * c + x, p.R - 1));
+      for (int x = 0; x < 2; ++x) at[n][x] = w.at(p, r0 + min(8 * n + 2 * c + x, R - 1));
 
     float acc[DH / 16][NT][4];
 #pragma unroll
@@ -493,7 +501,7 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (8 * n + 2 * c < p.R) {
+      if (8 * n + 2 * c < R) {
         float* O = mine + 32 + (8 * n + 2 * c) * RS + half * DH + 2 * g;
 #pragma unroll
         for (int i = 0; i < DH / 16; ++i) {
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
       }
     }
     __syncthreads();
-    const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(b) * p.HH + h;
+    const long long slot = static_cast<long long>(blockIdx.x) + static_cast<long long>(x) * p.HH + h;
     const bool store = TQ_CHECK(slot < p.n_recs, p.err);
     float* rec = p.recs + slot * SM::REC;
     if (threadIdx.x < TEAMS * 16) {
@@ -536,7 +544,7 @@ __global__ void __launch_bounds__(AttnShape<D, VB, NT>::THREADS, AttnShape<D, VB
     __syncthreads();
     if (store) {
 #pragma unroll 1
-      for (int i = threadIdx.x; i < p.R * (D / 4); i += blockDim.x) {
+      for (int i = threadIdx.x; i < R * (D / 4); i += blockDim.x) {
         const int r = i / (D / 4), e = i % (D / 4) * 4;  // elements e .. e + 3 of row r
         const int in = e % DH, at = r * RS + (e - in) + 16 * (in % L::EV / 2) + 2 * (in / L::EV);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -586,7 +594,7 @@ struct SpanFew {
     if (e != cudaSuccess) return e;
     const int most = per_sm();
     long long grid = static_cast<long long>(most < kAttnGridPerSm ? most : kAttnGridPerSm) * sm_count();
-    const long long team = SM::NW / AttnSplit<D>::SPL * 2, segments = static_cast<long long>(p.B) * p.HH;
+    const long long team = SM::NW / AttnSplit<D>::SPL * 2, segments = static_cast<long long>(p.B) * p.RB * p.HH;
     grid = std::min(grid, std::max((tiles + team - 1) / team, segments));
     p.grid = static_cast<int>(std::max(grid, 1LL));
     return launch_pdl_block(span_few_kernel<D, VB, KMODE, NT>, p.grid, SM::Shape::THREADS, p, s, SMEM);

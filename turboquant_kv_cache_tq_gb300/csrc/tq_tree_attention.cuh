@@ -634,11 +634,6 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
             p.q + (static_cast<long long>(w.b) * p.Hq + static_cast<long long>(h) * p.G) * p.N * D);
       else
         src = reinterpret_cast<const uint4*>(p.queries(w.b, h, D));
-      // where row x of the kv head's lies, in rows
-      auto place = [&](int x) -> long long {
-        if constexpr (TREE) return x;
-        else return p.query(x);
-      };
       auto load = [&](long long i) {
         if constexpr (TREE) return src[i];
         else return __ldcg(src + i);
@@ -648,11 +643,15 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
         const int at = (warp % QUADS) * 32 + x;
         return at < p.rows && rb * p.rows + at < p.R ? rb * p.rows + at : -1;
       };
+      // (spans: where row x of the warp's 32 lies, found by lane x)
+      long long place = -1;
+      if constexpr (!TREE)
+        if (row_at(lane) >= 0) place = p.query(row_at(lane));
       std::conditional_t<TREE, int, long long> from[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        from[i] = row_at(8 * i + (lane >> 2));
-        if (from[i] >= 0) from[i] = place(static_cast<int>(from[i]));
+        if constexpr (TREE) from[i] = row_at(8 * i + (lane >> 2));
+        else from[i] = __shfl_sync(kFull, place, 8 * i + (lane >> 2));
       }
       constexpr int SHARE = S::QT / 2 / S::SW, STEP = SHARE < 32 ? SHARE : 32;
 #pragma unroll 1
@@ -684,8 +683,10 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
         static_assert(D - S::QT == 256, "a row's rest: 16 bytes a lane");
 #pragma unroll 8
         for (int x = 0; x < 32; ++x) {
-          const int r2 = row_at(x);
-          const uint4 u = r2 >= 0 ? load(place(r2) * (D / 8) + S::QT / 8 + lane)
+          long long r2;
+          if constexpr (TREE) r2 = row_at(x);
+          else r2 = __shfl_sync(kFull, place, x);
+          const uint4 u = r2 >= 0 ? load(r2 * (D / 8) + S::QT / 8 + lane)
                                   : make_uint4(0u, 0u, 0u, 0u);
           sts128(sm + S::Q_OFF + (lane >> 3) * (128 * 128) + (warp * 32 + x) * 128 + (((lane ^ x) & 7) << 4), u.x, u.y,
                  u.z, u.w);
