@@ -44,6 +44,7 @@ struct SpanPass {
   int copies, slots;  // as for the tree attention
   int HH;             // segments of a (cache row, row block): Hkv * value halves
   int kmode, vb, out_f32, grid;
+  int per_sm;         // few rows: blocks that an SM holds
   int x_keys, x_values;  // bytes of a token's packed codes
   unsigned vtab_stride;  // 128: bytes between entries of the value table
   int bulk;           // every tile of the cache starts on 16 bytes in every buffer (few rows: and ends inside it)
@@ -182,9 +183,10 @@ struct SpanOutput {
 constexpr int kFewTurn = 8;
 
 // Launches, translation units of their own. launch_span_few: at most 8 NT rows a kv
-// head (NT: 1 or 2) and `tiles` tiles of 16 tokens in all; sets p.grid.
+// head (NT: 1 or 2) and `tiles` tiles of 16 tokens in all; sets p.grid and p.per_sm (plan:
+// and nothing else).
 template <int D, int NT>
-cudaError_t launch_span_few(SpanPass& p, long long tiles, cudaStream_t s);
+cudaError_t launch_span_few(SpanPass& p, long long tiles, bool plan, cudaStream_t s);
 template <int D, bool F32>
 cudaError_t launch_span_rows(const SpanPass& p, cudaStream_t s);
 

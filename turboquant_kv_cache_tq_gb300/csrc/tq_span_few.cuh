@@ -585,41 +585,43 @@ struct SpanFew {
     }
     return n;
   }
-  // Sets p.grid to one wave of blocks, fewer where a team of warps would get less than
+  // Sets p.per_sm, and p.grid to one wave of blocks, fewer where a team of warps would get less than
   // two of `tiles` tiles, but a block a segment. (One, two, four tiles a team: 8 heads
   // x 4096 tokens 12.4 / 11.2 / 16.4 us, head_dim 512 22.5 / 23.1 / 26.5; two segments
   // of three tiles 7.5 us in two blocks, 10.6 in one.)
-  static cudaError_t launch(SpanPass& p, long long tiles, cudaStream_t s) {
+  // plan: only sets them.
+  static cudaError_t launch(SpanPass& p, long long tiles, bool plan, cudaStream_t s) {
     const cudaError_t e = allow_smem<span_few_kernel<D, VB, KMODE, NT>>(SMEM);
     if (e != cudaSuccess) return e;
-    const int most = per_sm();
-    long long grid = static_cast<long long>(most < kAttnGridPerSm ? most : kAttnGridPerSm) * sm_count();
+    p.per_sm = std::min(per_sm(), kAttnGridPerSm);
+    long long grid = static_cast<long long>(p.per_sm) * sm_count();
     const long long team = SM::NW / AttnSplit<D>::SPL * 2, segments = static_cast<long long>(p.B) * p.RB * p.HH;
     grid = std::min(grid, std::max((tiles + team - 1) / team, segments));
     p.grid = static_cast<int>(std::max(grid, 1LL));
+    if (plan) return cudaSuccess;
     return launch_pdl_block(span_few_kernel<D, VB, KMODE, NT>, p.grid, SM::Shape::THREADS, p, s, SMEM);
   }
 };
 
 template <int D, int VB, int NT>
-cudaError_t launch_span_few_keys(SpanPass& p, long long tiles, cudaStream_t s) {
+cudaError_t launch_span_few_keys(SpanPass& p, long long tiles, bool plan, cudaStream_t s) {
   switch (p.kmode) {
-    case kK2: return SpanFew<D, VB, kK2, NT>::launch(p, tiles, s);
-    case kK4: return SpanFew<D, VB, kK4, NT>::launch(p, tiles, s);
-    case kK5: return SpanFew<D, VB, kK5, NT>::launch(p, tiles, s);
-    case kK8: return SpanFew<D, VB, kK8, NT>::launch(p, tiles, s);
-    default: return SpanFew<D, VB, kK8Signed, NT>::launch(p, tiles, s);
+    case kK2: return SpanFew<D, VB, kK2, NT>::launch(p, tiles, plan, s);
+    case kK4: return SpanFew<D, VB, kK4, NT>::launch(p, tiles, plan, s);
+    case kK5: return SpanFew<D, VB, kK5, NT>::launch(p, tiles, plan, s);
+    case kK8: return SpanFew<D, VB, kK8, NT>::launch(p, tiles, plan, s);
+    default: return SpanFew<D, VB, kK8Signed, NT>::launch(p, tiles, plan, s);
   }
 }
 
 template <int D, int NT>
-cudaError_t launch_span_few(SpanPass& p, long long tiles, cudaStream_t s) {
+cudaError_t launch_span_few(SpanPass& p, long long tiles, bool plan, cudaStream_t s) {
   switch (p.vb) {
-    case 2: return launch_span_few_keys<D, 2, NT>(p, tiles, s);
-    case 3: return launch_span_few_keys<D, 3, NT>(p, tiles, s);
-    case 4: return launch_span_few_keys<D, 4, NT>(p, tiles, s);
-    case 5: return launch_span_few_keys<D, 5, NT>(p, tiles, s);
-    default: return launch_span_few_keys<D, 8, NT>(p, tiles, s);
+    case 2: return launch_span_few_keys<D, 2, NT>(p, tiles, plan, s);
+    case 3: return launch_span_few_keys<D, 3, NT>(p, tiles, plan, s);
+    case 4: return launch_span_few_keys<D, 4, NT>(p, tiles, plan, s);
+    case 5: return launch_span_few_keys<D, 5, NT>(p, tiles, plan, s);
+    default: return launch_span_few_keys<D, 8, NT>(p, tiles, plan, s);
   }
 }
 

@@ -3,5 +3,5 @@
 #include "tq_span_few.cuh"
 
 namespace tq {
-template cudaError_t launch_span_few<64, 2>(SpanPass&, long long, cudaStream_t);
+template cudaError_t launch_span_few<64, 2>(SpanPass&, long long, bool, cudaStream_t);
 }  // namespace tq
