@@ -243,7 +243,7 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, int item, 
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
   using G = Geo<D>;
   constexpr int NG = D / kGroup;
   __shared__ CellEntry s_cells[CellGrid<8>::NC];
@@ -368,7 +368,7 @@ template <int D, bool F32>
 cudaError_t launch_append(const AppendParams& params, cudaStream_t s) {
   using S = AppendPieces<D, F32>;
   AppendParams p = params;
-  const long long kv_items = 2LL * ((p.kv_rows + Geo<D>::RPW - 1) / Geo<D>::RPW), warps = 2LL * sm_count() * (kAppendThreads / 32);
+  const long long kv_items = 2LL * ((p.kv_rows + Geo<D>::RPW - 1) / Geo<D>::RPW), warps = 3LL * sm_count() * (kAppendThreads / 32);
   p.pieces = p.R % (2 * S::C) == 0;
   p.steps = 1;
   long long q_items = (p.q_rows + Geo<D>::RPW - 1) / Geo<D>::RPW;
@@ -382,7 +382,7 @@ cudaError_t launch_append(const AppendParams& params, cudaStream_t s) {
   }
   p.q_items = static_cast<int>(q_items);
   const long long blocks = (kv_items + q_items + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  const int grid = static_cast<int>(std::max(std::min(blocks, 2LL * sm_count()), 1LL));
+  const int grid = static_cast<int>(std::max(std::min(blocks, 3LL * sm_count()), 1LL));
   return launch_pdl(append_kernel<D, F32>, grid, p, s, 0, kAppendThreads);
 }
 

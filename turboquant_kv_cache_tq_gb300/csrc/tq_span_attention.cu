@@ -271,9 +271,9 @@ cudaError_t launch_span(SpanPass* passes, const SpanPlan* plans, int64_t reach, 
     if (e != cudaSuccess) return e;
     parts = std::max(parts, (passes[k].grid / (plans[k].lines * plans[k].HH) + 1) * plans[k].copies);
   }
-  // (the rule of the tree attention's combine kernel)
+  // (the rule of the tree attention's combine kernel, while four warps a row are one wave)
   const long long rows = static_cast<long long>(o.B) * o.Hq * o.N;
-  if (parts >= 8) return launch_pdl_block(span_combine_kernel<D, 4>, static_cast<int>(rows), 128, o, s, 0);
+  if (parts >= 8 && rows <= 7LL * sm_count()) return launch_pdl_block(span_combine_kernel<D, 4>, static_cast<int>(rows), 128, o, s, 0);
   return launch_pdl_block(span_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, o, s, 0);
 }
 
