@@ -166,7 +166,7 @@ def test_binding_refusals(tq):
         with pytest.raises(ValueError, match="bfloat16"):
             call(q.float())
         with pytest.raises(ValueError, match="contiguous"):
-            call(q.transpose(2, 3))
+            call(q[..., ::2])
         with pytest.raises(ValueError, match="out_dtype"):
             call(q, out_dtype=torch.float16)
         with pytest.raises(ValueError, match="CUDA device"):
