@@ -27,10 +27,11 @@ namespace {
 
 // Merges the partial results of each output row's passes, divides, turns the row
 // back and stores it (see tree_combine_kernel, whose steps these are). W warps share
-// a row. A query that its sequence does not have gets zeros and -inf here, whatever
-// its rows of the passes hold.
-template <int D, int W>
+// a row, or a warp takes NR rows. A query that its sequence does not have gets zeros
+// and -inf here, whatever its rows of the passes hold.
+template <int D, int W, int NR>
 __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(const __grid_constant__ SpanOutput p) {
+  static_assert((W == 1 || NR == 1) && NR <= 8, "a warp's rows, or a row's warps");
   constexpr int E = D / 32, V = E < 4 ? E : 4;
   // head_dim 512: a pass of many rows keeps the halves of the values in records of
   // their own, so half a warp looks at the parts of each
@@ -41,12 +42,14 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = p.B * p.Hq * p.N, row0 = blockIdx.x * (4 / W) + warp / W, row = min(row0, rows - 1);
+  // Where the rows' records are. Lanes 2 i and 2 i + 1 (head_dim 512: and 16 on, for
+  // the other half of the values) find row i's of the first and the second pass, in one
+  // code with one wait, as instructions that run once are paid in fetches. Then a row's
+  // parts of both passes are one list.
+  const int rows = p.B * p.Hq * p.N, row0 = (blockIdx.x * (4 / W) + warp / W) * NR;
+  const int row = min(row0 + ((lane >> 1) & 7) % NR, rows - 1);
   const int b = row / (p.Hq * p.N), in_b = row - b * (p.Hq * p.N), hq = in_b / p.N, n = in_b - hq * p.N;
   const int h = hq / p.G, g = hq - h * p.G;
-  // Where the row's records are: even lanes find those of the first pass, odd lanes
-  // the second's (one code for both, as instructions that run once are paid in
-  // fetches, and one wait). From here on the parts of both passes are one list.
   const SpanSource& s = p.from[lane & (p.sources - 1)];
   const int half = lane >> 4, hh = h * s.halves + (s.halves == 1 ? 0 : half);
   const float* recs;
@@ -75,106 +78,109 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
     rec_floats = s.slots * (D / s.halves + 2);
     recs = s.recs + slot * rec_floats;
   }
-  const int group = D == 512 ? lane & 16 : 0;  // the lanes that look at the parts of this lane's half
-  const int parts0 = __shfl_sync(kFull, mine, group);
-  const int parts = parts0 + (p.sources > 1 ? __shfl_sync(kFull, mine, group + 1) : 0);
-  int most = parts;
-  if constexpr (D == 512) most = max(most, __shfl_xor_sync(kFull, most, 16));
-  float m = kNegInf, l = 0.0f, o[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = 0.0f;
-  // LANES parts at a time: every lane looks at one maximum and sum, then all take
-  // the values with the factors known (no result waits for the last one).
 #pragma unroll 1
-  for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
-    const int part = s0 + (lane % LANES) * W, k = part >= parts0 ? 1 : 0, y = part - (k ? parts0 : 0);
-    const SpanSource& f = p.from[k];
-    const int shift = f.copies - 1, from = group + k;
-    const int at = __shfl_sync(kFull, rl, from) + (y & shift) * f.rows;
-    const float* rec = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(recs), from)) +
-                       static_cast<long long>(y >> shift) * __shfl_sync(kFull, rec_floats, from);
-    const float* values = rec + 2 * f.slots + static_cast<long long>(at) * (D / f.halves);
-    float m2 = kNegInf, l2 = 0.0f;
-    if (part < parts) {
-      m2 = rec[at];
-      l2 = rec[f.slots + at];
-    }
-    auto load = [&](int z, float (&u)[E]) {
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(values), group + z));
-      // (a record of half the values has them from its own first on)
-      const int first = D == 512 && p.from[s0 + z * W >= parts0 ? 1 : 0].halves == 2 ? (lane & 15) * E : lane * E;
-      if (s0 + z * W < parts) {
+  for (int nr = 0; nr < NR; ++nr) {
+    const int group = D == 512 ? lane & 16 : 0;  // the lanes that look at the parts of this lane's half
+    const int parts0 = __shfl_sync(kFull, mine, group + 2 * nr);
+    const int parts = parts0 + (p.sources > 1 ? __shfl_sync(kFull, mine, group + 2 * nr + 1) : 0);
+    int most = parts;
+    if constexpr (D == 512) most = max(most, __shfl_xor_sync(kFull, most, 16));
+    float m = kNegInf, l = 0.0f, o[E];
 #pragma unroll
-        for (int i = 0; i < E; i += V) {
-          if constexpr (V == 2) {
-            const float2 v = *reinterpret_cast<const float2*>(src + first + i);
-            u[i] = v.x; u[i + 1] = v.y;
-          } else {
-            const float4 v = *reinterpret_cast<const float4*>(src + first + i);
-            u[i] = v.x; u[i + 1] = v.y; u[i + 2] = v.z; u[i + 3] = v.w;
+    for (int i = 0; i < E; ++i) o[i] = 0.0f;
+    // LANES parts at a time: every lane looks at one maximum and sum, then all take
+    // the values with the factors known (no result waits for the last one).
+#pragma unroll 1
+    for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
+      const int part = s0 + (lane % LANES) * W, k = part >= parts0 ? 1 : 0, y = part - (k ? parts0 : 0);
+      const SpanSource& f = p.from[k];
+      const int shift = f.copies - 1, from = group + 2 * nr + k;
+      const int at = __shfl_sync(kFull, rl, from) + (y & shift) * f.rows;
+      const float* rec = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(recs), from)) +
+                         static_cast<long long>(y >> shift) * __shfl_sync(kFull, rec_floats, from);
+      const float* values = rec + 2 * f.slots + static_cast<long long>(at) * (D / f.halves);
+      float m2 = kNegInf, l2 = 0.0f;
+      if (part < parts) {
+        m2 = rec[at];
+        l2 = rec[f.slots + at];
+      }
+      auto load = [&](int z, float (&u)[E]) {
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(values), group + z));
+        // (a record of half the values has them from its own first on)
+        const int first = D == 512 && p.from[s0 + z * W >= parts0 ? 1 : 0].halves == 2 ? (lane & 15) * E : lane * E;
+        if (s0 + z * W < parts) {
+#pragma unroll
+          for (int i = 0; i < E; i += V) {
+            if constexpr (V == 2) {
+              const float2 v = *reinterpret_cast<const float2*>(src + first + i);
+              u[i] = v.x; u[i + 1] = v.y;
+            } else {
+              const float4 v = *reinterpret_cast<const float4*>(src + first + i);
+              u[i] = v.x; u[i + 1] = v.y; u[i + 2] = v.z; u[i + 3] = v.w;
+            }
           }
         }
-      }
-    };
-    // the first AHEAD results' values meanwhile
-    float u[AHEAD][E];
+      };
+      // the first AHEAD results' values meanwhile
+      float u[AHEAD][E];
 #pragma unroll
-    for (int z = 0; z < AHEAD; ++z) load(z, u[z]);
-    float mn = m2;
+      for (int z = 0; z < AHEAD; ++z) load(z, u[z]);
+      float mn = m2;
 #pragma unroll
-    for (int z = LANES / 2; z > 0; z >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, z));
-    mn = fmaxf(mn, m);
-    const float fa = m == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m2, mn));
-    float add = __fmul_rn(l2, fb);
+      for (int z = LANES / 2; z > 0; z >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, z));
+      mn = fmaxf(mn, m);
+      const float fa = m == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m2, mn));
+      float add = __fmul_rn(l2, fb);
 #pragma unroll
-    for (int z = LANES / 2; z > 0; z >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, z));
-    l = __fmaf_rn(l, fa, add);
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
-    const int n_here = min(LANES, (most - s0 + W - 1) / W);
-    // (a part that saw no key is left out, whatever its values are; nor does one
-    // past the end count)
-    auto add_part = [&](int z, const float (&v)[E]) {
-      const float x = __shfl_sync(kFull, fb, group + z);
-      if (x != 0.0f) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(v[i], x, o[i]);
-      }
-    };
-#pragma unroll
-    for (int z = 0; z < AHEAD; ++z) add_part(z, u[z]);
-#pragma unroll 1
-    for (int z = AHEAD; z < n_here; z += AHEAD) {
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a) load(min(z + a, LANES - 1), u[a]);
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a)
-        if (z + a < n_here) add_part(z + a, u[a]);
-    }
-  }
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) s_part[warp][i][lane] = o[i];
-    s_part[warp][E][lane] = l;
-    s_part[warp][E + 1][lane] = m;
-    __syncthreads();
-    if (warp % W != 0) return;
-#pragma unroll 1
-    for (int x = 1; x < W; ++x) {
-      const float m2 = s_part[warp + x][E + 1][lane], l2 = s_part[warp + x][E][lane], mn = fmaxf(m, m2);
-      const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
-      l = __fmaf_rn(l2, fb, __fmul_rn(l, fa));
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(s_part[warp + x][i][lane], fb, __fmul_rn(o[i], fa));
+      for (int z = LANES / 2; z > 0; z >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, z));
+      l = __fmaf_rn(l, fa, add);
       m = mn;
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
+      const int n_here = min(LANES, (most - s0 + W - 1) / W);
+      // (a part that saw no key is left out, whatever its values are; nor does one
+      // past the end count)
+      auto add_part = [&](int z, const float (&v)[E]) {
+        const float x = __shfl_sync(kFull, fb, group + z);
+        if (x != 0.0f) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(v[i], x, o[i]);
+        }
+      };
+#pragma unroll
+      for (int z = 0; z < AHEAD; ++z) add_part(z, u[z]);
+#pragma unroll 1
+      for (int z = AHEAD; z < n_here; z += AHEAD) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) load(min(z + a, LANES - 1), u[a]);
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+          if (z + a < n_here) add_part(z + a, u[a]);
+      }
     }
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) s_part[warp][i][lane] = o[i];
+      s_part[warp][E][lane] = l;
+      s_part[warp][E + 1][lane] = m;
+      __syncthreads();
+      if (warp % W != 0) return;
+#pragma unroll 1
+      for (int x = 1; x < W; ++x) {
+        const float m2 = s_part[warp + x][E + 1][lane], l2 = s_part[warp + x][E][lane], mn = fmaxf(m, m2);
+        const float fa = m == kNegInf ? 0.0f : exp2f(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : exp2f(__fsub_rn(m2, mn));
+        l = __fmaf_rn(l2, fb, __fmul_rn(l, fa));
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(s_part[warp + x][i][lane], fb, __fmul_rn(o[i], fa));
+        m = mn;
+      }
+    }
+    if constexpr (D == 512) {  // a value group may have spoiled one half's sum: the row's lse is NaN then
+      const float other = __shfl_xor_sync(kFull, l, 16);
+      if (other != other) l = other;
+    }
+    finish_row<D>(o, m, l, row0 + nr, row0 + nr < rows, p.out, p.out_f32, p.lse, p.rot_scale, lane);
   }
-  if constexpr (D == 512) {  // a value group may have spoiled one half's sum: the row's lse is NaN then
-    const float other = __shfl_xor_sync(kFull, l, 16);
-    if (other != other) l = other;
-  }
-  finish_row<D>(o, m, l, row, row0 < rows, p.out, p.out_f32, p.lse, p.rot_scale, lane);
 }
 
 // How the query rows of a pass are laid out, and the scratch that follows.
@@ -273,8 +279,12 @@ cudaError_t launch_span(SpanPass* passes, const SpanPlan* plans, int64_t reach, 
   }
   // (the rule of the tree attention's combine kernel, while four warps a row are one wave)
   const long long rows = static_cast<long long>(o.B) * o.Hq * o.N;
-  if (parts >= 8 && rows <= 7LL * sm_count()) return launch_pdl_block(span_combine_kernel<D, 4>, static_cast<int>(rows), 128, o, s, 0);
-  return launch_pdl_block(span_combine_kernel<D, 1>, static_cast<int>((rows + 3) / 4), 128, o, s, 0);
+  if (parts >= 8 && rows <= 7LL * sm_count())
+    return launch_pdl_block(span_combine_kernel<D, 4, 1>, static_cast<int>(rows), 128, o, s, 0);
+  // (more rows than two waves of warps: four a warp, which finds their records at once)
+  if (rows > 2LL * 28 * sm_count())
+    return launch_pdl_block(span_combine_kernel<D, 1, 4>, static_cast<int>((rows + 15) / 16), 128, o, s, 0);
+  return launch_pdl_block(span_combine_kernel<D, 1, 1>, static_cast<int>((rows + 3) / 4), 128, o, s, 0);
 }
 
 constexpr int64_t kSpanMostRows = 1 << 20;  // query rows of a kv head
