@@ -75,7 +75,7 @@ def test_window_every_format(D, kb, ks, vb, dtype, N):
 
 @pytest.mark.parametrize("win,sinks", [(1, 0), (1, 1), (1, 40), (7, 0), (16, 16), (17, 5), (64, 64), (65, 63), (128, 4),
                                        (299, 1), (300, 0), (10 ** 9, 0), (2 ** 40, 2 ** 40), (3, 299), (3, 1000)])
-@pytest.mark.parametrize("N", [1, 3, 33])
+@pytest.mark.parametrize("N", [1, 3, 33, 140])
 def test_window_shapes(win, sinks, N):
     window(3, 1, 3, N, 300, 128, 8, True, 3, win, sinks, torch.float32, lens=[300, 133, 64], left_pad=[0, 17, 60])
 
@@ -97,7 +97,7 @@ def test_window_rows(G, N, dtype):
 
 def test_window_empty_rows():
     """No tokens, fewer tokens than new ones, no new tokens, pads past the end."""
-    for N in (1, 4, 50):
+    for N in (1, 4, 50, 150):
         window(7, 2, 2, N, 90, 128, 8, True, 3, 20, 2, torch.float32, lens=[0, 1, 3, 90, 90, -5, 1000],
                left_pad=[0, 0, 2, 90, 89, 3, 200], count=[N, N, N, N, N, N, N])
         window(6, 2, 2, N, 90, 128, 8, True, 3, 20, 2, lens=[90, 90, 40, 40, 0, 1], count=[0, 1, -3, 1000, 0, N])
@@ -110,19 +110,19 @@ def test_window_empty_rows():
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
 def test_window_capacities(cap, D):
     """Capacities that break the rows' alignment, and T far below the capacity."""
-    for N in (1, 30):
+    for N in (1, 30, 70):
         window(2, 3, 2, N, 301, D, 2 if D == 64 else 5, False, 5 if D == 64 else 2, 100, 4, lens=[301, 150], cap=cap)
 
 
 def test_window_scales():
-    for N in (2, 20):
+    for N in (2, 20, 140):
         for scale in (-0.2, 0.0, 3.0):
             window(2, 2, 2, N, 200, 128, 8, True, 8, 60, 3, torch.float32, scale=scale, lens=[200, 9])
 
 
 def test_window_large_scores():
     """Scores in the hundreds, whose maximum rises along the sequence."""
-    for N in (1, 40):
+    for N in (1, 20, 40):
         window(1, 2, 4, N, 2000, 128, 8, True, 8, 1500, 4, torch.float32, qscale=30.0)
         window(1, 2, 4, N, 2000, 64, 8, False, 3, 5000, 0, qscale=30.0, offset=2.0)
 
@@ -146,7 +146,7 @@ def _poison(tokens, what):
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_window_bad_tokens(what, D, dtype):
     """Tokens that decode to NaN or infinities reach the rows that see them, and no other."""
-    for N, G in ((1, 4), (4, 2), (30, 3)):
+    for N, G in ((1, 4), (4, 2), (30, 3), (70, 2)):
         T, win = 300, 60
         first = T - N
         tokens = [(0, 0, first - win + 1), (0, 1, 100), (1, 0, 5), (1, 1, 2), (2, 0, first - win + (N + 1) // 2), (2, 1, T - 1)]
@@ -157,14 +157,17 @@ def test_window_bad_tokens(what, D, dtype):
 def test_window_queries_of_their_own_values():
     """A query of zeros weighs its tokens equally; one with an infinity spoils its own row only."""
     c = sc.cache(1, 1, 50, 128, 8, True, 8, 3)
-    for N in (2, 20):
+    for N in (2, 20, 90):
         q = sc.normal((1, 2, N, 128), 1)
         q[0, 0, 0] = 0
         q[0, 1, 1, 7] = math.inf
         out, lse = tq.tq_window_attention(q, c, 50, 8, True, 8, 10, out_dtype=torch.float32)
-        assert abs(lse[0, 0, 0].item() - math.log(10)) < 1e-6
+        assert N > 50 or abs(lse[0, 0, 0].item() - math.log(10)) < 1e-6
         nan = out.isnan().any(-1)
-        assert nan[0, 1, 1] and nan.sum() == 1 and lse.isnan().sum() == 1
+        if N > 50:  # (its last 50 new tokens are all that the sequence has)
+            assert not nan.any() and (lse[0, :, :N - 50] == -math.inf).all()
+        else:
+            assert nan[0, 1, 1] and nan.sum() == 1 and lse.isnan().sum() == 1
 
 
 def test_window_many_sequences():
@@ -207,7 +210,7 @@ def test_prefix_rows(S, G, N, dtype):
 
 
 def test_prefix_empty_rows():
-    for N in (1, 30):
+    for N in (1, 30, 80):
         # no own tokens but the new one, none at all, no prefix, neither
         prefix(2, 4, 2, 2, N, 100, 40, 128, 8, True, 3, torch.float32, prefix_lens=[100, 0],
                lens=[40, 1, 0, 20, 40, 1, 0, 20], left_pad=[0, 0, 0, 20, 0, 0, 0, 20])
@@ -222,10 +225,11 @@ def test_prefix_empty_rows():
 def test_prefix_capacities(cap, pcap, D):
     prefix(2, 5, 2, 2, 1, 200, 61, D, 5, False, 3, prefix_lens=[200, 90], cap=cap, pcap=pcap)
     prefix(2, 2, 2, 2, 12, 200, 61, D, 2, False, 2, prefix_lens=[200, 90], cap=cap, pcap=pcap)
+    prefix(2, 2, 2, 2, 50, 200, 61, D, 4, False, 4, prefix_lens=[200, 90], cap=cap, pcap=pcap)
 
 
 def test_prefix_scales_and_large_scores():
-    for S in (2, 12):
+    for S in (2, 12, 100):
         for scale in (-0.2, 0.0, 3.0):
             prefix(1, S, 2, 2, 1, 200, 60, 128, 8, True, 8, torch.float32, scale=scale)
         prefix(1, S, 2, 4, 1, 3000, 500, 128, 8, True, 8, torch.float32, qscale=30.0)
@@ -234,7 +238,7 @@ def test_prefix_scales_and_large_scores():
 @pytest.mark.parametrize("what", ["value", "value nan", "key", "zero point"])
 @pytest.mark.parametrize("D", [64, 128, 512])
 def test_prefix_bad_tokens(what, D):
-    for S, N in ((3, 1), (20, 1), (3, 9)):
+    for S, N in ((3, 1), (20, 1), (3, 9), (70, 1)):
         def edit(pre, c):
             _poison([(1, 0, 10), (0, 1, 70)], what)(pre)  # (70: behind prefix 0's end)
             _poison([(1, 1, 20), (2, 0, 0)], what)(c)
