@@ -190,26 +190,32 @@ struct SpanPlan {
   bool few;
 };
 
-// Whether a pass of `rows` query rows a kv head over `tiles` tiles of 16 tokens (of
-// one row block, all heads and cache rows) decodes in registers, 16 rows at a time:
-// the kernel of 128 rows starts and ends more slowly, but decodes a tile once. Both
+// How many rows at a time a pass of `rows` query rows a kv head over `tiles` tiles of 16
+// tokens (of one row block, all heads and cache rows) decodes in registers; 0: rows by
+// the 128.
+//   The kernel of 128 rows starts and ends more slowly, but decodes a tile once. Both
 // sides at 8 heads (registers / 128 rows): 32 rows, head_dim 128, 2048 tokens 14.7 /
 // 16.9 us, 8192 24 / 21; 64 rows, 512 tokens 14.3 / 15.4, 2048 18.5 / 17.5; 32 rows, 64,
 // 8192 17.6 / 19.3, 32768 50 / 33; 256, 2048 19.5 / 20.5, 8192 38 / 31. At head_dim 512,
 // where 128 rows decode the keys once for each half of the values: 32 rows, 32768 tokens
 // 203 / 294; 64 rows, 2048 50 / 52, 8192 116 / 102. Above 128 rows never (which the
 // scratch is sized by).
+//   Blocks of 8 rows in place of 16 decode a tile twice as often, but the code for 16 at
+// head_dim 512 is 40 KB of instructions, which a pass of a few tiles pays to fetch: 12
+// rows, 8 heads x 2048 tokens 24.0 / 30.4 us, 8 sequences of 8192 186 / 161 (head_dim 256
+// 16.6 / 16.1 and 100 / 85, narrower ones alike).
 constexpr int kFewRows = kAttnRows, kFewMost = 128;
-bool span_few(int64_t rows, int64_t tiles, int64_t D) {
-  if (rows <= kFewRows || (D == 512 && rows <= 2 * kFewRows)) return true;
-  return rows <= kFewMost && tiles * ((rows + kFewRows - 1) / kFewRows) < (D == 512 ? 5000 : 450000 / D);
+int span_few(int64_t rows, int64_t tiles, int64_t D) {
+  const int block = D == 512 && tiles < 4000 ? kFewRows / 2 : kFewRows;
+  if (rows <= kFewRows || (D == 512 && rows <= 2 * kFewRows)) return block;
+  return rows <= kFewMost && tiles * ((rows + kFewRows - 1) / kFewRows) < (D == 512 ? 5000 : 450000 / D) ? block : 0;
 }
 
 // B rows of the cache, `rows` query rows a kv head in each. (Long sequences and bf16
 // outputs need the most scratch.)
-bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool f32, bool few, SpanPlan* t) {
+bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool f32, int few, SpanPlan* t) {
   const long long lim = 0x7fffffffLL;
-  t->few = few;
+  t->few = few > 0;
   t->R = rows;
   t->halves = !t->few && D == 512 ? 2 : 1;
   t->HH = Hkv * t->halves;
@@ -225,7 +231,7 @@ bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool 
     };
     t->TT = f32 ? tile(std::true_type{}) : tile(std::false_type{});
   }
-  const int block = few ? kAttnRows : kTreeRows;
+  const int block = few > 0 ? few : kTreeRows;
   t->RB = (rows + block - 1) / block;
   t->rows = (rows + t->RB - 1) / t->RB;
   if (t->RB > lim / t->HH || (B > 0 && t->RB * t->HH > lim / B)) return false;
@@ -245,8 +251,8 @@ bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool 
 // The scratch of a pass, whatever its length and output type.
 bool span_bytes(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t* bytes) {
   SpanPlan few{}, many{};
-  if (rows <= kFewMost && !span_plan(B, Hkv, rows, D, 1LL << 40, false, true, &few)) return false;
-  if (rows > kFewRows && !span_plan(B, Hkv, rows, D, 1LL << 40, false, false, &many)) return false;
+  if (rows <= kFewMost && !span_plan(B, Hkv, rows, D, 1LL << 40, false, D == 512 ? kFewRows / 2 : kFewRows, &few)) return false;
+  if (rows > kFewRows && !span_plan(B, Hkv, rows, D, 1LL << 40, false, 0, &many)) return false;
   *bytes = std::max(few.bytes, many.bytes);
   return true;
 }
