@@ -36,7 +36,8 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
   // head_dim 512: a pass of many rows keeps the halves of the values in records of
   // their own, so half a warp looks at the parts of each
   constexpr int LANES = D == 512 ? 16 : 32;
-  constexpr int AHEAD = E <= 4 ? 6 : 2;
+  // (values of a row on their way at once: a warp's many rows have few parts each)
+  constexpr int AHEAD = NR > 1 || E > 4 ? 2 : 6;
   const float kNegInf = -__int_as_float(0x7f800000);
   __shared__ float s_part[4][E + 2][32];
   pdl_launch_dependents();
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
     rec_floats = s.slots * (D / s.halves + 2);
     recs = s.recs + slot * rec_floats;
   }
+  const uint32_t flips = row_flips<D>(lane);
 #pragma unroll 1
   for (int nr = 0; nr < NR; ++nr) {
     const int group = D == 512 ? lane & 16 : 0;  // the lanes that look at the parts of this lane's half
@@ -125,15 +127,17 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
       float u[AHEAD][E];
 #pragma unroll
       for (int z = 0; z < AHEAD; ++z) load(z, u[z]);
-      float mn = m2;
+      // (over the lanes; two parts are in the first two)
+      auto over = [&](float x, auto both) {
+        if (most <= 2) return both(__shfl_sync(kFull, x, group), __shfl_sync(kFull, x, group + 1));
 #pragma unroll
-      for (int z = LANES / 2; z > 0; z >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, z));
-      mn = fmaxf(mn, m);
-      const float fa = m == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m, mn)), fb = m2 == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m2, mn));
-      float add = __fmul_rn(l2, fb);
-#pragma unroll
-      for (int z = LANES / 2; z > 0; z >>= 1) add = __fadd_rn(add, __shfl_xor_sync(kFull, add, z));
-      l = __fmaf_rn(l, fa, add);
+        for (int z = LANES / 2; z > 0; z >>= 1) x = both(x, __shfl_xor_sync(kFull, x, z));
+        return x;
+      };
+      const float mn = fmaxf(m, over(m2, [](float a, float b) { return fmaxf(a, b); }));
+      const float fa = m == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m, mn));
+      const float fb = m2 == kNegInf ? 0.0f : fast_exp2(__fsub_rn(m2, mn));
+      l = __fmaf_rn(l, fa, over(__fmul_rn(l2, fb), [](float a, float b) { return __fadd_rn(a, b); }));
       m = mn;
 #pragma unroll
       for (int i = 0; i < E; ++i) o[i] = __fmul_rn(o[i], fa);
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
       const float other = __shfl_xor_sync(kFull, l, 16);
       if (other != other) l = other;
     }
-    finish_row<D>(o, m, l, row0 + nr, row0 + nr < rows, p.out, p.out_f32, p.lse, p.rot_scale, lane);
+    finish_row<D>(o, m, l, row0 + nr, row0 + nr < rows, p.out, p.out_f32, p.lse, p.rot_scale, flips, lane);
   }
 }
 

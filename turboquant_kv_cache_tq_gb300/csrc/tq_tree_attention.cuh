@@ -1073,12 +1073,23 @@ __global__ void __launch_bounds__(TreeShape<D, F32>::THREADS, 1) tree_split_kern
   p.end();
 }
 
+// The signs of a lane's elements of a row (bit i: element i is negated).
+template <int D>
+__device__ __forceinline__ uint32_t row_flips(int lane) {
+  constexpr int E = D / 32;
+  const uint8_t* neg = D == 64 ? kSignNeg64 : D == 128 ? kSignNeg128 : D == 256 ? kSignNeg256 : kSignNeg512;
+  uint32_t f = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) f |= (neg[(lane * E + i) >> 3] >> ((lane * E + i) & 7) & 1u) << i;
+  return f;
+}
+
 // An output row from its merged result: the division, the Hadamard butterflies, /
 // sqrt(D) and signs, the store, the log-sum-exp. Lane L holds elements [L D/32, (L+1)
 // D/32); whole warps call.
 template <int D>
 __device__ __forceinline__ void finish_row(float (&o)[D / 32], float m, float l, int row, bool store, void* out, int out_f32,
-                                           float* lse, float rot_scale, int lane) {
+                                           float* lse, float rot_scale, uint32_t flips, int lane) {
   constexpr int E = D / 32, V = E < 4 ? E : 4;
   const float kNegInf = -__int_as_float(0x7f800000);
   const bool empty = l == 0.0f;
@@ -1102,13 +1113,10 @@ __device__ __forceinline__ void finish_row(float (&o)[D / 32], float m, float l,
     for (int i = 0; i < E; ++i) o[i] = __fmaf_rn(o[i], sgn, __shfl_xor_sync(kFull, o[i], x));
   }
   if (!store) return;
-  const uint8_t* neg = D == 64 ? kSignNeg64 : D == 128 ? kSignNeg128 : D == 256 ? kSignNeg256 : kSignNeg512;
   const int e0 = lane * E;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const uint32_t flip = (neg[(e0 + i) >> 3] >> ((e0 + i) & 7) & 1u) << 31;
-    o[i] = __uint_as_float(__float_as_uint(__fmul_rn(o[i], rot_scale)) ^ flip);
-  }
+  for (int i = 0; i < E; ++i)
+    o[i] = __uint_as_float(__float_as_uint(__fmul_rn(o[i], rot_scale)) ^ (flips << (31 - i) & 0x80000000u));
   if (out_f32) {
     float* dst = static_cast<float*>(out) + static_cast<long long>(row) * D + e0;
 #pragma unroll
@@ -1257,7 +1265,7 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) tree_combine_kernel(con
     const float other = __shfl_xor_sync(kFull, l, 16);
     if (other != other) l = other;
   }
-  finish_row<D>(o, m, l, row, row0 < rows, p.out, p.out_f32, p.lse, p.rot_scale, lane);
+  finish_row<D>(o, m, l, row, row0 < rows, p.out, p.out_f32, p.lse, p.rot_scale, row_flips<D>(lane), lane);
 }
 
 template <int D, bool F32>
