@@ -559,7 +559,8 @@ TQ_API int64_t tq_prefix_attention_workspace_size(int64_t Bp, int64_t B, int64_t
 /* Device-side failures of the library's kernels on the current device (no
  * counterpart on the pages: failure detection of this library). Kernels that
  * wait on an asynchronous copy or a matrix product (the decode's bulk-copy path,
- * tq_tree_attention, tq_attention_weights) bound the wait;
+ * tq_tree_attention, tq_attention_weights, tq_window_attention,
+ * tq_prefix_attention) bound the wait;
  * one that gives up sets the device error word, stops early and leaves its
  * outputs incomplete. A debug build of the library (compiled with
  * -DTQ_DEBUG_CHECKS) also checks the row and record indices of its kernels'

@@ -1,6 +1,7 @@
 // Shared by the calls on ragged packed caches (tq_tree_attention,
-// tq_attention_weights, tq_evict_select, tq_cache_gather): per-row lengths
-// that only the device knows, draft trees, and the host's checks.
+// tq_attention_weights, tq_evict_select, tq_cache_gather, tq_append_kv,
+// tq_window_attention, tq_prefix_attention): per-row lengths that only the device
+// knows, and the host's checks.
 #pragma once
 
 #include <atomic>

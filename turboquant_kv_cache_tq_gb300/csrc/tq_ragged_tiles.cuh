@@ -1,6 +1,7 @@
 // Packed token rows on their way to the tensor core: tiles of a ragged packed
 // cache in shared memory, decoded into the swizzled bf16 tiles that the matrix
-// instructions read. Shared by the tree attention and the weight sums.
+// instructions read. Shared by the tree attention, the weight sums and the window
+// and prefix attention.
 #pragma once
 
 #include "tq_attention.cuh"

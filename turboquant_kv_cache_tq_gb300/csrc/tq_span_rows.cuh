@@ -4,6 +4,15 @@
 // line of tiles has (cache row, row block), as each block of 128 rows of a chunk
 // sees a window of its own, and a segment's tiles are the sequence's first tokens and
 // the window.
+//
+// What bounds it (2 x 512 new tokens, 32 heads, 8 kv heads, 2048 tokens back, head_dim
+// 128; 32 GFLOP, 17 us at the measured matrix rate): 91 us in a graph, some 70 of them in
+// the split kernel, whose 59 tiles a block take 1790 cycles each (two tiles' softmax in
+// 3580: 128 rows x 64 tokens of exponentials and their parts, with the decode of the
+// tiles in the same issue slots, 53% of which are used; tensor pipe 28%). A block's start
+// takes 7 us (cut 2, queries into tensor memory 4), a change of segments 6. A row a
+// block and a warp a token took 13361 us. (Where the instructions fall moves this case
+// by up to 10%: the first row's tokens found once for all roles, less code, 104 us.)
 #pragma once
 
 #include "tq_span_attention.cuh"

@@ -15,7 +15,8 @@
 // 148 us where 16 nodes take 162, and tq_decode_attention, which serves equal
 // lengths and at most 16 rows, reads the same format 1.6 times as fast (32 x 8
 // heads, k8 / v8: 8192 tokens a sequence in 124 us, where the 148 are for 6144 on
-// average).
+// average; tq_window_attention takes 101 for those). The split kernel also serves
+// the window and prefix attention's many rows, with another walk (tq_span_rows.cuh).
 //
 // The rows are padded to 128 lanes of tensor memory. With at most 64 rows (and
 // tiles of 64 tokens) each row takes two lanes, and lane copy c takes every
