@@ -495,7 +495,9 @@ typedef struct {
  *   new_lens int32 [B]: receives min(lens[b] + count[b], cache->t_cap).
  * The rotation rounds every product and sum to fp32; the turned keys are encoded
  * as tq_encode_kv encodes fp32 keys (they are not rounded to dtype on the way), the
- * values as it encodes dtype values. Nothing else of the cache is touched. */
+ * values as it encodes dtype values. Nothing else of the cache is touched.
+ * Limits: D in {64, 128, 256, 512}; N >= 0; 4 B Hq N and 4 B Hkv N below 2^31 - 2^24;
+ * cache->t_cap at most 2^31 - 2^13; length at most 2^31 - 1. B == 0 is a no-op. */
 TQ_API tq_status tq_append_kv(const tq_rows* q, const tq_rows* k, const tq_rows* v, tq_dtype dtype,
                               int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t D,
                               const float* cos, const float* sin, int64_t length, int64_t rot_dim, int interleaved,
