@@ -166,3 +166,25 @@ def test_on_another_stream_and_in_a_graph():
         graph.replay()
         assert lens.tolist() == n and sc.same_bytes(cache, after) and torch.equal(q_out.cpu(), qt.bfloat16())
         want = after
+
+
+def test_what_is_refused_writes_nothing():
+    B, H, N, D = 2, 2, 3, 64
+    k, v, q = (sc.normal((B, h, N, D), i) for i, h in enumerate((H, H, 4)))
+    cos, sin = tq.rope_tables(D, 16)
+    cache = _garbage(B, H, 10, D, 8, 3)
+    before = {n: t.clone() for n, t in cache.items()}
+    lens = sc.ints([0, 4])
+    for bad in (dict(q=q[:, :, :2]), dict(q=q.float()), dict(q_out=torch.empty_like(q)), dict(cos=cos), dict(cos=cos[0], sin=sin[0]),
+                dict(cos=cos, sin=sin[:8]), dict(cos=cos.double(), sin=sin.double()), dict(count=sc.ints([1])),
+                dict(positions=sc.ints([0, 1])), dict(left_pad=sc.ints([1, 1], "cpu")), dict(new_lens=lens.float())):
+        with pytest.raises(ValueError):
+            tq.tq_append_kv(k, v, cache, lens, 8, True, 3, **bad)
+    for bad in (dict(new_lens=lens), dict(q=q, q_out=q), dict(cos=torch.ones((4, 33), device="cuda"), sin=torch.ones((4, 33), device="cuda"))):
+        with pytest.raises(tq.TQError):
+            tq.tq_append_kv(k, v, cache, lens, 8, True, 3, **bad)
+    odd = torch.empty((B, H, N, D + 4), dtype=torch.bfloat16, device="cuda")[..., :D]
+    with pytest.raises(tq.TQError):  # (rows 136 bytes apart)
+        tq.tq_append_kv(odd, v, cache, lens, 8, True, 3)
+    torch.cuda.synchronize()
+    assert sc.same_bytes(cache, before) and lens.tolist() == [0, 4]

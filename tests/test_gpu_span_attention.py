@@ -319,3 +319,25 @@ def test_another_stream_and_two_calls_at_once():
         for w, g in zip(want, got):
             for x, y in zip(w, g):
                 assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+def test_outputs_and_workspaces_that_are_given():
+    c, pre = sc.cache(2, 2, 100, 128, 8, True, 8, 1), sc.cache(1, 2, 90, 128, 8, True, 8, 5)
+    q = sc.normal((2, 8, 3, 128), 1)
+    for call, need in (
+            (lambda **kw: tq.tq_window_attention(q, c, 100, 8, True, 8, 30, **kw),
+             tq.tq_window_attention_workspace_size(2, 8, 2, 3, 128)),
+            (lambda **kw: tq.tq_prefix_attention(q, pre, 90, c, 100, 8, True, 8, **kw),
+             tq.tq_prefix_attention_workspace_size(1, 2, 8, 2, 3, 128))):
+        want, log = call()
+        out, lse = torch.full_like(q, 7.0), torch.full((2, 8, 3), 7.0, device="cuda")
+        got = call(out=out, lse=lse, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+        assert got[0] is out and got[1] is lse and torch.equal(out, want) and torch.equal(lse, log)
+        with pytest.raises(tq.TQError):
+            call(workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+        for bad in (dict(out=out.float()), dict(out=out[:1]), dict(lse=lse.double()), dict(lse=lse[..., :1]),
+                    dict(workspace=torch.empty(need, dtype=torch.uint8)), dict(lens=sc.ints([1, 2, 3])),
+                    dict(count=sc.ints([1, 2]).long()), dict(left_pad=sc.ints([1, 2], "cpu"))):
+            with pytest.raises(ValueError):
+                call(**bad)
+    assert (out == want).all()  # (what was refused wrote nothing)
