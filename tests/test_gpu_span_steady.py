@@ -87,3 +87,22 @@ def test_a_short_prefix_beside_the_sequences():
             n = [i + 1] * S
             assert lens.tolist() == n
             sc.check(out, lse, sc.reference(q, cache, cap, 8, True, 3, n, prefix=pre, P=P, dtype=torch.bfloat16), "step %d" % i)
+
+
+@pytest.mark.parametrize("N", [1, 20, 150])
+def test_offsets_past_32_bits(N):
+    """Keys and values of 4.5 GB each: the last tokens of the last head are appended and attended to beyond 2^32 bytes."""
+    Hkv, G, D, cap, n = 8, 2, 512, 1_100_000, 256
+    at = cap - n
+    big, small = tq.alloc_cache(1, Hkv, cap, D, 8, 8), tq.alloc_cache(1, Hkv, n, D, 8, 8)
+    k, v = sc.normal((1, Hkv, n, D), 1), sc.normal((1, Hkv, n, D), 2)
+    assert big["k_codes"].numel() > 2 ** 32
+    _, new = tq.tq_append_kv(k, v, big, sc.ints([at]), 8, True, 8)
+    tq.tq_append_kv(k, v, small, None, 8, True, 8)
+    assert new.tolist() == [cap]
+    for name in big:
+        assert torch.equal(big[name][:, :, at:], small[name]) and not big[name][:, :, :at].any()
+    q = sc.normal((1, Hkv * G, N, D), 3)
+    ref = sc.reference(q, small, n, 8, True, 8, window=100, dtype=torch.float32)
+    out, lse = tq.tq_window_attention(q, big, cap, 8, True, 8, 100, out_dtype=torch.float32)
+    sc.check(out, lse, ref, "window")
