@@ -511,7 +511,8 @@ TQ_API tq_status tq_append_kv(const tq_rows* q, const tq_rows* k, const tq_rows*
  * p = lens[b] - count[b] + n and attends to the tokens left_pad[b] <= t <= p with
  * t > p - window or t < left_pad[b] + sinks.
  *   q        [B, Hq, N, D] bf16, contiguous.
- *   window   at least 1; T or more: every token up to p. sinks: at least 0.
+ *   window   at least 1; T or more: every token up to p. sinks: at least 0; T or more: the
+ *            same.
  *   out      [B, Hq, N, D] of out_dtype; lse NULL or fp32 [B, Hq, N], as for
  *            tq_tree_attention. A query that its sequence does not have (n >=
  *            count[b], or p < left_pad[b]) gives zeros and -inf.

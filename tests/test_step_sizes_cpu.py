@@ -1,0 +1,38 @@
+"""Sizes near the ends of their types in the calls on new tokens. Every call below is
+refused by its sizes, so none reaches a kernel launch, and they run without a GPU."""
+import ctypes
+
+import pytest
+
+INVALID = 1
+MOST = 2 ** 31 - 2 ** 13  # the most tokens of a sequence
+EVERY = 2 ** 63 - 1
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from turboquant_kv_cache_tq_gb300 import build
+
+    build.build()
+    import turboquant_kv_cache_tq_gb300 as tq
+
+    tq.lib()
+    return tq
+
+
+def _window(tq, B, Hq, Hkv, N, D, T, window, sinks):
+    """A call over addresses that are never read, far enough apart for any cache."""
+    at = [(i + 1) << 50 for i in range(8)]
+    cache = tq.TQPackedCache(*at[:5], T)
+    return tq.lib().tq_window_attention(at[5], B, Hq, N, ctypes.byref(cache), Hkv, T, D, 8, 1, 8, None, None, None, window,
+                                        sinks, ctypes.c_float(1.0), at[6], 1, None, at[7], 1 << 49, None)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,N,D", [(64, 4, 2, 1, 128), (64, 2, 2, 1, 512), (32, 4, 2, 512, 128), (64, 2, 2, 300, 512)])
+@pytest.mark.parametrize("window,sinks", [(1, EVERY), (4096, EVERY), (MOST - 1, EVERY), (1, EVERY - 4), (1, MOST), (1, MOST + 5),
+                                          (MOST - 1, 0), (MOST, 0), (EVERY, 0), (EVERY, EVERY)])
+def test_tiles_of_a_call_are_counted_for_any_window_and_sinks(tq, B, Hq, Hkv, N, D, window, sinks):
+    """Few rows and many over sequences whose tiles pass 32 bits in all: refused, however
+    the window and the first tokens say that a row sees all of its sequence (a sum
+    that wraps would be a negative number of tiles, which no limit stops)."""
+    assert _window(tq, B, Hq, Hkv, N, D, MOST, window, sinks) == INVALID

@@ -369,8 +369,9 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
   const bool f32 = out_dtype == TQ_F32;
   const int64_t G = Hq / Hkv, share = prefix ? B / Bp : 1;
   // tokens of a sequence that any new one may see, by which tiles are counted (a
-  // block of rows sees a window and what its tokens add to it)
-  const int64_t reach = window < T ? window + sinks + N + 64 < T ? window + sinks + N + 64 : T : T;
+  // block of rows sees a window and what its tokens add to it). Both are cut to the
+  // sequence before they are added: a caller may say 2^63 - 1 for "all".
+  const int64_t leading = std::min(sinks, T), reach = window < T ? std::min(T, window + leading + N + 64) : T;
   SpanPlan plans[2];
   auto plan = [&](int64_t rows_of, int64_t rows, int64_t tokens, SpanPlan* t) {
     span_plan(rows_of, Hkv, rows, D, tokens, f32, span_few(rows, rows_of * Hkv * (tokens / kAttnTile + 1), D), t);
@@ -404,7 +405,7 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
     p.T = static_cast<int>(tokens);
     p.share = k ? static_cast<int>(share) : 0;
     p.window = static_cast<int>(window < kRaggedMostTokens ? window : kRaggedMostTokens);
-    p.sinks = static_cast<int>(sinks < T ? sinks : T);
+    p.sinks = static_cast<int>(leading);
     p.R = static_cast<int>(t.R);
     SpanSource& s = o.from[k];
     if (k) {  // sequence after sequence, as they lie in memory
