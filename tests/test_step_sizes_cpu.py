@@ -1,6 +1,8 @@
 """Sizes near the ends of their types in the calls on new tokens. Every call below is
 refused by its sizes, so none reaches a kernel launch, and they run without a GPU."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -36,3 +38,16 @@ def test_tiles_of_a_call_are_counted_for_any_window_and_sinks(tq, B, Hq, Hkv, N,
     the window and the first tokens say that a row sees all of its sequence (a sum
     that wraps would be a negative number of tiles, which no limit stops)."""
     assert _window(tq, B, Hq, Hkv, N, D, MOST, window, sinks) == INVALID
+
+
+def test_a_kernel_that_starts_without_a_wait_acquires():
+    """Of two kernels of a call that run side by side, the second may read what the kernel
+    before the call wrote only after it has acquired what the first released, and waits
+    where it has not: the start of a dependent kernel orders no memory."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "turboquant_kv_cache_tq_gb300", "csrc")
+    text = open(os.path.join(csrc, "tq_span_attention.cuh")).read()
+    begin = re.search(r"void begin\(\) const \{(.*?)\n  \}\n", text, re.S).group(1)
+    begin = re.sub(r"\s*//[^\n]*", "", begin)
+    second, first = begin.split("return;")
+    assert re.search(r"if \(order == 2\) \{.*ld\.acquire\.gpu.*if \(seen != call\) pdl_wait\(\);", second, re.S)
+    assert re.search(r"pdl_wait\(\);.*st\.release\.gpu.*__syncthreads\(\);.*pdl_launch_dependents\(\);", first, re.S)

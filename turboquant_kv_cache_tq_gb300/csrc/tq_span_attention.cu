@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
   __shared__ float s_part[4][E + 2][32];
   pdl_launch_dependents();
   pdl_wait();
+  if (p.started != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.started = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Where the rows' records are. Lanes 2 i and 2 i + 1 (head_dim 512: and 16 on, for
   // the other half of the values) find row i's of the first and the second pass, in one
@@ -188,8 +189,9 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
 }
 
 // How the query rows of a pass are laid out, and the scratch that follows.
+// (started: where in it the call's number goes, see SpanPass::begin)
 struct SpanPlan {
-  long long R, RB, rows, copies, slots, HH, lines, n_recs, rec_floats, cut_bytes, bytes;
+  long long R, RB, rows, copies, slots, HH, lines, n_recs, rec_floats, started, cut_bytes, bytes;
   int TT, halves;
   bool few;
 };
@@ -247,7 +249,8 @@ bool span_plan(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t T, bool 
   }
   t->n_recs = (t->few ? kAttnGridPerSm : 1) * sm_count() + t->lines * t->HH;
   t->rec_floats = t->slots * (D / t->halves + 2);
-  t->cut_bytes = ((kCutRows + 2 * (t->lines + 1)) * 4 + 255) / 256 * 256;
+  t->started = ((kCutRows + 2 * (t->lines + 1)) * 4 + 7) / 8 * 8;
+  t->cut_bytes = (t->started + 8 + 255) / 256 * 256;
   t->bytes = t->cut_bytes + t->n_recs * t->rec_floats * 4;
   return true;
 }
@@ -468,10 +471,18 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
     s.slots = p.slots;
     s.copies = p.copies;
   }
-  // two passes run side by side, unless one reads narrow pieces (through L1)
+  // two passes run side by side, unless a tile of one may end past its capacity
   if (prefix && passes[0].bulk && passes[1].bulk) {
+    static std::atomic<unsigned long long> calls{0};
     passes[1].order = 1;
     passes[0].order = 2;
+    o.started = reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(passes[1].cut) + plans[1].started);
+    // (numbers of 64 bits that never come again, spread so that no other words look like them)
+    const unsigned long long call = (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9e3779b97f4a7c15ull;
+    for (SpanPass& p : passes) {
+      p.started = o.started;
+      p.call = call;
+    }
   }
   o.lens = lens;
   o.left_pad = left_pad;

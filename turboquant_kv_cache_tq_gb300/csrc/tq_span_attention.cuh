@@ -51,17 +51,37 @@ struct SpanPass {
   float scale_log2;   // scale * log2(e); rows by the 128: its magnitude
   int negate;         // rows by the 128: scale < 0
   int order;          // 1, 2: the first, second of two passes that run side by side (0: alone)
+  unsigned long long* started;  // where the first of them leaves the call's number
+  unsigned long long call;
 
   __device__ __forceinline__ bool alone() const { return bulk; }
   // A kernel's place in the stream. Of two passes that run side by side the first
-  // lets the second start only when all that came before this call is done, and the
-  // second starts without a wait: its inputs are written (they are read from L2, as
-  // nothing says that this SM's L1 knows of them) and its scratch is free. It waits for the
-  // first before it ends, so whatever waits for it has waited for both.
+  // waits for all that came before this call, leaves the call's number in the
+  // workspace (a release: whoever reads it there sees what the first pass may see) and
+  // only then lets the second start. The second reads the number (an acquire, by every
+  // thread) in place of a wait; one that finds another number waits for the first pass
+  // as any kernel does. So its inputs are written and its scratch is free either way,
+  // which neither the start of a dependent kernel nor a read from L2 promises. It waits
+  // for the first pass before it ends, so whatever waits for it has waited for both. The
+  // combine kernel takes the number away again, for a captured call's next run.
   __device__ __forceinline__ void begin() const {
     if (order != 1) pdl_launch_dependents();
-    if (order != 2) pdl_wait();
-    if (order == 1) pdl_launch_dependents();
+    if (order == 2) {
+      unsigned long long seen;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(started) : "memory");
+      if (seen != call) pdl_wait();
+      // (bulk copies read in order with the acquire)
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      return;
+    }
+    pdl_wait();
+    if (order == 1) {
+      if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(started), "l"(call) : "memory");
+        __syncthreads();
+      }
+      pdl_launch_dependents();
+    }
   }
   __device__ __forceinline__ void end() const {
     if (order == 2) pdl_wait();
@@ -92,7 +112,7 @@ struct SpanTiles {
   __device__ __forceinline__ static int tiles(int from, int to) { return to > from ? (to - from + TT - 1) / TT : 0; }
   __device__ __forceinline__ SpanTiles() {}
   __device__ __forceinline__ SpanTiles(const SpanPass& p, int b, int r0, int r1) {
-    // (read from L2: see begin)
+    // (past L1, and never by the read-only path: the kernel may have started before they were written)
     hi = p.lens != nullptr ? min(max(__ldcg(p.lens + b), 0), p.T) : p.T;
     lo = p.share == 0 && p.left_pad != nullptr ? min(max(__ldcg(p.left_pad + b), 0), hi) : 0;
     s2 = n2 = 0;
@@ -172,6 +192,7 @@ struct SpanOutput {
   void* out;
   float* lse;
   unsigned* err;
+  unsigned long long* started;  // the passes ran side by side: the number to take away
   int B, Hq, Hkv, G, N, T;
   int sources, out_f32;
   float rot_scale;
