@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(128, D <= 256 ? 7 : 1) span_combine_kernel(con
     for (int s0 = warp % W; s0 < most; s0 += LANES * W) {
       const int part = s0 + (lane % LANES) * W, k = part >= parts0 ? 1 : 0, y = part - (k ? parts0 : 0);
       const SpanSource& f = p.from[k];
+      (void)TQ_CHECK(f.copies > 0 && f.halves > 0, p.err);
       const int shift = f.copies - 1, from = group + 2 * nr + k;
       const int at = __shfl_sync(kFull, rl, from) + (y & shift) * f.rows;
       const float* rec = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(recs), from)) +
@@ -471,6 +472,8 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
     s.slots = p.slots;
     s.copies = p.copies;
   }
+  // (lanes past a row's last part look at a second pass too, for parts that they do not load)
+  if (!prefix) o.from[1] = o.from[0];
   // two passes run side by side, unless a tile of one may end past its capacity
   if (prefix && passes[0].bulk && passes[1].bulk) {
     static std::atomic<unsigned long long> calls{0};
