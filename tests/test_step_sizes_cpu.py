@@ -5,6 +5,7 @@ import os
 import re
 
 import pytest
+import torch
 
 INVALID = 1
 MOST = 2 ** 31 - 2 ** 13  # the most tokens of a sequence
@@ -51,3 +52,37 @@ def test_a_kernel_that_starts_without_a_wait_acquires():
     second, first = begin.split("return;")
     assert re.search(r"if \(order == 2\) \{.*ld\.acquire\.gpu.*if \(seen != call\) pdl_wait\(\);", second, re.S)
     assert re.search(r"pdl_wait\(\);.*st\.release\.gpu.*__syncthreads\(\);.*pdl_launch_dependents\(\);", first, re.S)
+
+
+class _Like:
+    """What the binding asks of a tensor before it takes the tensor's address."""
+
+    def __init__(self, t, device):
+        self.t, self.dtype, self.shape, self.device = t, t.dtype, t.shape, device
+
+    def get_device(self):
+        return self.device.index
+
+    def stride(self):
+        return self.t.stride()
+
+    def numel(self):
+        return self.t.numel()
+
+    def data_ptr(self):
+        return 1 << 40
+
+
+def test_the_binding_takes_contiguous_rows_only(tq):
+    dev = torch.device("cuda", 0)
+    k = torch.zeros((2, 2, 64, 64))
+    for t in (k, k[:, :1], k[:, :, 3:5], k[:1].expand(4, 2, 64, 64), k.transpose(1, 2)):
+        r = tq._rows(_Like(t, dev), t.shape, torch.float32, "k", dev)
+        assert (r.data, r.stride_b, r.stride_h, r.stride_t) == (1 << 40, *t.stride()[:3])
+    for t in (k.transpose(2, 3), k[..., ::2], k.permute(3, 1, 2, 0)):
+        with pytest.raises(ValueError, match="contiguous rows"):
+            tq._rows(_Like(t, dev), t.shape, torch.float32, "k", dev)
+    for x, shape, dtype in ((_Like(k, torch.device("cuda", 1)), k.shape, torch.float32), (_Like(k, dev), (2, 2, 64, 32), torch.float32),
+                            (_Like(k, dev), k.shape, torch.bfloat16)):
+        with pytest.raises(ValueError, match="contiguous rows"):
+            tq._rows(x, shape, dtype, "k", dev)
