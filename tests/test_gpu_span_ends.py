@@ -20,7 +20,7 @@ def _gpu():
     assert tq.lib().tq_device_status(None) == 0
 
 
-@pytest.mark.parametrize("sinks", [sys.maxsize, sys.maxsize - 300, 2 ** 31, 300, 299])
+@pytest.mark.parametrize("sinks", [2 ** 64, sys.maxsize, sys.maxsize - 300, 2 ** 31, 300, 299])
 @pytest.mark.parametrize("G,N", [(1, 1), (4, 3), (4, 20), (3, 70)])
 @pytest.mark.parametrize("D", [128, 512])
 def test_first_tokens_of_any_number(sinks, G, N, D):

@@ -86,3 +86,34 @@ def test_the_binding_takes_contiguous_rows_only(tq):
                             (_Like(k, dev), k.shape, torch.bfloat16)):
         with pytest.raises(ValueError, match="contiguous rows"):
             tq._rows(x, shape, dtype, "k", dev)
+
+
+def test_numbers_of_tokens_past_64_bits(tq, monkeypatch):
+    """ctypes drops the bits above 64: what the binding passes on has to fit."""
+    passed, cache = {}, tq.alloc_cache(1, 2, 16, 64, 8, 3, device="cpu")
+
+    class Library:
+        def tq_window_attention_workspace_size(self, *a):
+            return 16
+
+        tq_prefix_attention_workspace_size = tq_window_attention_workspace_size
+
+        def tq_window_attention(self, *a):
+            passed.update(T=a[6], window=a[14], sinks=a[15])
+
+        def tq_prefix_attention(self, *a):
+            passed.update(P=a[6], T=a[10])
+
+    monkeypatch.setattr(tq, "lib", Library)
+    monkeypatch.setattr(tq, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(tq, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(tq, "_packed", lambda *a: tq.TQPackedCache())
+    q = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16)
+    for x, want in ((5, 5), (0, 0), (-1, -1), (EVERY, EVERY), (EVERY + 1, EVERY), (2 ** 64, EVERY), (2 ** 64 + 5, EVERY),
+                    (2 ** 100, EVERY), (-5, -1), (-2 ** 64, -1), (-2 ** 64 + 5, -1)):
+        tq.tq_window_attention(q, cache, x, 8, True, 3, x, x)
+        assert passed == dict(T=want, window=want, sinks=want), x
+        passed.clear()
+        tq.tq_prefix_attention(q, cache, x, cache, x, 8, True, 3)
+        assert passed == dict(P=want, T=want), x
+        passed.clear()

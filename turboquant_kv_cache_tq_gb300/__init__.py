@@ -770,6 +770,12 @@ def tq_append_kv(k: torch.Tensor, v: torch.Tensor, cache: dict, lens, k_bits: in
     return q_out, new_lens
 
 
+def _count(x) -> int:
+    """A number of tokens for the library, which takes 64 bits (ctypes would drop
+    the bits above them): larger ones as the largest, negative ones as -1."""
+    return min(max(int(x), -1), 0x7fffffffffffffff)
+
+
 def tq_window_attention_workspace_size(B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
     """Bytes of scratch tq_window_attention needs (on the current device)."""
     r = lib().tq_window_attention_workspace_size(B, Hq, Hkv, N, D)
@@ -835,9 +841,9 @@ def tq_window_attention(q: torch.Tensor, cache: dict, T: int, k_bits: int, k_sig
         q, out_dtype, out, lse, workspace, tq_window_attention_workspace_size, (B, Hq, Hkv, N, D), dev)
     one = (B,)
     st = lib().tq_window_attention(
-        q.data_ptr(), B, Hq, N, ctypes.byref(cv), Hkv, int(T), D, int(k_bits), 1 if k_signed else 0, int(v_bits),
+        q.data_ptr(), B, Hq, N, ctypes.byref(cv), Hkv, _count(T), D, int(k_bits), 1 if k_signed else 0, int(v_bits),
         _int_ptr(lens, one, "lens", dev), _int_ptr(left_pad, one, "left_pad", dev), _int_ptr(count, one, "count", dev),
-        int(window), int(sinks), D ** -0.5 if scale is None else float(scale), out_ptr, _DTYPE[out_dtype], lse_ptr,
+        _count(window), _count(sinks), D ** -0.5 if scale is None else float(scale), out_ptr, _DTYPE[out_dtype], lse_ptr,
         ws_ptr, ws_bytes, _current_stream(dev))
     if st:
         _check(st, "tq_window_attention")
@@ -872,8 +878,8 @@ def tq_prefix_attention(q: torch.Tensor, prefix: dict, P: int, cache: dict, T: i
         q, out_dtype, out, lse, workspace, tq_prefix_attention_workspace_size, (Bp, B, Hq, Hkv, N, D), dev)
     one = (B,)
     st = lib().tq_prefix_attention(
-        q.data_ptr(), B, Hq, N, ctypes.byref(pv), Bp, int(P), _int_ptr(prefix_lens, (Bp,), "prefix_lens", dev),
-        ctypes.byref(cv), Hkv, int(T), D, int(k_bits), 1 if k_signed else 0, int(v_bits), _int_ptr(lens, one, "lens", dev),
+        q.data_ptr(), B, Hq, N, ctypes.byref(pv), Bp, _count(P), _int_ptr(prefix_lens, (Bp,), "prefix_lens", dev),
+        ctypes.byref(cv), Hkv, _count(T), D, int(k_bits), 1 if k_signed else 0, int(v_bits), _int_ptr(lens, one, "lens", dev),
         _int_ptr(left_pad, one, "left_pad", dev), _int_ptr(count, one, "count", dev),
         D ** -0.5 if scale is None else float(scale), out_ptr, _DTYPE[out_dtype], lse_ptr, ws_ptr, ws_bytes,
         _current_stream(dev))
