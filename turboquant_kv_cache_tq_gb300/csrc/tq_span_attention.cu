@@ -209,7 +209,7 @@ struct SpanPlan {
 // scratch is sized by).
 //   Blocks of 8 rows in place of 16 decode a tile twice as often, but the code for 16 at
 // head_dim 512 is 40 KB of instructions, which a pass of a few tiles pays to fetch: 12
-// rows, 8 heads x 2048 tokens 24.0 / 30.4 us, 8 sequences of 8192 186 / 161 (head_dim 256
+// rows, 8 heads x 2048 tokens 24.0 / 30.4 us, 8 sequences of up to 8192 186 / 161 (head_dim 256
 // 16.6 / 16.1 and 100 / 85, narrower ones alike).
 constexpr int kFewRows = kAttnRows, kFewMost = 128;
 int span_few(int64_t rows, int64_t tiles, int64_t D) {
@@ -275,11 +275,17 @@ cudaError_t launch_span(SpanPass* passes, const SpanPlan* plans, int64_t reach, 
   };
   // A prefix by the 128 rows takes whole SMs. Where it can leave some at the cost of
   // about 1 us, and those hold every block of the second pass, the two run at the same
-  // time (8 beams after 4096 tokens: 25.4 -> 20.0 us).
+  // time (8 beams after 4096 tokens: 25.4 -> 19.7 us).
+  //   A tile's time with one segment an SM (bf16 outputs, 3- and 8-bit values, from the
+  // difference between 2048 and 6144 tokens): head_dim 64, up to 64 rows 0.61 and 0.65 us,
+  // 128 rows 0.83 and 0.86; 128: 0.80 and 0.82, 0.91 and 0.95; 256 (tiles of 32 tokens): 0.93
+  // and 0.96 for either; 512 (of 32, for half of the values): 2.26. fp32 outputs at head_dim 128
+  // have tiles of 32 tokens that take 0.7 of that, so they leave fewer SMs than they could.
   if (passes[0].order == 2 && plans[0].few && !plans[1].few) {
     const cudaError_t e = few(0, true);
     if (e != cudaSuccess) return e;
-    const double tile = D == 512 ? 1.5 : D == 256 ? 1.0 : plans[1].rows <= 64 ? 0.55 : 0.9;  // us
+    const bool half = plans[1].rows <= 64;
+    const double tile = D == 512 ? 2.3 : D == 256 ? 0.95 : D == 128 ? (half ? 0.8 : 0.95) : half ? 0.65 : 0.85;  // us
     const double work = tile * plans[1].lines * plans[1].HH * (P / plans[1].TT + 1), sms = sm_count();
     const int blocks = static_cast<int>(std::ceil(work / (work / sms + 1.0)));
     if (blocks < passes[1].grid && (sms - blocks) * passes[0].per_sm >= passes[0].grid) passes[1].grid = blocks;
@@ -447,6 +453,8 @@ tq_status span_attention(const void* q, int64_t B, int64_t Hq, int64_t N, const 
     p.vtab_stride = 128;
     const tq_packed_cache* c = k ? prefix : cache;
     if (t.few) {
+      // whole tiles; any other capacity takes copies that look at each row's end and
+      // alignment, for every tile (at head_dim 256 and 512 they too are of 16 bytes)
       p.bulk = c->t_cap % kAttnTile == 0;
       p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     } else {

@@ -13,8 +13,9 @@
 // own sequence, or the prefix of all the sequences that share it (a row of the
 // cache then has the query rows of them all). Two kernels do a pass: rows by the
 // 128 on the fifth-generation tensor core (the tree attention's kernel with
-// another walk over tokens), and at most 16 rows, for which the decode in
-// registers is faster (span_few_kernel). A pass leaves partial records (maximum, weight
+// another walk over tokens), and blocks of at most 16 rows, for which the decode in
+// registers is faster (span_few_kernel: 16 rows a kv head or fewer, and up to 128 over
+// short caches; the rule is span_few). A pass leaves partial records (maximum, weight
 // sum, weighted values), and one combine kernel merges those of an output row's one or
 // two passes.
 #pragma once
@@ -203,9 +204,9 @@ struct SpanOutput {
 // 36 us, 32 x 8 x 4160 tokens 74 / 74 / 74).
 constexpr int kFewTurn = 8;
 
-// Launches, translation units of their own. launch_span_few: at most 8 NT rows a kv
-// head (NT: 1 or 2) and `tiles` tiles of 16 tokens in all; sets p.grid and p.per_sm (plan:
-// and nothing else).
+// Launches, translation units of their own. launch_span_few: blocks of at most 8 NT
+// rows (NT: 1 or 2; a kv head may have several, up to 128 rows in all, see span_few) and
+// `tiles` tiles of 16 tokens in all; sets p.grid and p.per_sm (plan: and nothing else).
 template <int D, int NT>
 cudaError_t launch_span_few(SpanPass& p, long long tiles, bool plan, cudaStream_t s);
 template <int D, bool F32>

@@ -1,5 +1,6 @@
 // A pass with few query rows a kv head: at most 16, a token or two of each sequence, or
-// some blocks of 16 over a cache too short for the tensor core's longer start.
+// some blocks of 8 or 16 (up to 128 rows) over a cache too short for the tensor core's
+// longer start (the rule: span_few).
 //
 // The decode of the packed bytes is the work: a tile of 16 tokens goes from the
 // bytes into the operands of mma.sync (m16n8k16: tokens x query rows) within the
@@ -15,10 +16,12 @@
 // read in narrower pieces.
 //
 // What bounds it (32 sequences x 8 heads x 4160 visible tokens, head_dim 128, k8 / v8, one
-// token, four rows a head; 299 MB, 45 us at the measured copy rate): 74 us in a graph,
-// of which about 57 are 815 instructions a tile at 0.8 of the issue slots of 16 warps
-// an SM, the rest a start (cut 1.5 us, first tile 2.5), the records (1.5 each) and the
-// combine kernel (4). The half-rate ALU pipe is at 46%, the tensor pipe at 20%. How it
+// token, four rows a head; 299 MB, 45 us at the measured copy rate): 74 us in a graph (fp32
+// outputs 76), of which about 57 are 815 instructions a tile, the rest a start (cut 1.5
+// us, first tile 2.5), the records (1.5 each) and the combine kernel (4). In those 57 the 16 warps of an
+// SM use 0.8 of its issue slots (66560 tiles, 54 M instructions); counters over the whole
+// of a kernel of 3400 tokens, its start and end included, say 62%. There the
+// half-rate ALU pipe is at 46%, the tensor pipe at 20%. How it
 // came there: a block a row and a warp a token 1631 us; this kernel 79; a shorter cut,
 // table, start and merge 74. (Codes read in 16-byte words: no change; copies by one
 // address and its offsets: 77.)

@@ -1,4 +1,4 @@
-// Window and prefix attention of at most 16 query rows a kv head, head_dim 128 (one
+// Window and prefix attention by blocks of at most 16 query rows, head_dim 128 (one
 // translation unit per head_dim and tile of rows, so the library builds in parallel).
 #include "tq_span_few.cuh"
 

@@ -922,7 +922,8 @@ __device__ void tree_softmax(const P& p, uint32_t sm, uint8_t* smem, uint8_t* ct
 // The partial results: one block an SM, which holds all of its tensor memory.
 //
 // What bounds it (32 sequences x 8 heads of 4096 to 8192 tokens, head_dim 128, 16
-// nodes, k8 / v8): 162 us in a graph, where the packed bytes take 67 and the
+// nodes, k8 / v8): 161 us in a graph (before and after the window and prefix attention
+// came to share the kernel), where the packed bytes take 67 and the
 // products 27. Neither is it: 3-bit values, 28% fewer bytes, take 157 us, 4-bit ones
 // 160. A counter run of 8 such sequences: 0.56 instructions a cycle and scheduler,
 // tensor pipe 35%, DRAM 28% busy; of the 12.5 cycles that a warp takes an
