@@ -492,7 +492,8 @@ typedef struct {
  *   lens     int32 device array [B], negative values count as 0; NULL: 0
  *            everywhere. left_pad: used for positions only, within [0, lens].
  *   q_out    [B, Hq, N, D] of dtype, contiguous.
- *   new_lens int32 [B]: receives min(lens[b] + count[b], cache->t_cap).
+ *   new_lens int32 [B]: receives min(lens[b] + count[b], cache->t_cap). Not lens itself: it is
+ *            written while lens is read.
  * The rotation rounds every product and sum to fp32; the turned keys are encoded
  * as tq_encode_kv encodes fp32 keys (they are not rounded to dtype on the way), the
  * values as it encodes dtype values. Nothing else of the cache is touched.

@@ -720,7 +720,8 @@ def tq_append_kv(k: torch.Tensor, v: torch.Tensor, cache: dict, lens, k_bits: in
     the elements of a row that turn, in neighbouring pairs when interleaved, else
     j with j + R / 2; None: nothing turns. positions: int32 [B,N] or None (lens -
     left_pad + n). q [B,Hq,N,D]: queries turned alike into q_out. Tokens past the
-    capacity are dropped. Returns (q_out or None, the new lengths)."""
+    capacity are dropped. Returns (q_out or None, the new lengths); new_lens may
+    not be lens itself, which is read while it is written."""
     dev = k.device
     kind = _DTYPE.get(k.dtype)
     if k.dim() != 4 or kind is None:
